@@ -18,6 +18,7 @@
 
 #include "mlaqp.h"
 #include "mlaqp_dispatch.h"
+#include "mlaqp_host.h"
 #include "mlaqp_kernel.cuh"
 #include "mlaqp_kernel_large.cuh"
 #include "mlaqp_kernel_warp.cuh"
@@ -979,6 +980,23 @@ int v_up_impl(const VUpArgs& a, mlaqp_stream_t stream, int pdl, unsigned long lo
 
 }  // namespace
 
+namespace mlaqp {
+
+int host_fail(int status, const std::string& msg) { return fail(status, msg); }
+
+int host_fail_cuda(const char* what, cudaError_t e) { return fail_cuda(what, e); }
+
+int host_device(int device, int* resolved, int* sm_count) {
+  int st = resolve_device(device, resolved);
+  if (st != MLAQP_OK) return st;
+  st = check_device(*resolved);
+  if (st != MLAQP_OK) return st;
+  *sm_count = g_dev[*resolved].sm_count;
+  return MLAQP_OK;
+}
+
+}  // namespace mlaqp
+
 extern "C" {
 
 int mlaqp_can_implement(int num_heads, int max_m, int nope_dim, int latent_dim, int rope_dim, int weight_format,
@@ -1220,15 +1238,18 @@ int mlaqp_prefetch_weights(const void* weight, const void* weight_scale, int H, 
 
 int mlaqp_device_status(unsigned int* status, int reset) {
   if (!status) return fail(MLAQP_ERR_INVALID_ARG, "status must not be NULL");
-  unsigned int a = 0, b = 0, c = 0, v = 0, wa = 0, wb = 0;
+  unsigned int a = 0, b = 0, c = 0, v = 0, wa = 0, wb = 0, ka = 0, kr = 0, kp = 0;
   cudaError_t e = mlaqp::device_status_bf16_weights(&a, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_mxfp8_weights(&b, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_large_m(&c, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_v_up(&v, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_warp_bf16(&wa, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_warp_mxfp8(&wb, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_attend(&ka, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_rows(&kr, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_pages(&kp, reset != 0);
   if (e != cudaSuccess) return fail_cuda("reading the device status word", e);
-  *status = a | b | c | v | wa | wb;
+  *status = a | b | c | v | wa | wb | ka | kr | kp;
   return MLAQP_OK;
 }
 

@@ -75,5 +75,8 @@ cudaError_t device_status_large_m(unsigned int* value, bool reset);
 cudaError_t device_status_v_up(unsigned int* value, bool reset);
 cudaError_t device_status_warp_bf16(unsigned int* value, bool reset);
 cudaError_t device_status_warp_mxfp8(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_attend(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_rows(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_pages(unsigned int* value, bool reset);
 
 }  // namespace mlaqp

@@ -1,4 +1,4 @@
-"""ctypes binding of ``libmlaqp.so`` (declared in ``include/mlaqp.h``).
+"""ctypes binding of ``libmlaqp.so`` (declared in ``include/mlaqp.h`` and ``include/mlaqp_kv4.h``).
 
 Argument marshalling only: every function here forwards to the C entry point
 of the same name and returns its status code unchanged; all of the operation
@@ -31,6 +31,8 @@ MLAQP_ERR_INVALID_ARG = 2
 MLAQP_ERR_CUDA = 3
 
 MLAQP_DEVSTATUS_WAIT_TIMEOUT = 1
+MLAQP_DEVSTATUS_BAD_INDEX = 2
+MLAQP_DEVSTATUS_OUT_OF_PAGES = 4
 
 NOPE_DIM = 128
 LATENT_DIM = 512
@@ -48,6 +50,11 @@ _lib = None
 
 _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
+_c_int64 = ctypes.c_int64
+# block_table, its stride, num_seqs, seq_lens, ref_count, num_pages, page_size
+_KV4_TABLES = [_c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int, _c_int]
+# cache, page_stride, layer_stride, layers
+_KV4_POOL = [_c_void_p, _c_int64, _c_int64, _c_int]
 _SIGNATURES = {
     "mlaqp_can_implement": (_c_int, [_c_int] * 8),
     "mlaqp_prewarm": (_c_int, [_c_int] * 5),
@@ -79,6 +86,23 @@ _SIGNATURES = {
     "mlaqp_debug_v_up_bounded_wait": (_c_int, [_c_void_p, ctypes.c_int64, ctypes.c_int64, _c_void_p, _c_void_p,
                                                _c_void_p, ctypes.c_int64, _c_int, _c_int, _c_int,
                                                ctypes.c_ulonglong, ctypes.c_uint, _c_void_p]),
+    "mlaqp_kv4_page_bytes": (_c_int64, [_c_int]),
+    "mlaqp_kv4_append": (_c_int, [_c_void_p, _c_int64, _c_void_p, _c_int64, _c_void_p, _c_int64, _c_int, _c_int,
+                                  _c_void_p, _c_int, _c_void_p]),
+    "mlaqp_kv4_gather": (_c_int, [_c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int, _c_void_p, _c_int64,
+                                  _c_void_p]),
+    "mlaqp_kv4_attend": (_c_int, [_c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int64, _c_int, _c_int,
+                                  _c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
+                                  ctypes.c_float, _c_void_p, _c_int64, _c_void_p, _c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_attend_workspace": (_c_int64, [_c_int] * 4),
+    "mlaqp_kv4_extend": (_c_int, _KV4_TABLES + [_c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p]),
+    "mlaqp_kv4_fork": (_c_int, _KV4_TABLES + [_c_void_p, _c_void_p, _c_int] + _KV4_POOL
+                       + [_c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_release": (_c_int, _KV4_TABLES + [_c_void_p, _c_int, _c_void_p]),
+    "mlaqp_kv4_compact": (_c_int, _KV4_TABLES + _KV4_POOL + [_c_void_p, _c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_copy_pages": (_c_int, _KV4_POOL + [_c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p]),
+    "mlaqp_kv4_pages_workspace": (_c_int64, [_c_int, _c_int]),
+    "mlaqp_kv4_prewarm": (_c_int, [_c_int]),
     "mlaqp_last_error": (ctypes.c_char_p, []),
     "mlaqp_version": (_c_int, []),
 }
@@ -277,6 +301,87 @@ def mlaqp_debug_v_plan(M, H, weight_format="bf16", pdl=1, sm_count=152):
     plan = {k: o.value for k, o in zip(keys, out)}
     plan["form"] = V_FORMS.get(plan["form"], plan["form"])
     return st, plan
+
+
+def mlaqp_kv4_page_bytes(page_size) -> int:
+    return load_library().mlaqp_kv4_page_bytes(int(page_size))
+
+
+def mlaqp_kv4_append(latent, latent_token_stride, k_pe, k_pe_token_stride, cache, page_stride, num_pages, page_size,
+                     slots, T, stream=None) -> int:
+    return load_library().mlaqp_kv4_append(
+        _ptr(latent), int(latent_token_stride), _ptr(k_pe), int(k_pe_token_stride), _ptr(cache), int(page_stride),
+        int(num_pages), int(page_size), _ptr(slots), int(T), _stream(stream))
+
+
+def mlaqp_kv4_gather(cache, page_stride, num_pages, page_size, slots, T, out, out_token_stride, stream=None) -> int:
+    return load_library().mlaqp_kv4_gather(_ptr(cache), int(page_stride), int(num_pages), int(page_size), _ptr(slots),
+                                           int(T), _ptr(out), int(out_token_stride), _stream(stream))
+
+
+def mlaqp_kv4_attend(q, q_token_stride, q_dtype, q_scale, cache, page_stride, num_pages, page_size, block_table,
+                     block_table_stride, num_seqs, seq_lens, seqs, B, q_len, H, softmax_scale, x, x_token_stride, lse,
+                     workspace, workspace_bytes, stream=None) -> int:
+    return load_library().mlaqp_kv4_attend(
+        _ptr(q), int(q_token_stride), _fmt(q_dtype, OUT_DTYPES), _ptr(q_scale), _ptr(cache), int(page_stride),
+        int(num_pages), int(page_size), _ptr(block_table), int(block_table_stride), int(num_seqs), _ptr(seq_lens),
+        _ptr(seqs), int(B), int(q_len), int(H), float(softmax_scale), _ptr(x), int(x_token_stride), _ptr(lse),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def mlaqp_kv4_attend_workspace(B, q_len, H, device=-1) -> int:
+    """Bytes of workspace, or -1 (see ``mlaqp_last_error``)."""
+    return load_library().mlaqp_kv4_attend_workspace(int(B), int(q_len), int(H), int(device))
+
+
+def _kv4_tables(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size):
+    return (_ptr(block_table), int(block_table_stride), int(num_seqs), _ptr(seq_lens), _ptr(ref_count), int(num_pages),
+            int(page_size))
+
+
+def mlaqp_kv4_extend(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size, seqs,
+                     new_tokens, n, slots, max_new, stream=None) -> int:
+    t = _kv4_tables(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size)
+    return load_library().mlaqp_kv4_extend(*t, _ptr(seqs), _ptr(new_tokens), int(n), _ptr(slots), int(max_new),
+                                           _stream(stream))
+
+
+def mlaqp_kv4_fork(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size, parents,
+                   children, n, cache, page_stride, layer_stride, layers, workspace, workspace_bytes,
+                   stream=None) -> int:
+    t = _kv4_tables(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size)
+    return load_library().mlaqp_kv4_fork(*t, _ptr(parents), _ptr(children), int(n), _ptr(cache), int(page_stride),
+                                         int(layer_stride), int(layers), _ptr(workspace), int(workspace_bytes),
+                                         _stream(stream))
+
+
+def mlaqp_kv4_release(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size, seqs, n,
+                      stream=None) -> int:
+    t = _kv4_tables(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size)
+    return load_library().mlaqp_kv4_release(*t, _ptr(seqs), int(n), _stream(stream))
+
+
+def mlaqp_kv4_compact(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size, cache,
+                      page_stride, layer_stride, layers, n_live, workspace, workspace_bytes, stream=None) -> int:
+    t = _kv4_tables(block_table, block_table_stride, num_seqs, seq_lens, ref_count, num_pages, page_size)
+    return load_library().mlaqp_kv4_compact(*t, _ptr(cache), int(page_stride), int(layer_stride), int(layers),
+                                            _ptr(n_live), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def mlaqp_kv4_copy_pages(cache, page_stride, layer_stride, layers, num_pages, page_size, src, dst, n,
+                         stream=None) -> int:
+    return load_library().mlaqp_kv4_copy_pages(_ptr(cache), int(page_stride), int(layer_stride), int(layers),
+                                               int(num_pages), int(page_size), _ptr(src), _ptr(dst), int(n),
+                                               _stream(stream))
+
+
+def mlaqp_kv4_pages_workspace(num_pages, n) -> int:
+    """Bytes of workspace, or -1 (see ``mlaqp_last_error``)."""
+    return load_library().mlaqp_kv4_pages_workspace(int(num_pages), int(n))
+
+
+def mlaqp_kv4_prewarm(device=-1) -> int:
+    return load_library().mlaqp_kv4_prewarm(int(device))
 
 
 def mlaqp_device_status(reset=False):
