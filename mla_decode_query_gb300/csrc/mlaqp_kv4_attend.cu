@@ -1,177 +1,864 @@
-// MLA decode attention over the paged 4-bit latent cache: the plain kernel.
-// One CTA takes one query token with all its heads and walks the sequence in
-// tiles of 32 tokens, decoded to FP32 in shared memory, with the running
-// maximum and sum of the softmax.
+// The attention kernel of the 4-bit latent cache, its join kernel and their
+// launch.  The mathematics and the layout are in mlaqp_kv4_attend.cuh.
+
+#include <cuda_fp16.h>
 
 #include "mlaqp_dispatch.h"
-#include "mlaqp_kv4.cuh"
-#include "mlaqp_kv4_launch.h"
+#include "mlaqp_kv4_attend.cuh"
 
 namespace mlaqp {
 
 namespace {
 
-constexpr int kAttendThreads = 256;
-constexpr int kAttendTile = 32;
-constexpr int kKeyStride = kOutDim + 1;
+constexpr unsigned long long kAttWaitNs = 1000000000ull;
 
-struct AttendSmem {
-  float q[16][kOutDim];
-  float k[kAttendTile][kKeyStride];
-  float p[16][kAttendTile];
-  float alpha[16], top[16], sum[16];
-  uint8_t valid[kAttendTile];
-};
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  const uint32_t two = e4m3x2_to_bf16x2_scaled(c);
-  if ((c & 0x7F) == 0x7F) return __uint_as_float(0x7FC00000u);
-  return bf16_lo(two) * 0x1p120f;
+// Bounded wait of one thread; gives up early once another one has.
+__device__ __forceinline__ bool att_wait_one(uint32_t bar, uint32_t parity, AttSchedule& s) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&s.fail)) return false;
+    if (globaltimer_ns() - t0 > kAttWaitNs) {
+      *reinterpret_cast<volatile int*>(&s.fail) = 1;
+      atomicOr(&g_device_status, kDevStatusWaitTimeout);
+      return false;
+    }
+  }
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kAttendThreads) mlaqp_kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
-  extern __shared__ uint8_t raw[];
-  AttendSmem& s = *reinterpret_cast<AttendSmem*>(raw);
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool att_wait(uint32_t bar, uint32_t parity, AttSchedule& s) {
+  return __all_sync(0xffffffffu, att_wait_one(bar, parity, s));
+}
+
+// The row groups of the CTA's stretch in order.
+struct AttItem {
+  int v;      // row group
+  int first;  // its first tile here
+  int count;  // tiles here
+};
+
+__device__ __forceinline__ AttItem att_item(const int* prefix, int V, int t, int end) {
+  AttItem it;
+  it.v = att_find(prefix, V, t);
+  it.first = t - prefix[it.v];
+  it.count = min(prefix[it.v + 1], end) - t;
+  return it;
+}
+
+// --------------------------------------------------------------------------
+// Warp 12: pages into shared memory.
+// --------------------------------------------------------------------------
+template <int R, bool E4>
+__device__ __forceinline__ void att_load(const Kv4AttendParams& p, AttShared<R>& s, uint32_t smem, uint32_t bars, int V,
+                                         int t0, int t1) {
+  using L = AttPlan<R, E4>;
+  const int lane = threadIdx.x & 31;
+  const int shift = p.cache.shift, page = 1 << shift;
+  const int entries = kAttTile >> shift;  // pages of a tile
+  const int per_unit = shift < 5 ? 2 : 1;
+  const uint32_t unit_tok = min(page, kAttUnit);
+
+  int v = att_find(s.prefix, V, t0);
+  // page of entry `lane` of tile t, -1: none
+  auto fetch = [&](int t) -> int {
+    while (t >= s.prefix[v + 1]) ++v;
+    const int64_t idx = (static_cast<int64_t>(t - s.prefix[v]) * kAttTile >> shift) + lane;
+    int id = -1;
+    if (lane < entries && idx << shift < s.len[v]) {
+      id = p.block_table[s.seq[v] * p.table_stride + idx];
+      if (id < 0 || id >= p.cache.num_pages) {
+        atomicOr(&g_device_status, kDevStatusBadIndex);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  int next = fetch(t0);
+  bool ok = true;
+  int k = 0, u = 0, rope = 0;
+  for (int t = t0; ok && t < t1; ++t, ++k) {
+    const int id = next;
+    if (t + 1 < t1) next = fetch(t + 1);
+    const uint8_t* base = p.cache.base + static_cast<int64_t>(max(id, 0)) * p.cache.page_stride;
+    auto load_rope = [&]() {
+      const int rb = k % L::RopeBufs;
+      if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rb), (k / L::RopeBufs - 1) & 1, s);
+      if (!ok) return;
+      const uint32_t bar = bars + 8 * (L::RopeFull + rb);
+      const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * page * kKv4RopeBytes);
+      __syncwarp();
+      if (id >= 0)
+        bulk_load_1d(smem + L::Rope + rb * kRopeTile + lane * page * kKv4RopeBytes, base + kv4_rope_off(0, shift),
+                     page * kKv4RopeBytes, bar);
+      ++rope;
+    };
+    if (L::RopeBufs == 2) load_rope();
+    for (int q = 0; ok && q < kAttUnits; ++q, ++u) {
+      const int st = u % L::Units;
+      if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + st), (u / L::Units - 1) & 1, s);
+      if (!ok) break;
+      const uint32_t bar = bars + 8 * (L::RawFull + st);
+      // lane e < per_unit copies the unit's e-th page part
+      const int entry = per_unit == 2 ? 2 * q + (lane & 1) : (q * kAttUnit) >> shift;
+      const int uid = __shfl_sync(0xffffffffu, id, entry);
+      const unsigned have = __ballot_sync(0xffffffffu, lane < per_unit && uid >= 0);
+      if (lane == 0) {
+        s.umask[st] = per_unit == 2 ? have : (have ? 3u : 0u);
+        mbar_arrive_expect_tx(bar, __popc(have) * unit_tok * (kKv4CodeBytes + kKv4Blocks));
+      }
+      __syncwarp();
+      if (lane < per_unit && uid >= 0) {
+        const uint8_t* from = p.cache.base + uid * p.cache.page_stride;
+        const uint32_t pos = (q * kAttUnit) & (page - 1);
+        const uint32_t dst = smem + L::Raw + st * kUnitBytes;
+        bulk_load_1d(dst + lane * unit_tok * kKv4CodeBytes, from + kv4_code_off(pos), unit_tok * kKv4CodeBytes, bar);
+        bulk_load_1d(dst + kUnitCodes + lane * unit_tok * kKv4Blocks, from + kv4_scale_off(pos, shift),
+                     unit_tok * kKv4Blocks, bar);
+      }
+    }
+    if (ok && L::RopeBufs == 1) load_rope();
+  }
+  if (!ok) {  // copies in flight land before the CTA ends
+    auto drain = [&](uint32_t bar, uint32_t parity) {
+      const unsigned long long at = globaltimer_ns();
+      while (!mbar_try_wait(bar, parity) && globaltimer_ns() - at < kAttWaitNs) {
+      }
+    };
+    for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
+    for (int i = max(0, rope - L::RopeBufs); i < rope; ++i)
+      drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
+  }
+}
+
+// --------------------------------------------------------------------------
+// Warps 4-11: codes -> E4M3 tile.  A lane takes one block of 32 latents of
+// one token; half a warp a token.
+// --------------------------------------------------------------------------
+template <int R, bool E4>
+__device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint32_t bars, int tiles) {
+  using L = AttPlan<R, E4>;
+  const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
+  const int j = lane & 15;
+  const bool low = lane < 16;
+  const int first_half = (j >> 2) & 1;
+  int u = 0;
+  for (int k = 0; k < tiles; ++k) {
+    const int b = k & 1;
+    if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b), (k / 2 - 1) & 1, s)) return;
+    uint8_t* tile = smem + L::K8 + b * kK8Tile + (j >> 2) * kK8Block;
+    for (int q = 0; q < kAttUnits; ++q, ++u) {
+      const int st = u % L::Units;
+      if (!att_wait(bars + 8 * (L::RawFull + st), (u / L::Units) & 1, s)) return;
+      const uint8_t* raw = smem + L::Raw + st * kUnitBytes;
+      uint4 w[2];
+      uint32_t sc[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = 4 * dw + 2 * i + (lane >> 4);
+        w[i] = *reinterpret_cast<const uint4*>(raw + tok * kKv4CodeBytes + 16 * j);
+        sc[i] = raw[kUnitCodes + tok * kKv4Blocks + j];
+      }
+      if (dw == 0 && lane == 0) s.tmask[b][q] = s.umask[st];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = kAttUnit * q + 4 * dw + 2 * i + (lane >> 4);
+        const uint32_t sv = kv4_scale_clamp(sc[i]);
+        const uint32_t m0 = __reduce_max_sync(0xffffffffu, low ? sv : 0u);
+        const uint32_t m1 = __reduce_max_sync(0xffffffffu, low ? 0u : sv);
+        const uint32_t sm = low ? m0 : m1;
+        if (j == 0) s.smax[b][row] = static_cast<uint8_t>(sm);
+        const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[min(sm - sv, 31u)]);
+        auto word = [&](uint32_t x, uint32_t& lo, uint32_t& hi) {
+          const uint32_t m = x & 0x77777777u;
+          lo = prmt(lut.x, lut.y, m) | (x & 0x80808080u);
+          hi = prmt(lut.x, lut.y, m >> 16) | ((x << 4) & 0x80808080u);
+        };
+        uint4 a, c;
+        word(w[i].x, a.x, a.y);
+        word(w[i].y, a.z, a.w);
+        word(w[i].z, c.x, c.y);
+        word(w[i].w, c.z, c.w);
+        const int at = 2 * (j & 3);
+        *reinterpret_cast<uint4*>(tile + row * 128 + (((at + first_half) ^ (row & 7)) << 4)) = a;
+        *reinterpret_cast<uint4*>(tile + row * 128 + (((at + (first_half ^ 1)) ^ (row & 7)) << 4)) = c;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (L::K8Full + b));
+  }
+}
+
+// --------------------------------------------------------------------------
+// Warp 13: one thread issues the MMAs.  The scores of tile k+1 go ahead of
+// the output product of tile k, so the tensor cores work while the softmax
+// warps do.
+// --------------------------------------------------------------------------
+template <int R, bool E4>
+__device__ __forceinline__ void att_mma(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V, int t0,
+                                        int t1) {
+  using L = AttPlan<R, E4>;
+  constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
+  constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
+  constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
+  bool ok = true;
+  // output product of tile k; first: it begins row group number `item`
+  auto output = [&](int k, bool first, int item) {
+    ok = att_wait_one(bars + 8 * L::PFull, k & 1, s);
+    if (ok && first && item > 0) ok = att_wait_one(bars + 8 * L::OEmpty, (item - 1) & 1, s);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int ks = 0; ks < kAttTile / 32; ++ks) {
+        // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
+        const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
+        // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
+        const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
+        umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (first && ks == 0) ? 0u : 1u);
+      }
+    umma_commit(bars + 8 * (L::K8Empty + (k & 1)));
+    umma_commit(bars + 8 * L::PvDone);
+  };
+  int k = 0, item = 0, last_item = 0;
+  bool last_first = false;
+  for (int t = t0; ok && t < t1; ++item) {
+    const AttItem it = att_item(s.prefix, V, t, t1);
+    t += it.count;
+    ok = att_wait_one(bars + 8 * L::QFull, item & 1, s);
+    for (int n = 0; ok && n < it.count; ++n, ++k) {
+      const int b = k & 1, rb = k % L::RopeBufs, sb = k % L::SBufs;
+      ok = att_wait_one(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
+      if (ok) ok = att_wait_one(bars + 8 * (L::K8Full + b), (k / 2) & 1, s);
+      if (ok && k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + sb * L::SCols;
+      const uint32_t k8 = smem + L::K8 + b * kK8Tile;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint64_t ad = smem_desc_sw128(k8 + (c >> 2) * kK8Block + (c & 3) * 32, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(smem + L::Q + (c >> 2) * L::QBlock + (c & 3) * 32, 16, 1024);
+        umma_f8(d, ad, bd, id_s, c > 0);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint64_t ad = smem_desc_sw128(smem + L::Rope + rb * kRopeTile + c * 32, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(smem + L::QPe + c * 32, 16, 1024);
+        umma_bf16(d + L::NQ, ad, bd, id_r, c > 0);
+      }
+      umma_commit(bars + 8 * (L::RopeEmpty + rb));
+      umma_commit(bars + 8 * (L::SFull + sb));
+      if (k > 0) output(k - 1, last_first, last_item);
+      last_first = n == 0;
+      last_item = item;
+    }
+  }
+  if (ok && k > 0) output(k - 1, last_first, last_item);
+  if (!ok) {  // what was issued completes before the CTA ends
+    umma_commit(bars + 8 * L::Drain);
+    const unsigned long long at = globaltimer_ns();
+    while (!mbar_try_wait(bars + 8 * L::Drain, 0) && globaltimer_ns() - at < kAttWaitNs) {
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Warps 0-3
+// --------------------------------------------------------------------------
+
+// Queries of row group v into shared memory, and what its rows need (turn:
+// which of the two copies).
+template <int R, bool E4>
+__device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>& s, uint8_t* smem, uint32_t bars, int v,
+                                          int turn) {
+  using L = AttPlan<R, E4>;
+  constexpr int TPR = 128 / R;  // threads per row
+  const int tid = threadIdx.x;
+  const int r = tid / TPR, sub = tid % TPR;
+  const int rows = p.q_len * p.H;
+  const int groups = (rows + R - 1) / R;
+  const int b = v / groups, rr = (v % groups) * R + r;
+  const bool real = rr < rows;
+  const int i = real ? rr / p.H : 0, h = real ? rr % p.H : 0;
+  const int64_t m = static_cast<int64_t>(b) * p.q_len + i;
+  const int64_t at = m * p.q_ts + h * kOutDim;
+  uint8_t* q8 = smem + L::Q;
+  float cr = p.softmax_scale * 1.4426950408889634f;
+  if constexpr (E4) {
+    const uint8_t* src = p.q + at;
+#pragma unroll
+    for (int c = sub; c < 36; c += TPR) {  // 16-byte chunks: 32 of latents, 4 of rope
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (real) x = ld_u128(src + 16 * c);
+      if (c < 32) {
+        *reinterpret_cast<uint4*>(q8 + (c >> 3) * L::QBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      } else {  // rope codes -> BF16, exact
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t o[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const uint32_t two = w[2 * e + (f >> 1)] >> (16 * (f & 1));
+            o[f] = mul_bf16x2(e4m3x2_to_bf16x2_scaled(two), 0x7B807B80u);  // 2^120
+            if ((two & 0x7Fu) == 0x7Fu) o[f] |= 0x7FC0u;
+            if ((two & 0x7F00u) == 0x7F00u) o[f] |= 0x7FC00000u;
+          }
+          const int ch = 2 * (c - 32) + e;
+          *reinterpret_cast<uint4*>(smem + L::QPe + r * 128 + ((ch ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+    cr *= *p.q_scale;
+  } else {
+    constexpr int N = 64 / TPR;  // 16-byte chunks (8 elements) of latents per thread
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + at;
+    uint4 x[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = real ? ld_u128(src + 8 * (n * TPR + sub)) : make_uint4(0, 0, 0, 0);
+    constexpr int NR = 8 / TPR;  // chunks of rope per thread
+    uint4 pe[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) pe[n] = real ? ld_u128(src + kLatent + 8 * (n * TPR + sub)) : make_uint4(0, 0, 0, 0);
+    auto top = [](uint4 a) {
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      uint32_t t = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t = max(t, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+      return t;
+    };
+    uint32_t ml = 0, mp = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) ml = max(ml, top(x[n]));
+#pragma unroll
+    for (int n = 0; n < NR; ++n) mp = max(mp, top(pe[n]));
+#pragma unroll
+    for (int d = 1; d < TPR; d <<= 1) {
+      ml = max(ml, __shfl_xor_sync(0xffffffffu, ml, d));
+      mp = max(mp, __shfl_xor_sync(0xffffffffu, mp, d));
+    }
+    // exponent of the row: its latents' largest, but not so far below the
+    // rope part's that scaling that part would overflow
+    int e = static_cast<int>(ml >> 7);
+    e = max(max(e, static_cast<int>(mp >> 7) - 40), 8);
+    const bool bad = ml >= 0x7F80u || mp >= 0x7F80u;  // NaN or infinity: the whole row
+    const float f = bad ? __uint_as_float(0x7FC00000u) : exp2f(static_cast<float>(134 - e));
+    cr *= exp2f(static_cast<float>(e - 134));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = n * TPR + sub;  // elements 8c..8c+7: half of 16-byte E4M3 chunk c/2
+      const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hh = 0, ll = 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float a = bf16_lo(w[2 * g + q]) * f, c1 = bf16_hi(w[2 * g + q]) * f;
+          const uint32_t t8 = pack_e4m3x2(c1, a);
+          // the code back as a float: bits * 2^-120 in BF16, exact
+          const uint32_t back = mul_bf16x2(e4m3x2_to_bf16x2_scaled(t8), 0x7B807B80u);
+          const uint32_t l8 = pack_e4m3x2((c1 - bf16_hi(back)) * 16.f, (a - bf16_lo(back)) * 16.f);
+          hh |= t8 << (16 * q);
+          ll |= l8 << (16 * q);
+        }
+        hi[g] = hh;
+        lo[g] = ll;
+      }
+      uint8_t* to = q8 + (c >> 4) * L::QBlock + ((((c >> 1) & 7) ^ (r & 7)) << 4) + 8 * (c & 1);
+      *reinterpret_cast<uint2*>(to + r * 128) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(to + (R + r) * 128) = make_uint2(lo[0], lo[1]);
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int c = n * TPR + sub;
+      const uint32_t w[4] = {pe[n].x, pe[n].y, pe[n].z, pe[n].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) o[g] = pack_bf16x2(bf16_hi(w[g]) * f, bf16_lo(w[g]) * f);
+      *reinterpret_cast<uint4*>(smem + L::QPe + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (sub == 0) {
+    s.cr[turn][r] = real ? cr : 0.f;
+    s.limit[turn][r] = real ? s.len[v] - (p.q_len - 1 - i) : 0x7fffffff;
+    s.xoff[turn][r] = real ? m * p.x_ts + h * kLatent : -1;
+    s.lseoff[turn][r] = static_cast<int>(m) * p.H + h;
+  }
+  fence_proxy_async_smem();
+  mbar_arrive(bars + 8 * L::QFull);
+}
+
+template <int R, bool E4>
+__device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<R>& s, uint8_t* smem, uint32_t bars,
+                                            uint32_t tmem, int V, int t0, int t1) {
+  using L = AttPlan<R, E4>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+  float* mref = s.mref[warp];
+  float* alpha = s.alpha[warp];
+  // Barrier of the four warps, bounded like every wait.
+  uint32_t soft_phase = 0;
+  auto soft_barrier = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * L::Soft);
+    const bool ok = att_wait(bars + 8 * L::Soft, soft_phase & 1, s);
+    ++soft_phase;
+    return ok;
+  };
+  AttItem it = att_item(s.prefix, V, t0, t1);
+  att_query<R, E4>(p, s, smem, bars, it.v, 0);
+  int k = 0;
+  for (int t = t0, item = 0; t < t1; ++item) {
+    const int turn = item & 1;
+    // every warp has left the row group before (what follows reuses its
+    // places), and the first one's rows are known
+    if (!soft_barrier()) return;
+    const int next_t = t + it.count;
+    AttItem next = it;
+    if (next_t < t1) next = att_item(s.prefix, V, next_t, t1);
+    float top = -INFINITY;  // M of row `lane`
+    float l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) l[r] = 0.f;
+    if (lane < R) mref[lane] = -kAttShift;
+    __syncwarp();
+    for (int n = 0; n < it.count; ++n, ++k) {
+      const int b = k & 1, sb = k % L::SBufs;
+      if (!att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s)) return;
+      if (!att_wait(bars + 8 * (L::K8Full + b), (k / 2) & 1, s)) return;  // smax and tmask are this tile's
+      tc_fence_after();
+      // the scores of the row group's last tile are in: its queries are done with
+      if (n == it.count - 1 && next_t < t1) att_query<R, E4>(p, s, smem, bars, next.v, turn ^ 1);
+      const uint32_t sm = s.smax[b][tid];
+      const float ts = sm == kKv4ScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((sm - 6u) << 23);
+      const float its = __uint_as_float((260u - sm) << 23);
+      const float et = static_cast<float>(static_cast<int>(sm) - 133);
+      const int64_t tile_tok = static_cast<int64_t>(it.first + n) * kAttTile;
+      const bool whole = *reinterpret_cast<const uint32_t*>(s.tmask[b]) == 0x03030303u &&
+                         tile_tok + kAttTile <= s.limit[turn][0];
+      const bool here = (s.tmask[b][warp] >> (lane >> 4)) & 1;
+      float y[R];
+#pragma unroll
+      for (int hb = 0; hb < R; hb += 16) {
+        float w[16];
+        const uint32_t d = tmem + lanes + sb * L::SCols + hb;
+        if constexpr (E4) {
+          uint32_t v[32];
+          tmem_ld2x16(d, d + R, v);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) w[r] = fmaf(__uint_as_float(v[r]), ts, __uint_as_float(v[16 + r]));
+        } else {
+          uint32_t v[48];
+          tmem_ld3x16(d, d + R, d + 2 * R, v);
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            w[r] = fmaf(fmaf(__uint_as_float(v[16 + r]), 0.0625f, __uint_as_float(v[r])), ts, __uint_as_float(v[32 + r]));
+        }
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(&s.cr[turn][hb + r]);
+          y[hb + r] = fmaf(w[r], c.x, et);
+          y[hb + r + 1] = fmaf(w[r + 1], c.y, et);
+          y[hb + r + 2] = fmaf(w[r + 2], c.z, et);
+          y[hb + r + 3] = fmaf(w[r + 3], c.w, et);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bars + 8 * (L::SEmpty + sb));
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (!here || tile_tok + tid >= s.limit[turn][r]) y[r] = -INFINITY;
+      }
+      float mine = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float m = warp_max(y[r]);
+        if (lane == r) mine = m;
+      }
+      if (lane < R) s.wmax[b][warp][lane] = mine;
+      if (!soft_barrier()) return;
+      bool up = false;
+      float tm = -INFINITY;
+      if (lane < R) {
+        tm = fmaxf(fmaxf(s.wmax[b][0][lane], s.wmax[b][1][lane]), fmaxf(s.wmax[b][2][lane], s.wmax[b][3][lane]));
+        up = tm > top + kAttSlack || (top == -INFINITY && tm > top);
+      }
+      if (__any_sync(0xffffffffu, up)) {
+        __syncwarp();
+        if (lane < R) {
+          alpha[lane] = up ? (top == -INFINITY ? 0.f : ex2(top - tm)) : 1.f;
+          if (up) {
+            top = tm;
+            mref[lane] = tm - kAttShift;
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R; r += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(&alpha[r]);
+          l[r] *= a.x;
+          l[r + 1] *= a.y;
+          l[r + 2] *= a.z;
+          l[r + 3] *= a.w;
+        }
+        if (n > 0) {
+          if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;
+          tc_fence_after();
+          for (int c = 0; c < 4 * L::NP; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tmem + lanes + L::OCol + c, o);
+            const float* a = &alpha[c % R];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * a[r]);
+            tmem_st16(tmem + lanes + L::OCol + c, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      if (k > 0 && !att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;  // P is free
+      uint8_t* ps = smem + L::P + tid * 16;
+#pragma unroll
+      for (int hb = 0; hb < R; hb += 16) {
+        uint32_t t[3][4];
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&mref[hb + r]);
+          const float e0 = ex2(y[hb + r] - m.x), e1 = ex2(y[hb + r + 1] - m.y), e2 = ex2(y[hb + r + 2] - m.z),
+                      e3 = ex2(y[hb + r + 3] - m.w);
+          l[hb + r] = fmaf(e0, its, l[hb + r]);
+          l[hb + r + 1] = fmaf(e1, its, l[hb + r + 1]);
+          l[hb + r + 2] = fmaf(e2, its, l[hb + r + 2]);
+          l[hb + r + 3] = fmaf(e3, its, l[hb + r + 3]);
+          // three E5M2 terms: the top bytes of FP16 are E5M2, truncated; the
+          // differences are exact, the last term is rounded
+          __half2 a = __floats2half2_rn(e0, e1), c = __floats2half2_rn(e2, e3);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            uint32_t au = *reinterpret_cast<uint32_t*>(&a), cu = *reinterpret_cast<uint32_t*>(&c);
+            if (q == 2) {
+              au += 0x00800080u;
+              cu += 0x00800080u;
+            }
+            t[q][r / 4] = prmt(au, cu, 0x7531u);
+            if (q < 2) {
+              uint32_t ah = au & 0xFF00FF00u, ch = cu & 0xFF00FF00u;
+              a = __hsub2(a, *reinterpret_cast<__half2*>(&ah));
+              c = __hsub2(c, *reinterpret_cast<__half2*>(&ch));
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<uint4*>(ps + (q * (R / 16) + hb / 16) * L::PChunk) =
+              make_uint4(t[q][0], t[q][1], t[q][2], t[q][3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(bars + 8 * L::PFull);
+    }
+
+    // The row group's end here: sums over the tokens, O from tensor memory.
+    const int tiles = s.prefix[it.v + 1] - s.prefix[it.v];
+    const bool complete = it.count == tiles;
+    float mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v = l[r];
+#pragma unroll
+      for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      if (lane == r) mine = v;
+    }
+    if (lane < R) s.lsum[warp][lane] = mine;
+    if (!soft_barrier()) return;
+    float* part = nullptr;
+    if (!complete) {
+      const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
+      part = reinterpret_cast<float*>(p.ws) + slot * att_slot_floats<R>();
+    }
+    __syncwarp();
+    if (lane < R) {
+      const float sum = (s.lsum[0][lane] + s.lsum[1][lane]) + (s.lsum[2][lane] + s.lsum[3][lane]);
+      const float m = mref[lane];
+      const int64_t xo = s.xoff[turn][lane];
+      if (complete) {
+        const bool none = s.limit[turn][lane] <= 0;
+        alpha[lane] = none ? 0.f : 1.f / sum;
+        if (warp == 0 && xo >= 0 && p.lse) p.lse[s.lseoff[turn][lane]] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      } else if (warp == 0) {
+        part[R * kLatent + lane] = top == -INFINITY ? top : m;
+        part[R * kLatent + R + lane] = sum;
+      }
+    }
+    __syncwarp();
+    if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;
+    tc_fence_after();
+    for (int mt = 0; mt < 4; ++mt) {
+      const int col = mt * 128 + 32 * warp + lane;
+#pragma unroll
+      for (int hb = 0; hb < R; hb += 16) {
+        uint32_t v[48];
+        const uint32_t d = tmem + lanes + L::OCol + mt * L::NP + hb;
+        tmem_ld3x16(d, d + R, d + 2 * R, v);
+        float o[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          o[r] = __uint_as_float(v[r]) + (__uint_as_float(v[16 + r]) + __uint_as_float(v[32 + r]));
+        if (!complete) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) part[(hb + r) * kLatent + col] = o[r];
+        } else {
+          // two rows at a time: even lanes take the first row's two latents, odd lanes the second's
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const float a = o[r] * alpha[hb + r], c = o[r + 1] * alpha[hb + r + 1];
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+            const int64_t xo = s.xoff[turn][hb + r + (odd ? 1 : 0)];
+            const uint32_t two = odd ? pack_bf16x2(c, got) : pack_bf16x2(got, a);
+            if (xo >= 0) *reinterpret_cast<uint32_t*>(p.x + xo + (col & ~1)) = two;
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(bars + 8 * L::OEmpty);
+    t = next_t;
+    it = next;
+  }
+}
+
+// Rows of the groups that see no token.
+template <int R>
+__device__ __forceinline__ void att_empty_rows(const Kv4AttendParams& p, const AttSchedule& s, int V) {
+  const int rows = p.q_len * p.H;
+  const int groups = (rows + R - 1) / R;
+  for (int v = blockIdx.x; v < V; v += gridDim.x) {
+    if (s.prefix[v + 1] != s.prefix[v]) continue;
+    const int r0 = (v % groups) * R, n = min(R, rows - r0);
+    for (int e = threadIdx.x; e < n * 64; e += 128) {
+      const int rr = r0 + e / 64;
+      const int64_t m = static_cast<int64_t>(v / groups) * p.q_len + rr / p.H;
+      st_u128(p.x + m * p.x_ts + (rr % p.H) * kLatent + 8 * (e % 64), make_uint4(0, 0, 0, 0));
+      if (e % 64 == 0 && p.lse) p.lse[m * p.H + rr % p.H] = -INFINITY;
+    }
+  }
+}
+
+template <int R, bool E4>
+__global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using L = AttPlan<R, E4>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  AttShared<R>& s = *reinterpret_cast<AttShared<R>*>(smem + L::Misc);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t bars = smem_u32(s.bars);
+  if (tid < L::BarCount) {
+    uint32_t count = 1;
+    if ((tid >= L::RawEmpty && tid < L::RopeFull) || tid == L::K8Full || tid == L::K8Full + 1) count = kAttDequantWarps;
+    if (tid == L::Soft) count = kAttSoftWarps;
+    if ((tid >= L::SEmpty && tid < L::PFull) || tid == L::PFull || tid == L::QFull || tid == L::OEmpty) count = 128;
+    mbar_init(bars + 8 * tid, count);
+    fence_barrier_init();
+  }
+  if (tid < 32) {
+    // row k: the magnitudes times 2^(6-k) as E4M3, exact up to k = 14
+    const float f = __uint_as_float(static_cast<uint32_t>(133 - tid) << 23);
+    s.lut[tid][0] = pack_e4m3x2(0.5f * f, 0.f) | (pack_e4m3x2(1.5f * f, f) << 16);
+    s.lut[tid][1] = pack_e4m3x2(3.f * f, 2.f * f) | (pack_e4m3x2(6.f * f, 4.f * f) << 16);
+    if (tid == 0) s.fail = 0;
+  }
+  pdl_wait();
+  if (warp == kAttMmaWarp) tmem_alloc(smem_u32(&s.tmem), 512);
+  const int V = att_schedule(p, R, s, blockIdx.x == 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
+  const int total = s.prefix[V];
+  const int active = att_active(total, gridDim.x);
+  const bool mine = static_cast<int>(blockIdx.x) < active;
+  const int t0 = mine ? att_begin(total, blockIdx.x, active) : 0, t1 = mine ? att_begin(total, blockIdx.x + 1, active) : 0;
+  const uint32_t base = smem_u32(smem);
+  if (warp < kAttSoftWarps) {
+    att_empty_rows<R>(p, s, V);
+    if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, V, t0, t1);
+  } else if (t0 < t1) {
+    if (warp < kAttLoadWarp) {
+      att_dequant<R, E4>(s, smem, bars, t1 - t0);
+    } else if (warp == kAttLoadWarp) {
+      att_load<R, E4>(p, s, base, bars, V, t0, t1);
+    } else if ((tid & 31) == 0) {
+      att_mma<R, E4>(s, base, bars, tmem, V, t0, t1);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == kAttMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// --------------------------------------------------------------------------
+// Join: the pieces of a row group that several CTAs worked on, in their
+// order.  A job is a row and 128 of its latents; eight warps take the pieces
+// in turn.
+// --------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+struct JoinShared {
+  AttSchedule s;
+  int split[kAttMaxSeqs];
+  int split_warp[8];
+  float m[8];
+  float wsum[8];
+  alignas(16) float part[8][128];
+};
+
+template <int R>
+__global__ void __launch_bounds__(kJoinThreads)
+    mlaqp_kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, const int grid) {
+  extern __shared__ uint8_t smem_raw[];
+  JoinShared& j = *reinterpret_cast<JoinShared*>(smem_raw);
   pdl_launch_dependents();
   pdl_wait();
-  const int m = blockIdx.x, b = m / p.q_len, i = m % p.q_len;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seq = p.seqs ? p.seqs[b] : b;
-  int64_t n = 0;
-  if (seq >= 0 && seq < p.num_seqs) {
-    n = p.seq_lens[seq];
-    if (n < 0 || n > p.table_stride << p.cache.shift) {
-      if (tid == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
-      n = 0;
-    }
-  } else if (tid == 0) {
-    atomicOr(&g_device_status, kDevStatusBadIndex);
-  }
-  n -= p.q_len - 1 - i;
-  const float qs = E4M3 ? *p.q_scale : 1.f;
-  for (int e = tid; e < p.H * kOutDim; e += kAttendThreads) {
-    const int64_t at = m * p.q_ts + e;
-    float v;
-    if constexpr (E4M3) v = e4m3_value(p.q[at]) * qs;
-    else v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.q)[at]) << 16);
-    s.q[e / kOutDim][e % kOutDim] = v;
-  }
-  if (tid < 16) {
-    s.top[tid] = -INFINITY;
-    s.sum[tid] = 0.f;
-  }
-  float acc[2][16];
-  for (int h = 0; h < 16; ++h) acc[0][h] = acc[1][h] = 0.f;
-  const int32_t* table = p.block_table + seq * p.table_stride;
-  for (int64_t t0 = 0; t0 < n; t0 += kAttendTile) {
-    __syncthreads();
-    for (int k = warp; k < kAttendTile; k += kAttendThreads / 32) {
-      const int64_t t = t0 + k;
-      const int page = t < n ? table[t >> p.cache.shift] : -1;
-      const bool ok = t < n && page >= 0 && page < p.cache.num_pages;
-      if (t < n && !ok && lane == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
-      if (lane == 0) s.valid[k] = ok;
-      float* key = s.k[k];
-      if (ok) {
-        const uint32_t pos = t & ((1 << p.cache.shift) - 1);
-        const uint8_t* base = p.cache.base + page * p.cache.page_stride;
-        const int j = lane >> 1, half = lane & 1;
-        const uint2 codes =
-            *reinterpret_cast<const uint2*>(base + kv4_code_off(pos) + 16 * j + 8 * (half ^ ((j >> 2) & 1)));
-        const uint32_t sc = kv4_scale_bf16x2(base[kv4_scale_off(pos, p.cache.shift) + j]);
-        uint32_t a[4], c[4];
-        kv4_word_bf16(codes.x, a);
-        kv4_word_bf16(codes.y, c);
-        for (int e = 0; e < 4; ++e) {
-          a[e] = mul_bf16x2(a[e], sc);
-          c[e] = mul_bf16x2(c[e], sc);
-          key[16 * lane + 2 * e] = bf16_lo(a[e]);
-          key[16 * lane + 2 * e + 1] = bf16_hi(a[e]);
-          key[16 * lane + 8 + 2 * e] = bf16_lo(c[e]);
-          key[16 * lane + 8 + 2 * e + 1] = bf16_hi(c[e]);
-        }
-        const uint32_t r = ld_u32(base + kv4_rope_off(pos, p.cache.shift) + 16 * ((lane >> 2) ^ (pos & 7)) + 4 * (lane & 3));
-        key[kLatent + 2 * lane] = bf16_lo(r);
-        key[kLatent + 2 * lane + 1] = bf16_hi(r);
-      } else {
-        for (int e = lane; e < kOutDim; e += 32) key[e] = 0.f;
-      }
-    }
-    __syncthreads();
-    for (int e = tid; e < p.H * kAttendTile; e += kAttendThreads) {
-      const int h = e / kAttendTile, k = e % kAttendTile;
-      float d = 0.f;
-      for (int c = 0; c < kOutDim; ++c) d += s.q[h][c] * s.k[k][c];
-      s.p[h][k] = s.valid[k] ? d * p.softmax_scale : -INFINITY;
-    }
-    __syncthreads();
-    for (int h = warp; h < p.H; h += kAttendThreads / 32) {
-      const float v = s.p[h][lane];
-      float top = v;
-      bool nan = v != v;
-      float sum;
-      for (int d = 16; d; d >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      }
-      nan = __any_sync(0xffffffffu, nan);
-      const float old = s.top[h];
-      top = nan ? __uint_as_float(0x7FC00000u) : fmaxf(old, top);
-      if (old != old) top = old;
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float e = expf(v - ref);
-      sum = e;
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      s.p[h][lane] = e;
-      __syncwarp();
-      if (lane == 0) {
-        const float alpha = expf(old - ref);
-        s.alpha[h] = alpha;
-        s.sum[h] = s.sum[h] * alpha + sum;
-        s.top[h] = top;
-      }
-    }
-    __syncthreads();
-    for (int h = 0; h < p.H; ++h) {
-      float a0 = acc[0][h] * s.alpha[h], a1 = acc[1][h] * s.alpha[h];
-      for (int k = 0; k < kAttendTile; ++k) {
-        a0 += s.p[h][k] * s.k[k][tid];
-        a1 += s.p[h][k] * s.k[k][tid + 256];
-      }
-      acc[0][h] = a0;
-      acc[1][h] = a1;
-    }
-  }
+  const int V = att_schedule(p, R, j.s, false);
+  const int* prefix = j.s.prefix;
+  const int total = prefix[V];
+  if (total == 0) return;
+  const int ctas = att_active(total, grid);
+  // the row groups that more than one CTA worked on, in order
+  const bool split = tid < V && prefix[tid + 1] > prefix[tid] &&
+                     att_owner(total, prefix[tid], ctas) != att_owner(total, prefix[tid + 1] - 1, ctas);
+  const unsigned who = __ballot_sync(0xffffffffu, split);
+  if (lane == 0) j.split_warp[warp] = __popc(who);
   __syncthreads();
-  for (int h = 0; h < p.H; ++h) {
-    const float sum = s.sum[h];
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* x = p.x + m * p.x_ts + h * kLatent;
-    x[tid] = static_cast<uint16_t>(pack_bf16x2(0.f, acc[0][h] * inv));
-    x[tid + 256] = static_cast<uint16_t>(pack_bf16x2(0.f, acc[1][h] * inv));
-    if (tid == 0 && p.lse) p.lse[m * p.H + h] = sum == 0.f ? -INFINITY : s.top[h] + logf(sum);
+  int rank = __popc(who & ((1u << lane) - 1u)), n_split = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) rank += j.split_warp[w];
+    n_split += j.split_warp[w];
   }
+  if (split) j.split[rank] = tid;
+  __syncthreads();
+  const int rows = p.q_len * p.H, groups = (rows + R - 1) / R;
+  const int jobs = n_split * R * 4;
+  for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
+    const int v = j.split[job / (R * 4)], r = job / 4 % R, quarter = job % 4;
+    const int rr = (v % groups) * R + r;
+    if (rr >= rows) continue;
+    const int c0 = att_owner(total, prefix[v], ctas), c1 = att_owner(total, prefix[v + 1] - 1, ctas);
+    auto slot = [&](int c) {
+      const int at = 2 * c + (c == c0 && prefix[v] > att_begin(total, c, ctas) ? 1 : 0);
+      return reinterpret_cast<const float*>(p.ws) + at * att_slot_floats<R>();
+    };
+    float top = -INFINITY;
+    for (int c = c0 + tid; c <= c1; c += kJoinThreads) top = fmaxf(top, slot(c)[R * kLatent + r]);
+    top = warp_max(top);
+    __syncthreads();
+    if (lane == 0) j.m[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, j.m[w]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = c0 + warp; c <= c1; c += 8) {
+      const float* q = slot(c);
+      const float f = ex2(q[R * kLatent + r] - top);
+      const float4 o = *reinterpret_cast<const float4*>(q + r * kLatent + 128 * quarter + 4 * lane);
+      sum = fmaf(q[R * kLatent + R + r], f, sum);
+      acc.x = fmaf(o.x, f, acc.x);
+      acc.y = fmaf(o.y, f, acc.y);
+      acc.z = fmaf(o.z, f, acc.z);
+      acc.w = fmaf(o.w, f, acc.w);
+    }
+    *reinterpret_cast<float4*>(&j.part[warp][4 * lane]) = acc;
+    if (lane == 0) j.wsum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(&j.part[w][4 * lane]);
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+        sum += j.wsum[w];
+      }
+      const int i = rr / p.H, h = rr % p.H;
+      const int64_t m = static_cast<int64_t>(v / groups) * p.q_len + i;
+      const bool none = j.s.len[v] - (p.q_len - 1 - i) <= 0;
+      const float inv = 1.f / sum;
+      uint2 o = make_uint2(0u, 0u);
+      if (!none) {
+        o.x = pack_bf16x2(acc.y * inv, acc.x * inv);
+        o.y = pack_bf16x2(acc.w * inv, acc.z * inv);
+      }
+      *reinterpret_cast<uint2*>(p.x + m * p.x_ts + h * kLatent + 128 * quarter + 4 * lane) = o;
+      if (lane == 0 && quarter == 0 && p.lse)
+        p.lse[m * p.H + h] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+}
+
+struct AttKernels {
+  const void* main;
+  const void* join;
+  int smem;
+};
+
+template <int R, bool E4>
+AttKernels att_kernels() {
+  return AttKernels{reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<R, E4>),
+                    reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), AttPlan<R, E4>::Bytes};
+}
+
+// 16 rows where all (query token, head) pairs of a sequence fit, else groups of 32.
+AttKernels att_pick(int q_len, int H, bool e4m3) {
+  if (q_len * H <= 16) return e4m3 ? att_kernels<16, true>() : att_kernels<16, false>();
+  return e4m3 ? att_kernels<32, true>() : att_kernels<32, false>();
 }
 
 }  // namespace
 
-cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int, cudaStream_t stream) {
-  void* args[1] = {const_cast<Kv4AttendParams*>(&p)};
-  const void* fn = q_e4m3 ? reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<true>)
-                          : reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<false>);
-  return kv4_launch(fn, static_cast<unsigned>(p.B * p.q_len), kAttendThreads, sizeof(AttendSmem), stream, args);
+cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream) {
+  const AttKernels k = att_pick(p.q_len, p.H, q_e4m3);
+  void* args[2] = {const_cast<Kv4AttendParams*>(&p), &sm_count};
+  const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(sm_count), kAttThreads, k.smem, stream, args);
+  if (e != cudaSuccess) return e;
+  return kv4_launch(k.join, static_cast<unsigned>(2 * sm_count), kJoinThreads, sizeof(JoinShared), stream, args);
 }
 
 cudaError_t kv4_attend_setup() {
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<true>),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttendSmem));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<false>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(AttendSmem));
-  return e;
+  const AttKernels all[4] = {att_kernels<16, false>(), att_kernels<16, true>(), att_kernels<32, false>(),
+                             att_kernels<32, true>()};
+  for (const AttKernels& k : all) {
+    cudaError_t e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k.join);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-int64_t kv4_attend_workspace(int, int, int, int) { return 16; }
+int64_t kv4_attend_workspace(int, int q_len, int H, int sm_count) {
+  const int64_t slot = q_len * H <= 16 ? att_slot_floats<16>() : att_slot_floats<32>();
+  return 2 * sm_count * slot * 4;
+}
 
 cudaError_t device_status_kv4_attend(unsigned int* value, bool reset) { return read_device_status(value, reset); }
 

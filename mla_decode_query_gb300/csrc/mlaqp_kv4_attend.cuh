@@ -1,0 +1,304 @@
+// MLA decode attention over the paged 4-bit latent cache on the tcgen05
+// tensor cores of sm_103a.
+//
+// Mathematics.  A cached token t has E2M1 codes c with block scales
+// 2^(s_j-127).  With s_t the largest of its 16 scale bytes,
+//   latent[t,n] = K8[t,n] * 2^(s_t-133),   K8 = code * 2^(s_j-s_t+6)
+// and K8 is exact in E4M3 while s_t - s_j <= 14 (below that it rounds, at
+// 2^-16 of the token's largest step).  So one 8-bit tile K8 [tokens][512]
+// serves both products:
+//   scores  D[t,r]  = sum_n K8[t,n] * Q8[r,n]         A = K8, rows = tokens
+//   output  O[n,r] += sum_t K8[t,n] * P8[t,r]         A = K8 transposed
+// with the 16 or 32 query rows r = (query token, head) on the narrow N side
+// of the MMA (swap-AB), and the token's scale folded into a number per (t,r)
+// in registers:
+//   y = (D * 2^(s_t-133) + Dr) * C_r + (s_t-133)      log2 units
+//   P = 2^(y - M_r + 12)     l_r += P * 2^(133-s_t)   M_r the running maximum
+//   x[r,n] = O[n,r] / l_r    lse_r = ln l_r + (M_r-12) ln 2
+// Dr is the rope part, a BF16 product of its own; C_r holds the softmax
+// scale, log2 e and the row's power of two.
+//
+// 8-bit operands without loss of the inputs' precision:
+//   Q   BF16 rows are scaled to a maximum in [128,256) and split into two
+//       E4M3 terms hi + lo/16: a BF16 significand has 8 bits, two terms of 4
+//       hold it, elements below 2^-20 of the row's maximum lose their tail.
+//       E4M3 queries are used as they are.  The terms are extra N rows.
+//   P   FP16 (11 bits), cut into three E5M2 terms, again extra N rows: 9
+//       bits or more down to 2^-20 of the maximum, and absolute steps of 2^-28
+//       below, so that 2^17 tokens far below the maximum still add up.
+// The MMAs cost what the A tile's reads from shared memory cost, so the
+// extra rows are free.
+//
+// Work split.  The sequences' 128-token tiles form one line; CTA c of the
+// grid (one per SM) takes an equal stretch of it, whatever the lengths.  A
+// stretch that holds a whole sequence writes x; the others leave (O, M, l)
+// in the workspace and the join kernel adds the pieces in order.
+//
+// A CTA is a pipeline of warps:
+//   warp 12      copies pages into shared memory (bulk copies: codes and
+//                scales in units of 32 tokens, rope rows straight into the
+//                swizzled tile, the cache's layout being that of the tile);
+//   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
+//                the eight values of their block's scale;
+//   warp 13      one thread issues the MMAs;
+//   warps 0-3    queries, softmax (one token per thread), rescaling, output.
+// O stays in tensor memory; it is rescaled only when a row's maximum has
+// grown by more than 2^3.
+#pragma once
+
+#include "mlaqp_kernel_large.cuh"
+#include "mlaqp_kv4.cuh"
+#include "mlaqp_kv4_launch.h"
+
+namespace mlaqp {
+
+constexpr int kAttThreads = 448;
+constexpr int kAttSoftWarps = 4;
+constexpr int kAttDequantWarps = 8;
+constexpr int kAttLoadWarp = 12;
+constexpr int kAttMmaWarp = 13;
+constexpr int kAttTile = 128;   // tokens per tile (MMA M of the scores)
+constexpr int kAttUnit = 32;    // tokens per copy unit
+constexpr int kAttUnits = kAttTile / kAttUnit;
+constexpr int kAttMaxSeqs = 256;  // sequences x row groups of a call
+constexpr float kAttSlack = 3.f;  // log2 growth of the maximum that is let pass
+constexpr float kAttShift = 12.f; // 2^(12+3) stays inside E5M2 and FP16
+
+constexpr int kUnitCodes = kAttUnit * kKv4CodeBytes;
+constexpr int kUnitBytes = kUnitCodes + kAttUnit * kKv4Blocks;
+constexpr int kRopeTile = kAttTile * kKv4RopeBytes;
+constexpr int kK8Block = kAttTile * 128;  // 128 latents of a tile
+constexpr int kK8Tile = 4 * kK8Block;
+
+// What follows from the lengths, and the mark that a wait ran out.
+struct AttSchedule {
+  int prefix[kAttMaxSeqs + 1];  // tiles before each row group
+  int len[kAttMaxSeqs];
+  int seq[kAttMaxSeqs];
+  int scan[8];
+  int fail;
+};
+
+template <int R>
+struct AttShared : AttSchedule {
+  uint32_t tmem;
+  alignas(8) uint32_t lut[32][2];           // E4M3 of the 8 magnitudes * 2^(6-k)
+  alignas(16) float wmax[2][kAttSoftWarps][R];
+  alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12 (-12: nothing seen yet)
+  alignas(16) float alpha[kAttSoftWarps][R];
+  float lsum[kAttSoftWarps][R];
+  // of the row group at hand and the next one, by turns
+  alignas(16) float cr[2][R];               // C_r
+  int limit[2][R];                          // visible tokens of a row
+  alignas(8) int64_t xoff[2][R];            // its place in x, -1: padding
+  int lseoff[2][R];
+  alignas(4) uint8_t smax[2][kAttTile];     // s_t per K8 buffer
+  uint8_t umask[8];                         // copied 16-token halves of a copy unit
+  alignas(4) uint8_t tmask[2][kAttUnits];
+  alignas(8) uint64_t bars[40];
+};
+
+// Shared memory and tensor memory of a variant: R query rows, E4M3 or BF16
+// queries.  RopeBufs / Units fill what the K8 tiles, queries and P leave.
+template <int R, bool E4>
+struct AttPlan {
+  static constexpr int QTerms = E4 ? 1 : 2;
+  static constexpr int NQ = QTerms * R;            // N of the score MMA
+  static constexpr int NP = 3 * R;                 // N of the output MMA
+  static constexpr int SCols = NQ + R;             // scores + rope part
+  static constexpr int SBufs = (R == 32 && !E4) ? 1 : 2;
+  static constexpr int OCol = SBufs * SCols;
+  static constexpr int RopeBufs = (R == 32 && !E4) ? 1 : 2;
+  static constexpr int Units = R == 16 ? (E4 ? 5 : 4) : 3;
+  static constexpr int K8 = 0;
+  static constexpr int Rope = K8 + 2 * kK8Tile;
+  static constexpr int Q = Rope + RopeBufs * kRopeTile;
+  static constexpr int QBlock = NQ * 128;          // 128 latents of the queries
+  static constexpr int QPe = Q + 4 * QBlock;
+  static constexpr int P = QPe + R * 128;
+  static constexpr int PChunk = 16 * kAttTile;     // 16 rows of P
+  static constexpr int Raw = P + NP / 16 * PChunk;
+  static constexpr int Misc = Raw + Units * kUnitBytes;
+  static constexpr int Bytes = Misc + static_cast<int>(sizeof(AttShared<R>)) + 1024;
+  static_assert(OCol + 4 * NP <= 512, "tensor memory");
+  static_assert(Bytes <= 232448, "shared memory");
+  // barrier indexes
+  static constexpr int RawFull = 0, RawEmpty = RawFull + Units, RopeFull = RawEmpty + Units,
+                       RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,
+                       SFull = K8Empty + 2, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
+                       QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, Soft = Drain + 1,
+                       BarCount = Soft + 1;
+  static_assert(BarCount <= 40, "barriers");
+};
+
+// Instruction descriptor: FP32 accumulator, operand formats and majors.
+__host__ __device__ constexpr uint32_t att_idesc(int m, int n, int afmt, int bfmt, bool a_mn, bool b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(afmt) << 7) | (static_cast<uint32_t>(bfmt) << 10) |
+         (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+constexpr int kFmtE4M3 = 0, kFmtE5M2 = 1, kFmtBf16 = 1;
+
+// Descriptor of an unswizzled operand (bits 61..63 = 0).
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define MLAQP_R16(r, o)                                                                                               \
+  "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]),        \
+      "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),              \
+      "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
+
+// 16 columns each from two or three places of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld2x16(uint32_t a, uint32_t b, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : MLAQP_R16(r, 0), MLAQP_R16(r, 16)
+      : "r"(a), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld3x16(uint32_t a, uint32_t b, uint32_t c, uint32_t (&r)[48]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%49];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%50];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : MLAQP_R16(r, 0), MLAQP_R16(r, 16), MLAQP_R16(r, 32)
+      : "r"(a), "r"(b), "r"(c)
+      : "memory");
+}
+#undef MLAQP_R16
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Largest value of the warp; NaNs are left out.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Everything that follows from the lengths: the tiles of each row group and
+// the stretch of this CTA.  All kAttThreads (or more than 256) threads call.
+__device__ __forceinline__ int att_schedule(const Kv4AttendParams& p, int R, AttSchedule& s, bool tell) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int groups = (p.q_len * p.H + R - 1) / R;
+  const int V = p.B * groups;
+  int tiles = 0;
+  if (tid < kAttMaxSeqs) {
+    int len = 0, seq = -1;
+    if (tid < V) {
+      const int b = tid / groups, g = tid % groups;
+      seq = p.seqs ? p.seqs[b] : b;
+      bool bad = seq < 0 || seq >= p.num_seqs;
+      if (!bad) {
+        len = p.seq_lens[seq];
+        // a sequence holds a page once, so the pool bounds its length too
+        bad = len < 0 || len > p.table_stride << p.cache.shift || len > p.cache.num_pages << p.cache.shift;
+      }
+      if (bad) {
+        if (tell) atomicOr(&g_device_status, kDevStatusBadIndex);
+        len = 0;
+      }
+      // the group's last row sees the most
+      const int last = min(g * R + R, p.q_len * p.H) - 1;
+      const int seen = max(0, len - (p.q_len - 1 - last / p.H));
+      tiles = static_cast<int>((static_cast<int64_t>(seen) + kAttTile - 1) / kAttTile);
+    }
+    s.len[tid] = len;
+    s.seq[tid] = seq;
+    int inc = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) s.scan[warp] = inc;
+    tiles = inc;
+  }
+  __syncthreads();
+  if (tid < kAttMaxSeqs) {
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s.scan[w];
+    s.prefix[tid + 1] = before + tiles;
+    if (tid == 0) s.prefix[0] = 0;
+  }
+  __syncthreads();
+  return V;
+}
+
+// CTAs that get tiles, one or more each.
+__device__ __forceinline__ int att_active(int total, int grid) { return min(total, grid); }
+
+// First tile of CTA c of n (c = n: the end).
+__device__ __forceinline__ int att_begin(int total, int c, int n) {
+  return static_cast<int>(static_cast<int64_t>(total) * c / n);
+}
+
+// The CTA whose stretch holds tile t.
+__device__ __forceinline__ int att_owner(int total, int t, int n) {
+  int c = static_cast<int>(static_cast<int64_t>(t) * n / total);
+  while (c + 1 < n && att_begin(total, c + 1, n) <= t) ++c;
+  while (c > 0 && att_begin(total, c, n) > t) --c;
+  return c;
+}
+
+// The row group that holds tile t.
+__device__ __forceinline__ int att_find(const int* prefix, int V, int t) {
+  int lo = 0, hi = V;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Workspace: slot 2c for the piece that begins CTA c's stretch, 2c+1 for one
+// that begins inside it; R rows of 512 sums, then M and l of each row.
+template <int R>
+__host__ __device__ constexpr int64_t att_slot_floats() { return R * (kLatent + 2); }
+
+}  // namespace mlaqp
