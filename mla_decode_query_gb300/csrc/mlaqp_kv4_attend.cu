@@ -145,45 +145,62 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
   const int j = lane & 15;
   const bool low = lane < 16;
   const int first_half = (j >> 2) & 1;
-  int u = 0;
+  // The next unit's codes are fetched while this one's are looked up.
+  struct Unit {
+    uint4 w[2];
+    uint32_t sc[2];
+    uint32_t mask;
+  };
+  auto fetch = [&](int u, Unit& x) -> bool {
+    const int st = u % L::Units;
+    if (!att_wait(bars + 8 * (L::RawFull + st), (u / L::Units) & 1, s)) return false;
+    const uint8_t* raw = smem + L::Raw + st * kUnitBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tok = 4 * dw + 2 * i + (lane >> 4);
+      x.w[i] = *reinterpret_cast<const uint4*>(raw + tok * kKv4CodeBytes + 16 * j);
+      x.sc[i] = raw[kUnitCodes + tok * kKv4Blocks + j];
+    }
+    x.mask = s.umask[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+    return true;
+  };
+  Unit cur;
+  if (!fetch(0, cur)) return;
+  const int units = tiles * kAttUnits;
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
     if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b), (k / 2 - 1) & 1, s)) return;
     uint8_t* tile = smem + L::K8 + b * kK8Tile + (j >> 2) * kK8Block;
-    for (int q = 0; q < kAttUnits; ++q, ++u) {
-      const int st = u % L::Units;
-      if (!att_wait(bars + 8 * (L::RawFull + st), (u / L::Units) & 1, s)) return;
-      const uint8_t* raw = smem + L::Raw + st * kUnitBytes;
-      uint4 w[2];
-      uint32_t sc[2];
+    for (int q = 0; q < kAttUnits; ++q) {
+      const Unit x = cur;
+      const int u = k * kAttUnits + q + 1;
+      if (u < units && !fetch(u, cur)) return;
+      if (dw == 0 && lane == 0) s.tmask[b][q] = static_cast<uint8_t>(x.mask);
+      uint32_t sv[2], sm[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tok = 4 * dw + 2 * i + (lane >> 4);
-        w[i] = *reinterpret_cast<const uint4*>(raw + tok * kKv4CodeBytes + 16 * j);
-        sc[i] = raw[kUnitCodes + tok * kKv4Blocks + j];
+        sv[i] = kv4_scale_clamp(x.sc[i]);
+        const uint32_t m0 = __reduce_max_sync(0xffffffffu, low ? sv[i] : 0u);
+        const uint32_t m1 = __reduce_max_sync(0xffffffffu, low ? 0u : sv[i]);
+        sm[i] = low ? m0 : m1;
       }
-      if (dw == 0 && lane == 0) s.tmask[b][q] = s.umask[st];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = kAttUnit * q + 4 * dw + 2 * i + (lane >> 4);
-        const uint32_t sv = kv4_scale_clamp(sc[i]);
-        const uint32_t m0 = __reduce_max_sync(0xffffffffu, low ? sv : 0u);
-        const uint32_t m1 = __reduce_max_sync(0xffffffffu, low ? 0u : sv);
-        const uint32_t sm = low ? m0 : m1;
-        if (j == 0) s.smax[b][row] = static_cast<uint8_t>(sm);
-        const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[min(sm - sv, 31u)]);
-        auto word = [&](uint32_t x, uint32_t& lo, uint32_t& hi) {
-          const uint32_t m = x & 0x77777777u;
-          lo = prmt(lut.x, lut.y, m) | (x & 0x80808080u);
-          hi = prmt(lut.x, lut.y, m >> 16) | ((x << 4) & 0x80808080u);
+        if (j == 0) s.smax[b][row] = static_cast<uint8_t>(sm[i]);
+        const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[min(sm[i] - sv[i], 31u)]);
+        auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
+          const uint32_t m = c & 0x77777777u;
+          lo = prmt(lut.x, lut.y, m) | (c & 0x80808080u);
+          hi = prmt(lut.x, lut.y, m >> 16) | ((c << 4) & 0x80808080u);
         };
         uint4 a, c;
-        word(w[i].x, a.x, a.y);
-        word(w[i].y, a.z, a.w);
-        word(w[i].z, c.x, c.y);
-        word(w[i].w, c.z, c.w);
+        word(x.w[i].x, a.x, a.y);
+        word(x.w[i].y, a.z, a.w);
+        word(x.w[i].z, c.x, c.y);
+        word(x.w[i].w, c.z, c.w);
         const int at = 2 * (j & 3);
         *reinterpret_cast<uint4*>(tile + row * 128 + (((at + first_half) ^ (row & 7)) << 4)) = a;
         *reinterpret_cast<uint4*>(tile + row * 128 + (((at + (first_half ^ 1)) ^ (row & 7)) << 4)) = c;
@@ -196,59 +213,40 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
 }
 
 // --------------------------------------------------------------------------
-// Warp 13: one thread issues the MMAs.  The scores of tile k+1 go ahead of
-// the output product of tile k, so the tensor cores work while the softmax
-// warps do.
+// Warps 13 and 14: one thread each issues the MMAs of the scores and of the
+// output.  Two threads, because each product has to go as soon as its
+// operands are there: with one thread in program order, the output product
+// that frees a K8 tile waited behind the scores of the next one, and the
+// pipeline took 5500 cycles a tile.
 // --------------------------------------------------------------------------
+
+// What was issued completes before the CTA ends (bar: the warp's own).
+__device__ __forceinline__ void att_drain(uint32_t bar) {
+  umma_commit(bar);
+  const unsigned long long at = globaltimer_ns();
+  while (!mbar_try_wait(bar, 0) && globaltimer_ns() - at < kAttWaitNs) {
+  }
+}
+
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V, int t0,
-                                        int t1) {
+__device__ __forceinline__ void att_mma_scores(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
+                                               int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
   constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
-  constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
   bool ok = true;
-  // output product of tile k; first: it begins row group number `item`
-  auto output = [&](int k, bool first, int item) {
-    ok = att_wait_one(bars + 8 * L::PFull, k & 1, s);
-    if (ok && first && item > 0) ok = att_wait_one(bars + 8 * L::OEmpty, (item - 1) & 1, s);
-    if (!ok) return;
-    tc_fence_after();
-    const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int ks = 0; ks < kAttTile / 32; ++ks) {
-        // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
-        const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
-        // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
-        const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
-        umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (first && ks == 0) ? 0u : 1u);
-      }
-    umma_commit(bars + 8 * (L::K8Empty + (k & 1)));
-    umma_commit(bars + 8 * L::PvDone);
-  };
-  int k = 0, item = 0, last_item = 0;
-  bool last_first = false;
+  int k = 0, item = 0;
   for (int t = t0; ok && t < t1; ++item) {
     const AttItem it = att_item(s.prefix, V, t, t1);
     t += it.count;
     ok = att_wait_one(bars + 8 * L::QFull, item & 1, s);
     for (int n = 0; ok && n < it.count; ++n, ++k) {
       const int b = k & 1, rb = k % L::RopeBufs, sb = k % L::SBufs;
-      ok = att_wait_one(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
-      if (ok) ok = att_wait_one(bars + 8 * (L::K8Full + b), (k / 2) & 1, s);
-      if (ok && k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
+      if (k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
+      if (ok) ok = att_wait_one(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + sb * L::SCols;
-      const uint32_t k8 = smem + L::K8 + b * kK8Tile;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint64_t ad = smem_desc_sw128(k8 + (c >> 2) * kK8Block + (c & 3) * 32, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(smem + L::Q + (c >> 2) * L::QBlock + (c & 3) * 32, 16, 1024);
-        umma_f8(d, ad, bd, id_s, c > 0);
-      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint64_t ad = smem_desc_sw128(smem + L::Rope + rb * kRopeTile + c * 32, 16, 1024);
@@ -256,19 +254,53 @@ __device__ __forceinline__ void att_mma(AttShared<R>& s, uint32_t smem, uint32_t
         umma_bf16(d + L::NQ, ad, bd, id_r, c > 0);
       }
       umma_commit(bars + 8 * (L::RopeEmpty + rb));
+      ok = att_wait_one(bars + 8 * (L::K8Full + b), (k / 2) & 1, s);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t k8 = smem + L::K8 + b * kK8Tile;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const uint64_t ad = smem_desc_sw128(k8 + (c >> 2) * kK8Block + (c & 3) * 32, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(smem + L::Q + (c >> 2) * L::QBlock + (c & 3) * 32, 16, 1024);
+        umma_f8(d, ad, bd, id_s, c > 0);
+      }
       umma_commit(bars + 8 * (L::SFull + sb));
-      if (k > 0) output(k - 1, last_first, last_item);
-      last_first = n == 0;
-      last_item = item;
     }
   }
-  if (ok && k > 0) output(k - 1, last_first, last_item);
-  if (!ok) {  // what was issued completes before the CTA ends
-    umma_commit(bars + 8 * L::Drain);
-    const unsigned long long at = globaltimer_ns();
-    while (!mbar_try_wait(bars + 8 * L::Drain, 0) && globaltimer_ns() - at < kAttWaitNs) {
+  if (!ok) att_drain(bars + 8 * L::Drain);
+}
+
+template <int R, bool E4>
+__device__ __forceinline__ void att_mma_output(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
+                                               int t0, int t1) {
+  using L = AttPlan<R, E4>;
+  constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
+  bool ok = true;
+  int k = 0, item = 0;
+  for (int t = t0; ok && t < t1; ++item) {
+    const AttItem it = att_item(s.prefix, V, t, t1);
+    t += it.count;
+    if (item > 0) ok = att_wait_one(bars + 8 * L::OEmpty, (item - 1) & 1, s);
+    for (int n = 0; ok && n < it.count; ++n, ++k) {
+      ok = att_wait_one(bars + 8 * L::PFull, k & 1, s);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < kAttTile / 32; ++ks) {
+          // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
+          const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
+          // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
+          const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
+          umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (n == 0 && ks == 0) ? 0u : 1u);
+        }
+      umma_commit(bars + 8 * (L::K8Empty + (k & 1)));
+      umma_commit(bars + 8 * L::PvDone);
     }
   }
+  if (!ok) att_drain(bars + 8 * (L::Drain + 1));
 }
 
 // --------------------------------------------------------------------------
@@ -659,7 +691,8 @@ template <int R, bool E4>
 __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
   using L = AttPlan<R, E4>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // by an offset, so that the compiler still sees shared memory
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   AttShared<R>& s = *reinterpret_cast<AttShared<R>*>(smem + L::Misc);
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t bars = smem_u32(s.bars);
@@ -679,7 +712,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     if (tid == 0) s.fail = 0;
   }
   pdl_wait();
-  if (warp == kAttMmaWarp) tmem_alloc(smem_u32(&s.tmem), 512);
+  if (warp == kAttScoreWarp) tmem_alloc(smem_u32(&s.tmem), 512);
   const int V = att_schedule(p, R, s, blockIdx.x == 0);
   tc_fence_before();
   __syncthreads();
@@ -691,6 +724,15 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   const bool mine = static_cast<int>(blockIdx.x) < active;
   const int t0 = mine ? att_begin(total, blockIdx.x, active) : 0, t1 = mine ? att_begin(total, blockIdx.x + 1, active) : 0;
   const uint32_t base = smem_u32(smem);
+  // Registers of the four warpgroups (128 at launch): softmax, codes twice,
+  // copies and MMAs.
+  if (warp < kAttSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  } else if (warp < kAttLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  }
   if (warp < kAttSoftWarps) {
     att_empty_rows<R>(p, s, V);
     if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, V, t0, t1);
@@ -699,15 +741,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
       att_dequant<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, V, t0, t1);
-    } else if ((tid & 31) == 0) {
-      att_mma<R, E4>(s, base, bars, tmem, V, t0, t1);
+    } else if (warp == kAttScoreWarp) {
+      if ((tid & 31) == 0) att_mma_scores<R, E4>(s, base, bars, tmem, V, t0, t1);
+    } else if (warp == kAttOutputWarp) {
+      if ((tid & 31) == 0) att_mma_output<R, E4>(s, base, bars, tmem, V, t0, t1);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   __syncwarp();
-  if (warp == kAttMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kAttScoreWarp) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------------

@@ -40,7 +40,7 @@
 //                swizzled tile, the cache's layout being that of the tile);
 //   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
-//   warp 13      one thread issues the MMAs;
+//   warps 13, 14 one thread each issues the MMAs of scores and output;
 //   warps 0-3    queries, softmax (one token per thread), rescaling, output.
 // O stays in tensor memory; it is rescaled only when a row's maximum has
 // grown by more than 2^3.
@@ -52,11 +52,12 @@
 
 namespace mlaqp {
 
-constexpr int kAttThreads = 448;
+constexpr int kAttThreads = 512;
 constexpr int kAttSoftWarps = 4;
 constexpr int kAttDequantWarps = 8;
 constexpr int kAttLoadWarp = 12;
-constexpr int kAttMmaWarp = 13;
+constexpr int kAttScoreWarp = 13;
+constexpr int kAttOutputWarp = 14;
 constexpr int kAttTile = 128;   // tokens per tile (MMA M of the scores)
 constexpr int kAttUnit = 32;    // tokens per copy unit
 constexpr int kAttUnits = kAttTile / kAttUnit;
@@ -126,7 +127,7 @@ struct AttPlan {
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, RopeFull = RawEmpty + Units,
                        RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,
                        SFull = K8Empty + 2, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
-                       QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, Soft = Drain + 1,
+                       QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, Soft = Drain + 2,
                        BarCount = Soft + 1;
   static_assert(BarCount <= 40, "barriers");
 };

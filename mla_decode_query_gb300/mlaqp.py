@@ -120,6 +120,8 @@ def header_functions(header: Path | None = None) -> list[str]:
 def load_library(path: Path | str | None = None) -> ctypes.CDLL:
     """Load ``libmlaqp.so`` once and attach the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -138,19 +140,38 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
 
 
 def _ptr(x) -> int | None:
-    if x is None:
-        return None
+    if x is None or type(x) is int:
+        return x
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     raise TypeError(f"expected a tensor, an int address or None, got {type(x)!r}")
+
+
+_current_stream = None
+
+
+def _find_current_stream():
+    """The handle of PyTorch's current stream.  Building the Stream object that
+    torch.cuda.current_stream() returns takes 2.8 us (on the Arm host of a
+    GB300), longer than a launch; the raw handle takes 0.2 us."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = torch.cuda.current_device
+    if raw is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_current_stream or _find_current_stream())()
     if isinstance(stream, int):
         return stream
     if hasattr(stream, "cuda_stream"):
