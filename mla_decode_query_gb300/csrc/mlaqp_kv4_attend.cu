@@ -15,17 +15,19 @@ constexpr unsigned long long kAttWaitNs = 1000000000ull;
 // Bounded wait of one thread; gives up early once another one has.
 __device__ __forceinline__ bool att_wait_one(uint32_t bar, uint32_t parity, AttSchedule& s) {
   if (mbar_try_wait(bar, parity)) return true;
+  // (kept short: it is inlined some thirty times, and a larger kernel than
+  // the instruction caches hold runs at half the speed)
   const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<volatile int*>(&s.fail)) return false;
-    if (globaltimer_ns() - t0 > kAttWaitNs) {
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    const bool late = globaltimer_ns() - t0 > kAttWaitNs;
+    if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
+    if (late || *reinterpret_cast<volatile int*>(&s.fail)) {
       *reinterpret_cast<volatile int*>(&s.fail) = 1;
-      atomicOr(&g_device_status, kDevStatusWaitTimeout);
       return false;
     }
   }
+  return true;
 }
 
 // The same for a whole warp, with one answer for all its lanes.
@@ -48,6 +50,19 @@ __device__ __forceinline__ AttItem att_item(const int* prefix, int V, int t, int
   return it;
 }
 
+// Position in a ring of N buffers and the parity of its barriers' phase.
+template <int N>
+struct AttRing {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // --------------------------------------------------------------------------
 // Warp 12: pages into shared memory.
 // --------------------------------------------------------------------------
@@ -56,154 +71,212 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, AttShared<R>&
                                          int t0, int t1) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31;
-  const int shift = p.cache.shift, page = 1 << shift;
+  const int shift = p.cache.shift;
   const int entries = kAttTile >> shift;  // pages of a tile
-  const int per_unit = shift < 5 ? 2 : 1;
-  const uint32_t unit_tok = min(page, kAttUnit);
+  const int groups = (p.q_len * p.H + R - 1) / R;
 
+  // A unit of 32 tokens lies in one page, or in two of 16 tokens.  Lanes
+  // 0..2 (and 3..5 for the second page) copy its codes, scales and rope rows
+  // with one instruction; what a lane copies differs from unit to unit by
+  // constants only.
+  const int parts = shift < 5 ? 2 : 1;
+  const int tok = kAttUnit / parts;  // tokens of a part
+  const int what = lane % 3, part = lane / 3;
+  const bool copies = lane < 3 * parts;
+  const uint32_t row_bytes = what == 0 ? kKv4CodeBytes : (what == 1 ? kKv4Blocks : kKv4RopeBytes);
+  const uint32_t plane = what == 0 ? 0u : (what == 1 ? kv4_scale_off(0, shift) : kv4_rope_off(0, shift));
+  const uint32_t bytes = tok * row_bytes;
+  const uint32_t to = smem + part * bytes + (what == 0 ? L::Raw : (what == 1 ? L::Raw + kUnitCodes : L::Rope));
+
+  // Table entry of page `lane` of tile t, as loaded: judged when it is used,
+  // a tile later, so that the load's latency is not waited for.
   int v = att_find(s.prefix, V, t0);
-  // page of entry `lane` of tile t, -1: none
-  auto fetch = [&](int t) -> int {
+  const int32_t* row = nullptr;
+  int row_of = -1;
+  auto fetch = [&](int t, bool& inside) -> int {
     while (t >= s.prefix[v + 1]) ++v;
+    if (v != row_of) {
+      row_of = v;
+      row = p.block_table + (p.seqs ? p.seqs[v / groups] : v / groups) * p.table_stride;
+    }
     const int64_t idx = (static_cast<int64_t>(t - s.prefix[v]) * kAttTile >> shift) + lane;
-    int id = -1;
-    if (lane < entries && idx << shift < s.len[v]) {
-      id = p.block_table[s.seq[v] * p.table_stride + idx];
-      if (id < 0 || id >= p.cache.num_pages) {
-        atomicOr(&g_device_status, kDevStatusBadIndex);
-        id = -1;
-      }
-    }
-    return id;
+    inside = lane < entries && idx << shift < s.len[v];
+    return inside ? row[idx] : -1;
   };
-  int next = fetch(t0);
+  bool inside = false;
+  int next = fetch(t0, inside);
   bool ok = true;
-  int k = 0, u = 0, rope = 0;
-  for (int t = t0; ok && t < t1; ++t, ++k) {
-    const int id = next;
-    if (t + 1 < t1) next = fetch(t + 1);
-    const uint8_t* base = p.cache.base + static_cast<int64_t>(max(id, 0)) * p.cache.page_stride;
-    auto load_rope = [&]() {
-      const int rb = k % L::RopeBufs;
-      if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rb), (k / L::RopeBufs - 1) & 1, s);
-      if (!ok) return;
-      const uint32_t bar = bars + 8 * (L::RopeFull + rb);
-      const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * page * kKv4RopeBytes);
-      __syncwarp();
-      if (id >= 0)
-        bulk_load_1d(smem + L::Rope + rb * kRopeTile + lane * page * kKv4RopeBytes, base + kv4_rope_off(0, shift),
-                     page * kKv4RopeBytes, bar);
-      ++rope;
-    };
-    if (L::RopeBufs == 2) load_rope();
-    for (int q = 0; ok && q < kAttUnits; ++q, ++u) {
-      const int st = u % L::Units;
-      if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + st), (u / L::Units - 1) & 1, s);
-      if (!ok) break;
-      const uint32_t bar = bars + 8 * (L::RawFull + st);
-      // lane e < per_unit copies the unit's e-th page part
-      const int entry = per_unit == 2 ? 2 * q + (lane & 1) : (q * kAttUnit) >> shift;
-      const int uid = __shfl_sync(0xffffffffu, id, entry);
-      const unsigned have = __ballot_sync(0xffffffffu, lane < per_unit && uid >= 0);
-      if (lane == 0) {
-        s.umask[st] = per_unit == 2 ? have : (have ? 3u : 0u);
-        mbar_arrive_expect_tx(bar, __popc(have) * unit_tok * (kKv4CodeBytes + kKv4Blocks));
-      }
-      __syncwarp();
-      if (lane < per_unit && uid >= 0) {
-        const uint8_t* from = p.cache.base + uid * p.cache.page_stride;
-        const uint32_t pos = (q * kAttUnit) & (page - 1);
-        const uint32_t dst = smem + L::Raw + st * kUnitBytes;
-        bulk_load_1d(dst + lane * unit_tok * kKv4CodeBytes, from + kv4_code_off(pos), unit_tok * kKv4CodeBytes, bar);
-        bulk_load_1d(dst + kUnitCodes + lane * unit_tok * kKv4Blocks, from + kv4_scale_off(pos, shift),
-                     unit_tok * kKv4Blocks, bar);
-      }
+  int k = 0, u = 0;
+  AttRing<L::Units> ring;
+  AttRing<L::RopeBufs> rope;
+  for (int t = t0; t < t1; ++t, ++k) {
+    int id = next;
+    if (inside && (id < 0 || id >= p.cache.num_pages)) {
+      atomicOr(&g_device_status, kDevStatusBadIndex);
+      id = -1;
     }
-    if (ok && L::RopeBufs == 1) load_rope();
+    if (t + 1 < t1) next = fetch(t + 1, inside);
+    const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+    const uint32_t rope_bar = bars + 8 * (L::RopeFull + rope.at);
+    if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rope.at), rope.parity ^ 1, s);
+    if (!ok) break;
+    if (lane == 0) {
+      // copied 16-token parts of the tile, a bit each
+      const int rep = 1 << (shift - 4);
+      uint32_t mask = 0;
+#pragma unroll 1
+      for (int e = 0; e < entries; ++e) mask |= (have >> e & 1) ? ((1u << rep) - 1u) << (e * rep) : 0u;
+      s.tmask[k % kAttMaskTiles] = mask;
+      mbar_arrive_expect_tx(rope_bar, __popc(have) * kKv4RopeBytes << shift);
+    }
+#pragma unroll 1
+    for (int q = 0; q < kAttUnits; ++q, ++u, ring.next()) {
+      const int entry = q * kAttUnit >> shift;  // the (first) page of the unit
+      const int uid = __shfl_sync(0xffffffffu, id, entry + (parts == 2 ? part & 1 : 0));
+      const uint8_t* from = p.cache.base + uid * p.cache.page_stride + plane +
+                            (static_cast<uint32_t>(q * kAttUnit) & ((1u << shift) - 1u)) * row_bytes;
+      const uint32_t bar = bars + 8 * (L::RawFull + ring.at);
+      const uint32_t dst = to + (what == 2 ? rope.at * kRopeTile + q * kAttUnit * kKv4RopeBytes : ring.at * kUnitBytes);
+      // the stage's fill before this one has been taken
+      if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1, s);
+      if (!ok) break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar, __popc(have >> entry & ((1u << parts) - 1u)) * tok * (kKv4CodeBytes + kKv4Blocks));
+      __syncwarp();
+      if (copies && uid >= 0) bulk_load_1d(dst, from, bytes, what == 2 ? rope_bar : bar);
+    }
+    if (!ok) break;
+    rope.next();
   }
   if (!ok) {  // copies in flight land before the CTA ends
     auto drain = [&](uint32_t bar, uint32_t parity) {
       const unsigned long long at = globaltimer_ns();
+#pragma unroll 1
       while (!mbar_try_wait(bar, parity) && globaltimer_ns() - at < kAttWaitNs) {
       }
     };
+#pragma unroll 1
     for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
-    for (int i = max(0, rope - L::RopeBufs); i < rope; ++i)
+#pragma unroll 1
+    for (int i = max(0, k + 1 - L::RopeBufs); i <= k; ++i)
       drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
   }
 }
 
 // --------------------------------------------------------------------------
+// Warp 15: scale bytes, one token per lane.  s_t = the largest of the 16;
+// s_t - s_j, at most 31, picks the row of the E4M3 table.  Bytes are taken as
+// pairs of 16-bit numbers; none of the differences borrows.
+// --------------------------------------------------------------------------
+template <int R, bool E4>
+__device__ __forceinline__ void att_scales(AttShared<R>& s, uint8_t* smem, uint32_t bars, int tiles) {
+  using L = AttPlan<R, E4>;
+  const int lane = threadIdx.x & 31;
+  AttRing<L::Units> ring;
+  for (int k = 0; k < tiles; ++k) {
+    const int kb = k % kAttScaleTiles;
+#pragma unroll 1
+    for (int q = 0; q < kAttUnits; ++q, ring.next()) {
+      const int st = ring.at;
+      if (!att_wait(bars + 8 * (L::RawFull + st), ring.parity, s)) return;
+      const uint4 x = *reinterpret_cast<const uint4*>(smem + L::Raw + st * kUnitBytes + kUnitCodes + lane * kKv4Blocks);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t e[4], o[4];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e[i] = w[i] & 0x00FF00FFu;
+        o[i] = (w[i] >> 8) & 0x00FF00FFu;
+        m = __vmaxu2(m, __vmaxu2(e[i], o[i]));
+      }
+      m = max(m & 0xFFFFu, m >> 16);
+      const uint32_t mm = m * 0x00010001u;
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = __vminu2(mm - e[i], 0x001F001Fu) | (__vminu2(mm - o[i], 0x001F001Fu) << 8);
+      *reinterpret_cast<uint4*>(&s.rel[st][lane * kKv4Blocks]) = make_uint4(r[0], r[1], r[2], r[3]);
+      s.smax[kb][kAttUnit * q + lane] = static_cast<uint8_t>(m);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (L::ScaleFull + st));
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
 // Warps 4-11: codes -> E4M3 tile.  A lane takes one block of 32 latents of
-// one token; half a warp a token.
+// one token, half a warp a token, a warp four tokens of each copy unit.
+// Bound by the ALU pipe (six operations a word of eight codes).
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
   const int j = lane & 15;
-  const bool low = lane < 16;
   const int first_half = (j >> 2) & 1;
+  const int tok0 = 4 * dw + (lane >> 4);  // and tok0 + 2
+  // places of the two 16-byte chunks of both tokens in a tile
+  uint32_t to[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = tok0 + 2 * i;
+      to[i][h] = (j >> 2) * kK8Block + row * 128 + (((2 * (j & 3) + (first_half ^ h)) ^ (row & 7)) << 4);
+    }
   // The next unit's codes are fetched while this one's are looked up.
   struct Unit {
     uint4 w[2];
-    uint32_t sc[2];
-    uint32_t mask;
+    uint32_t rel[2];
   };
-  auto fetch = [&](int u, Unit& x) -> bool {
-    const int st = u % L::Units;
-    if (!att_wait(bars + 8 * (L::RawFull + st), (u / L::Units) & 1, s)) return false;
-    const uint8_t* raw = smem + L::Raw + st * kUnitBytes;
+  AttRing<L::Units> ring;
+  auto fetch = [&](Unit& x) -> bool {
+    const int st = ring.at;
+    // the scale warp has seen the copies land
+    if (!att_wait(bars + 8 * (L::ScaleFull + st), ring.parity, s)) return false;
+    const uint8_t* raw = smem + L::Raw + st * kUnitBytes + tok0 * kKv4CodeBytes + 16 * j;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tok = 4 * dw + 2 * i + (lane >> 4);
-      x.w[i] = *reinterpret_cast<const uint4*>(raw + tok * kKv4CodeBytes + 16 * j);
-      x.sc[i] = raw[kUnitCodes + tok * kKv4Blocks + j];
+      x.rel[i] = s.rel[st][(tok0 + 2 * i) * kKv4Blocks + j];
+      x.w[i] = *reinterpret_cast<const uint4*>(raw + 2 * i * kKv4CodeBytes);
     }
-    x.mask = s.umask[st];
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+    ring.next();
     return true;
   };
-  Unit cur;
-  if (!fetch(0, cur)) return;
-  const int units = tiles * kAttUnits;
+  Unit cur, nxt;
+  uint2 lut[2];
+  if (!fetch(cur)) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
     if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b), (k / 2 - 1) & 1, s)) return;
-    uint8_t* tile = smem + L::K8 + b * kK8Tile + (j >> 2) * kK8Block;
+    uint8_t* tile = smem + L::K8 + b * kK8Tile;
+#pragma unroll 1
     for (int q = 0; q < kAttUnits; ++q) {
-      const Unit x = cur;
-      const int u = k * kAttUnits + q + 1;
-      if (u < units && !fetch(u, cur)) return;
-      if (dw == 0 && lane == 0) s.tmask[b][q] = static_cast<uint8_t>(x.mask);
-      uint32_t sv[2], sm[2];
+      const bool more = q + 1 < kAttUnits || k + 1 < tiles;
+      if (more && !fetch(nxt)) return;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        sv[i] = kv4_scale_clamp(x.sc[i]);
-        const uint32_t m0 = __reduce_max_sync(0xffffffffu, low ? sv[i] : 0u);
-        const uint32_t m1 = __reduce_max_sync(0xffffffffu, low ? 0u : sv[i]);
-        sm[i] = low ? m0 : m1;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = kAttUnit * q + 4 * dw + 2 * i + (lane >> 4);
-        if (j == 0) s.smax[b][row] = static_cast<uint8_t>(sm[i]);
-        const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[min(sm[i] - sv[i], 31u)]);
         auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
           const uint32_t m = c & 0x77777777u;
-          lo = prmt(lut.x, lut.y, m) | (c & 0x80808080u);
-          hi = prmt(lut.x, lut.y, m >> 16) | ((c << 4) & 0x80808080u);
+          lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
+          hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
         };
         uint4 a, c;
-        word(x.w[i].x, a.x, a.y);
-        word(x.w[i].y, a.z, a.w);
-        word(x.w[i].z, c.x, c.y);
-        word(x.w[i].w, c.z, c.w);
-        const int at = 2 * (j & 3);
-        *reinterpret_cast<uint4*>(tile + row * 128 + (((at + first_half) ^ (row & 7)) << 4)) = a;
-        *reinterpret_cast<uint4*>(tile + row * 128 + (((at + (first_half ^ 1)) ^ (row & 7)) << 4)) = c;
+        word(cur.w[i].x, a.x, a.y);
+        word(cur.w[i].y, a.z, a.w);
+        word(cur.w[i].z, c.x, c.y);
+        word(cur.w[i].w, c.z, c.w);
+        *reinterpret_cast<uint4*>(tile + to[i][0] + q * kAttUnit * 128) = a;
+        *reinterpret_cast<uint4*>(tile + to[i][1] + q * kAttUnit * 128) = c;
+      }
+      if (more) {
+        cur = nxt;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
       }
     }
     fence_proxy_async_smem();
@@ -258,7 +331,7 @@ __device__ __forceinline__ void att_mma_scores(AttShared<R>& s, uint32_t smem, u
       if (!ok) break;
       tc_fence_after();
       const uint32_t k8 = smem + L::K8 + b * kK8Tile;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < 16; ++c) {
         const uint64_t ad = smem_desc_sw128(k8 + (c >> 2) * kK8Block + (c & 3) * 32, 16, 1024);
         const uint64_t bd = smem_desc_sw128(smem + L::Q + (c >> 2) * L::QBlock + (c & 3) * 32, 16, 1024);
@@ -286,7 +359,7 @@ __device__ __forceinline__ void att_mma_output(AttShared<R>& s, uint32_t smem, u
       if (!ok) break;
       tc_fence_after();
       const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
-#pragma unroll
+#pragma unroll 1
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int ks = 0; ks < kAttTile / 32; ++ks) {
@@ -327,7 +400,7 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>
   float cr = p.softmax_scale * 1.4426950408889634f;
   if constexpr (E4) {
     const uint8_t* src = p.q + at;
-#pragma unroll
+#pragma unroll 1
     for (int c = sub; c < 36; c += TPR) {  // 16-byte chunks: 32 of latents, 4 of rope
       uint4 x = make_uint4(0, 0, 0, 0);
       if (real) x = ld_u128(src + 16 * c);
@@ -352,27 +425,20 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>
     }
     cr *= *p.q_scale;
   } else {
-    constexpr int N = 64 / TPR;  // 16-byte chunks (8 elements) of latents per thread
+    // Two passes over the row, the second from the caches: first its largest
+    // latent and rope element, then the terms.
     const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + at;
-    uint4 x[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) x[n] = real ? ld_u128(src + 8 * (n * TPR + sub)) : make_uint4(0, 0, 0, 0);
-    constexpr int NR = 8 / TPR;  // chunks of rope per thread
-    uint4 pe[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) pe[n] = real ? ld_u128(src + kLatent + 8 * (n * TPR + sub)) : make_uint4(0, 0, 0, 0);
     auto top = [](uint4 a) {
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-      uint32_t t = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t = max(t, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-      return t;
+      const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu), __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+      return max(m & 0xFFFFu, m >> 16);
     };
     uint32_t ml = 0, mp = 0;
-#pragma unroll
-    for (int n = 0; n < N; ++n) ml = max(ml, top(x[n]));
-#pragma unroll
-    for (int n = 0; n < NR; ++n) mp = max(mp, top(pe[n]));
+    if (real) {
+#pragma unroll 4
+      for (int c = sub; c < 64; c += TPR) ml = max(ml, top(ld_u128(src + 8 * c)));
+#pragma unroll 1
+      for (int c = sub; c < 8; c += TPR) mp = max(mp, top(ld_u128(src + kLatent + 8 * c)));
+    }
 #pragma unroll
     for (int d = 1; d < TPR; d <<= 1) {
       ml = max(ml, __shfl_xor_sync(0xffffffffu, ml, d));
@@ -380,40 +446,33 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>
     }
     // exponent of the row: its latents' largest, but not so far below the
     // rope part's that scaling that part would overflow
-    int e = static_cast<int>(ml >> 7);
-    e = max(max(e, static_cast<int>(mp >> 7) - 40), 8);
+    const int e = max(max(static_cast<int>(ml >> 7), static_cast<int>(mp >> 7) - 40), 8);
     const bool bad = ml >= 0x7F80u || mp >= 0x7F80u;  // NaN or infinity: the whole row
     const float f = bad ? __uint_as_float(0x7FC00000u) : exp2f(static_cast<float>(134 - e));
     cr *= exp2f(static_cast<float>(e - 134));
+#pragma unroll 1
+    for (int c = sub; c < 64; c += TPR) {  // elements 8c..8c+7: half of 16-byte E4M3 chunk c/2
+      const uint4 x = real ? ld_u128(src + 8 * c) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = n * TPR + sub;  // elements 8c..8c+7: half of 16-byte E4M3 chunk c/2
-      const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t hh = 0, ll = 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float a = bf16_lo(w[2 * g + q]) * f, c1 = bf16_hi(w[2 * g + q]) * f;
-          const uint32_t t8 = pack_e4m3x2(c1, a);
-          // the code back as a float: bits * 2^-120 in BF16, exact
-          const uint32_t back = mul_bf16x2(e4m3x2_to_bf16x2_scaled(t8), 0x7B807B80u);
-          const uint32_t l8 = pack_e4m3x2((c1 - bf16_hi(back)) * 16.f, (a - bf16_lo(back)) * 16.f);
-          hh |= t8 << (16 * q);
-          ll |= l8 << (16 * q);
-        }
-        hi[g] = hh;
-        lo[g] = ll;
+      for (int q = 0; q < 4; ++q) {
+        const float a = bf16_lo(w[q]) * f, c1 = bf16_hi(w[q]) * f;
+        const uint32_t t8 = pack_e4m3x2(c1, a);
+        // the code back as a float: bits * 2^-120 in BF16, exact
+        const uint32_t back = mul_bf16x2(e4m3x2_to_bf16x2_scaled(t8), 0x7B807B80u);
+        const uint32_t l8 = pack_e4m3x2((c1 - bf16_hi(back)) * 16.f, (a - bf16_lo(back)) * 16.f);
+        hi[q >> 1] |= t8 << (16 * (q & 1));
+        lo[q >> 1] |= l8 << (16 * (q & 1));
       }
       uint8_t* to = q8 + (c >> 4) * L::QBlock + ((((c >> 1) & 7) ^ (r & 7)) << 4) + 8 * (c & 1);
       *reinterpret_cast<uint2*>(to + r * 128) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(to + (R + r) * 128) = make_uint2(lo[0], lo[1]);
     }
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const int c = n * TPR + sub;
-      const uint32_t w[4] = {pe[n].x, pe[n].y, pe[n].z, pe[n].w};
+#pragma unroll 1
+    for (int c = sub; c < 8; c += TPR) {
+      const uint4 x = real ? ld_u128(src + kLatent + 8 * c) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       uint32_t o[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) o[g] = pack_bf16x2(bf16_hi(w[g]) * f, bf16_lo(w[g]) * f);
@@ -438,23 +497,17 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
   const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
   float* mref = s.mref[warp];
   float* alpha = s.alpha[warp];
-  // Barrier of the four warps, bounded like every wait.
-  uint32_t soft_phase = 0;
-  auto soft_barrier = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * L::Soft);
-    const bool ok = att_wait(bars + 8 * L::Soft, soft_phase & 1, s);
-    ++soft_phase;
-    return ok;
-  };
-  AttItem it = att_item(s.prefix, V, t0, t1);
-  att_query<R, E4>(p, s, smem, bars, it.v, 0);
+  // A wait that runs out (then all later ones do at once) does not end the
+  // warp here: it goes on with what is there, so that no other one is left
+  // alone at a barrier, and writes nothing.
+  // Row group -1 has no tiles: it only prepares the first one's queries.
+  AttItem it = {0, 0, 0};
   int k = 0;
-  for (int t = t0, item = 0; t < t1; ++item) {
+  for (int t = t0, item = -1; t < t1; ++item) {
     const int turn = item & 1;
     // every warp has left the row group before (what follows reuses its
-    // places), and the first one's rows are known
-    if (!soft_barrier()) return;
+    // places), and this one's rows are known
+    soft_barrier();
     const int next_t = t + it.count;
     AttItem next = it;
     if (next_t < t1) next = att_item(s.prefix, V, next_t, t1);
@@ -462,23 +515,25 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
     float l[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) l[r] = 0.f;
-    if (lane < R) mref[lane] = -kAttShift;
+    if (lane < R) mref[lane] = kAttUnseen;
     __syncwarp();
-    for (int n = 0; n < it.count; ++n, ++k) {
-      const int b = k & 1, sb = k % L::SBufs;
-      if (!att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s)) return;
-      if (!att_wait(bars + 8 * (L::K8Full + b), (k / 2) & 1, s)) return;  // smax and tmask are this tile's
-      tc_fence_after();
+    for (int n = item < 0 ? -1 : 0; n < it.count; ++n) {
+      const int kb = k % kAttScaleTiles, sb = k % L::SBufs;
+      if (n >= 0) att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s);
       // the scores of the row group's last tile are in: its queries are done with
       if (n == it.count - 1 && next_t < t1) att_query<R, E4>(p, s, smem, bars, next.v, turn ^ 1);
-      const uint32_t sm = s.smax[b][tid];
+      if (n < 0) continue;
+      att_wait(bars + 8 * (L::K8Full + (k & 1)), (k / 2) & 1, s);  // the tile's scales are in, too
+      tc_fence_after();
+      const uint32_t sm = s.smax[kb][tid];
       const float ts = sm == kKv4ScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((sm - 6u) << 23);
       const float its = __uint_as_float((260u - sm) << 23);
       const float et = static_cast<float>(static_cast<int>(sm) - 133);
       const int64_t tile_tok = static_cast<int64_t>(it.first + n) * kAttTile;
-      const bool whole = *reinterpret_cast<const uint32_t*>(s.tmask[b]) == 0x03030303u &&
+      const uint32_t mask = s.tmask[k % kAttMaskTiles];
+      const bool whole = mask == 0xFFu &&
                          tile_tok + kAttTile <= s.limit[turn][0];
-      const bool here = (s.tmask[b][warp] >> (lane >> 4)) & 1;
+      const bool here = mask >> (tid >> 4) & 1;
       float y[R];
 #pragma unroll
       for (int hb = 0; hb < R; hb += 16) {
@@ -512,23 +567,27 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
         for (int r = 0; r < R; ++r)
           if (!here || tile_tok + tid >= s.limit[turn][r]) y[r] = -INFINITY;
       }
-      float mine = -INFINITY;
+      // Has any row outgrown its reference?  Mostly not: then one barrier
+      // tells, and no maximum is taken.
+      bool grown = false;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float m = warp_max(y[r]);
-        if (lane == r) mine = m;
+      for (int r = 0; r < R; r += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&mref[r]);
+        grown |= y[r] > m.x + (kAttShift + kAttSlack);
+        grown |= y[r + 1] > m.y + (kAttShift + kAttSlack);
+        grown |= y[r + 2] > m.z + (kAttShift + kAttSlack);
+        grown |= y[r + 3] > m.w + (kAttShift + kAttSlack);
       }
-      if (lane < R) s.wmax[b][warp][lane] = mine;
-      if (!soft_barrier()) return;
-      bool up = false;
-      float tm = -INFINITY;
-      if (lane < R) {
-        tm = fmaxf(fmaxf(s.wmax[b][0][lane], s.wmax[b][1][lane]), fmaxf(s.wmax[b][2][lane], s.wmax[b][3][lane]));
-        up = tm > top + kAttSlack || (top == -INFINITY && tm > top);
-      }
-      if (__any_sync(0xffffffffu, up)) {
-        __syncwarp();
+      if (soft_barrier_any(grown || n == 0)) {
+#pragma unroll
+        for (int r = 0; r < R; r += 4) {
+          const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
+          if (lane == 0) *reinterpret_cast<float4*>(&s.wmax[warp][r]) = m;
+        }
+        soft_barrier();
         if (lane < R) {
+          const float tm = fmaxf(fmaxf(s.wmax[0][lane], s.wmax[1][lane]), fmaxf(s.wmax[2][lane], s.wmax[3][lane]));
+          const bool up = tm > top;
           alpha[lane] = up ? (top == -INFINITY ? 0.f : ex2(top - tm)) : 1.f;
           if (up) {
             top = tm;
@@ -545,8 +604,9 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
           l[r + 3] *= a.w;
         }
         if (n > 0) {
-          if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;
+          att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
           tc_fence_after();
+#pragma unroll 1
           for (int c = 0; c < 4 * L::NP; c += 16) {
             uint32_t o[16];
             tmem_ld16(tmem + lanes + L::OCol + c, o);
@@ -558,7 +618,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
           tmem_wait_st();
         }
       }
-      if (k > 0 && !att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;  // P is free
+      if (k > 0) att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);  // P is free
       uint8_t* ps = smem + L::P + tid * 16;
 #pragma unroll
       for (int hb = 0; hb < R; hb += 16) {
@@ -598,6 +658,11 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(bars + 8 * L::PFull);
+      ++k;
+    }
+    if (item < 0) {
+      it = next;
+      continue;
     }
 
     // The row group's end here: sums over the tokens, O from tensor memory.
@@ -612,7 +677,14 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
       if (lane == r) mine = v;
     }
     if (lane < R) s.lsum[warp][lane] = mine;
-    if (!soft_barrier()) return;
+    soft_barrier();
+    const bool done = att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
+    if (!done || *reinterpret_cast<volatile int*>(&s.fail)) {
+      t = next_t;
+      it = next;
+      continue;
+    }
+    tc_fence_after();
     float* part = nullptr;
     if (!complete) {
       const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
@@ -633,8 +705,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<
       }
     }
     __syncwarp();
-    if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) return;
-    tc_fence_after();
+#pragma unroll 1
     for (int mt = 0; mt < 4; ++mt) {
       const int col = mt * 128 + 32 * warp + lane;
 #pragma unroll
@@ -698,8 +769,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   const uint32_t bars = smem_u32(s.bars);
   if (tid < L::BarCount) {
     uint32_t count = 1;
-    if ((tid >= L::RawEmpty && tid < L::RopeFull) || tid == L::K8Full || tid == L::K8Full + 1) count = kAttDequantWarps;
-    if (tid == L::Soft) count = kAttSoftWarps;
+    if ((tid >= L::RawEmpty && tid < L::ScaleFull) || tid == L::K8Full || tid == L::K8Full + 1) count = kAttDequantWarps;
     if ((tid >= L::SEmpty && tid < L::PFull) || tid == L::PFull || tid == L::QFull || tid == L::OEmpty) count = 128;
     mbar_init(bars + 8 * tid, count);
     fence_barrier_init();
@@ -741,6 +811,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
       att_dequant<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, V, t0, t1);
+    } else if (warp == kAttScaleWarp) {
+      att_scales<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttScoreWarp) {
       if ((tid & 31) == 0) att_mma_scores<R, E4>(s, base, bars, tmem, V, t0, t1);
     } else if (warp == kAttOutputWarp) {

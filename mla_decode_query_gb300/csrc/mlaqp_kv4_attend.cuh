@@ -38,6 +38,7 @@
 //   warp 12      copies pages into shared memory (bulk copies: codes and
 //                scales in units of 32 tokens, rope rows straight into the
 //                swizzled tile, the cache's layout being that of the tile);
+//   warp 15      scale bytes -> s_t and s_t - s_j, a token per lane;
 //   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
 //   warps 13, 14 one thread each issues the MMAs of scores and output;
@@ -58,12 +59,21 @@ constexpr int kAttDequantWarps = 8;
 constexpr int kAttLoadWarp = 12;
 constexpr int kAttScoreWarp = 13;
 constexpr int kAttOutputWarp = 14;
+constexpr int kAttScaleWarp = 15;
 constexpr int kAttTile = 128;   // tokens per tile (MMA M of the scores)
 constexpr int kAttUnit = 32;    // tokens per copy unit
 constexpr int kAttUnits = kAttTile / kAttUnit;
+constexpr int kAttMaxUnits = 4;    // copy units in flight at most
+// Tiles whose scales are kept: the scale warp runs up to four units ahead of
+// the code warps, these up to two tiles ahead of the softmax.
+constexpr int kAttScaleTiles = 4;
+constexpr int kAttMaskTiles = 8;   // the same for what the copying warp notes, which is ahead of both
 constexpr int kAttMaxSeqs = 256;  // sequences x row groups of a call
 constexpr float kAttSlack = 3.f;  // log2 growth of the maximum that is let pass
 constexpr float kAttShift = 12.f; // 2^(12+3) stays inside E5M2 and FP16
+
+// Reference of a row that has seen no token: whatever it sees first is above.
+constexpr float kAttUnseen = -1e30f;
 
 constexpr int kUnitCodes = kAttUnit * kKv4CodeBytes;
 constexpr int kUnitBytes = kUnitCodes + kAttUnit * kKv4Blocks;
@@ -75,7 +85,6 @@ constexpr int kK8Tile = 4 * kK8Block;
 struct AttSchedule {
   int prefix[kAttMaxSeqs + 1];  // tiles before each row group
   int len[kAttMaxSeqs];
-  int seq[kAttMaxSeqs];
   int scan[8];
   int fail;
 };
@@ -84,8 +93,9 @@ template <int R>
 struct AttShared : AttSchedule {
   uint32_t tmem;
   alignas(8) uint32_t lut[32][2];           // E4M3 of the 8 magnitudes * 2^(6-k)
-  alignas(16) float wmax[2][kAttSoftWarps][R];
-  alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12 (-12: nothing seen yet)
+  alignas(16) uint8_t rel[kAttMaxUnits][kAttUnit * kKv4Blocks];  // s_t - s_j of a copy unit, at most 31
+  alignas(16) float wmax[kAttSoftWarps][R];
+  alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12, or kAttUnseen
   alignas(16) float alpha[kAttSoftWarps][R];
   float lsum[kAttSoftWarps][R];
   // of the row group at hand and the next one, by turns
@@ -93,9 +103,8 @@ struct AttShared : AttSchedule {
   int limit[2][R];                          // visible tokens of a row
   alignas(8) int64_t xoff[2][R];            // its place in x, -1: padding
   int lseoff[2][R];
-  alignas(4) uint8_t smax[2][kAttTile];     // s_t per K8 buffer
-  uint8_t umask[8];                         // copied 16-token halves of a copy unit
-  alignas(4) uint8_t tmask[2][kAttUnits];
+  uint8_t smax[kAttScaleTiles][kAttTile];   // s_t
+  uint32_t tmask[kAttMaskTiles];            // 16-token parts of a tile that were copied, a bit each
   alignas(8) uint64_t bars[40];
 };
 
@@ -110,7 +119,7 @@ struct AttPlan {
   static constexpr int SBufs = (R == 32 && !E4) ? 1 : 2;
   static constexpr int OCol = SBufs * SCols;
   static constexpr int RopeBufs = (R == 32 && !E4) ? 1 : 2;
-  static constexpr int Units = R == 16 ? (E4 ? 5 : 4) : 3;
+  static constexpr int Units = R == 16 ? 4 : 3;
   static constexpr int K8 = 0;
   static constexpr int Rope = K8 + 2 * kK8Tile;
   static constexpr int Q = Rope + RopeBufs * kRopeTile;
@@ -124,11 +133,11 @@ struct AttPlan {
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
   // barrier indexes
-  static constexpr int RawFull = 0, RawEmpty = RawFull + Units, RopeFull = RawEmpty + Units,
+  static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
+                       RopeFull = ScaleFull + Units,
                        RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,
                        SFull = K8Empty + 2, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
-                       QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, Soft = Drain + 2,
-                       BarCount = Soft + 1;
+                       QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, BarCount = Drain + 2;
   static_assert(BarCount <= 40, "barriers");
 };
 
@@ -209,6 +218,23 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
+// Barrier of the four softmax warps; the second form tells whether any thread
+// says yes.  Every one of these warps passes every barrier, also after a wait
+// has run out.
+__device__ __forceinline__ void soft_barrier() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_barrier_any(bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return any != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -230,10 +256,10 @@ __device__ __forceinline__ int att_schedule(const Kv4AttendParams& p, int R, Att
   const int V = p.B * groups;
   int tiles = 0;
   if (tid < kAttMaxSeqs) {
-    int len = 0, seq = -1;
+    int len = 0;
     if (tid < V) {
       const int b = tid / groups, g = tid % groups;
-      seq = p.seqs ? p.seqs[b] : b;
+      const int seq = p.seqs ? p.seqs[b] : b;
       bool bad = seq < 0 || seq >= p.num_seqs;
       if (!bad) {
         len = p.seq_lens[seq];
@@ -250,7 +276,6 @@ __device__ __forceinline__ int att_schedule(const Kv4AttendParams& p, int R, Att
       tiles = static_cast<int>((static_cast<int64_t>(seen) + kAttTile - 1) / kAttTile);
     }
     s.len[tid] = len;
-    s.seq[tid] = seq;
     int inc = tiles;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
