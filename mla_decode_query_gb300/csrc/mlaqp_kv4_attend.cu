@@ -64,89 +64,113 @@ struct AttRing {
 };
 
 // --------------------------------------------------------------------------
-// Warp 12: pages into shared memory.
+// Warp 20: pages into shared memory.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
-__device__ __forceinline__ void att_load(const Kv4AttendParams& p, AttShared<R>& s, uint32_t smem, uint32_t bars, int V,
+__device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, int V,
                                          int t0, int t1) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31;
   const int shift = p.cache.shift;
   const int entries = kAttTile >> shift;  // pages of a tile
   const int groups = (p.q_len * p.H + R - 1) / R;
+  const uint8_t* const cache = p.cache.base;
+  const int64_t page_stride = p.cache.page_stride;
+  const int num_pages = p.cache.num_pages;
 
-  // A unit of 32 tokens lies in one page, or in two of 16 tokens.  Lanes
-  // 0..2 (and 3..5 for the second page) copy its codes, scales and rope rows
-  // with one instruction; what a lane copies differs from unit to unit by
-  // constants only.
-  const int parts = shift < 5 ? 2 : 1;
-  const int tok = kAttUnit / parts;  // tokens of a part
-  const int what = lane % 3, part = lane / 3;
-  const bool copies = lane < 3 * parts;
-  const uint32_t row_bytes = what == 0 ? kKv4CodeBytes : (what == 1 ? kKv4Blocks : kKv4RopeBytes);
-  const uint32_t plane = what == 0 ? 0u : (what == 1 ? kv4_scale_off(0, shift) : kv4_rope_off(0, shift));
-  const uint32_t bytes = tok * row_bytes;
-  const uint32_t to = smem + part * bytes + (what == 0 ? L::Raw : (what == 1 ? L::Raw + kUnitCodes : L::Rope));
+  // A unit lies in one page or in several whole ones (parts).  Lane 2e copies
+  // the codes of its part e, lane 2e+1 the scales, all with one instruction;
+  // what a lane copies differs from unit to unit by constants only.
+  constexpr int kLog = L::Unit == 64 ? 6 : 5;
+  const int log_parts = max(kLog - shift, 0);
+  const int parts = 1 << log_parts;
+  const bool scales = lane & 1;
+  const int part = min(lane >> 1, parts - 1);
+  const bool copies = lane >> 1 < parts;
+  const uint32_t row_bytes = scales ? kKv4Blocks : kKv4CodeBytes;
+  const uint32_t bytes = row_bytes * (L::Unit >> log_parts);
+  const uint32_t plane = scales ? kv4_scale_off(0, shift) : 0u;
+  const uint32_t to = smem + L::Raw + part * bytes + (scales ? L::UnitCodes : 0);
+  const uint32_t unit_tx = (kKv4CodeBytes + kKv4Blocks) * L::Unit >> log_parts;
+  const uint32_t page_mask = (1u << shift) - 1u;
+  const uint32_t rope_plane = kv4_rope_off(0, shift), rope_bytes = kKv4RopeBytes << shift;
+  const unsigned tile_pages = (1u << entries) - 1u;
 
-  // Table entry of page `lane` of tile t, as loaded: judged when it is used,
-  // a tile later, so that the load's latency is not waited for.
-  int v = att_find(s.prefix, V, t0);
-  const int32_t* row = nullptr;
-  int row_of = -1;
-  auto fetch = [&](int t, bool& inside) -> int {
-    while (t >= s.prefix[v + 1]) ++v;
-    if (v != row_of) {
-      row_of = v;
-      row = p.block_table + (p.seqs ? p.seqs[v / groups] : v / groups) * p.table_stride;
-    }
-    const int64_t idx = (static_cast<int64_t>(t - s.prefix[v]) * kAttTile >> shift) + lane;
-    inside = lane < entries && idx << shift < s.len[v];
-    return inside ? row[idx] : -1;
-  };
-  bool inside = false;
-  int next = fetch(t0, inside);
   bool ok = true;
   int k = 0, u = 0;
   AttRing<L::Units> ring;
   AttRing<L::RopeBufs> rope;
-  for (int t = t0; t < t1; ++t, ++k) {
-    int id = next;
-    if (inside && (id < 0 || id >= p.cache.num_pages)) {
-      atomicOr(&g_device_status, kDevStatusBadIndex);
-      id = -1;
-    }
-    if (t + 1 < t1) next = fetch(t + 1, inside);
-    const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-    const uint32_t rope_bar = bars + 8 * (L::RopeFull + rope.at);
-    if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rope.at), rope.parity ^ 1, s);
-    if (!ok) break;
-    if (lane == 0) {
-      // copied 16-token parts of the tile, a bit each
-      const int rep = 1 << (shift - 4);
-      uint32_t mask = 0;
+  for (int t = t0; ok && t < t1;) {
+    const AttItem it = att_item(s.prefix, V, t, t1);
+    t += it.count;
+    // Each lane holds one entry of the table row and the page's address (0:
+    // no page); the entries after these are loaded long before their turn,
+    // so that a tile costs this warp, alone with its latencies, little.
+    const int32_t* row = p.block_table + (p.seqs ? p.seqs[it.v / groups] : it.v / groups) * p.table_stride;
+    const int64_t len = s.len[it.v];
+    int64_t at = (static_cast<int64_t>(it.first) << 7 >> shift) + lane;  // of the entries loaded last
+    int entry = 0, raw = -1;
+    unsigned have = 0;
+    uint64_t addr = 0;
+    bool in = at << shift < len;
+    if (in) raw = row[at];
 #pragma unroll 1
-      for (int e = 0; e < entries; ++e) mask |= (have >> e & 1) ? ((1u << rep) - 1u) << (e * rep) : 0u;
-      s.tmask[k % kAttMaskTiles] = mask;
-      mbar_arrive_expect_tx(rope_bar, __popc(have) * kKv4RopeBytes << shift);
-    }
+    for (int n = 0; n < it.count; ++n, ++k) {
+      if ((entry & 31) == 0) {
+        const bool good = in && raw >= 0 && raw < num_pages;
+        if (in && !good) atomicOr(&g_device_status, kDevStatusBadIndex);
+        addr = good ? reinterpret_cast<uint64_t>(cache) + static_cast<uint64_t>(raw) * page_stride : 0;
+        have = __ballot_sync(0xffffffffu, good);
+        at += 32;
+        in = at << shift < len;
+        if (in) raw = row[at];
+        entry = 0;
+      }
+      const unsigned pages = have >> entry & tile_pages;
+      auto load_rope = [&]() {
+        if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rope.at), rope.parity ^ 1, s);
+        if (!ok) return;
+        const uint32_t bar = bars + 8 * (L::RopeFull + rope.at);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages) * rope_bytes);
+        __syncwarp();
+        const int e = lane - entry;
+        if (e >= 0 && e < entries && addr)
+          bulk_load_1d(smem + L::Rope + rope.at * kRopeTile + e * rope_bytes,
+                       reinterpret_cast<const uint8_t*>(addr + rope_plane), rope_bytes, bar);
+        rope.next();
+      };
+      if (lane == 0) {
+        // copied 16-token parts of the tile, a bit each
+        uint32_t mask = 0xFFu;
+        if (pages != tile_pages) {
+          mask = 0;
+          const int rep = 1 << (shift - 4);
 #pragma unroll 1
-    for (int q = 0; q < kAttUnits; ++q, ++u, ring.next()) {
-      const int entry = q * kAttUnit >> shift;  // the (first) page of the unit
-      const int uid = __shfl_sync(0xffffffffu, id, entry + (parts == 2 ? part & 1 : 0));
-      const uint8_t* from = p.cache.base + uid * p.cache.page_stride + plane +
-                            (static_cast<uint32_t>(q * kAttUnit) & ((1u << shift) - 1u)) * row_bytes;
-      const uint32_t bar = bars + 8 * (L::RawFull + ring.at);
-      const uint32_t dst = to + (what == 2 ? rope.at * kRopeTile + q * kAttUnit * kKv4RopeBytes : ring.at * kUnitBytes);
-      // the stage's fill before this one has been taken
-      if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1, s);
+          for (int e = 0; e < entries; ++e) mask |= (pages >> e & 1) ? ((1u << rep) - 1u) << (e * rep) : 0u;
+        }
+        s.tmask[k % kAttMaskTiles] = mask;
+      }
+      if (L::RopeBufs == 2) load_rope();
+#pragma unroll 1
+      for (int q = 0; ok && q < L::PerTile; ++q) {
+        const int e = q << kLog >> shift;  // the (first) page of the unit in the tile
+        const uint64_t page = __shfl_sync(0xffffffffu, addr, entry + e + part);
+        const uint32_t off = plane + (static_cast<uint32_t>(q << kLog) & page_mask) * row_bytes;
+        const uint32_t bar = bars + 8 * (L::RawFull + ring.at);
+        // the stage's fill before this one has been taken
+        if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1, s);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages >> e & ((1u << parts) - 1u)) * unit_tx);
+        __syncwarp();
+        if (copies && page)
+          bulk_load_1d(to + ring.at * L::UnitBytes, reinterpret_cast<const uint8_t*>(page + off), bytes, bar);
+        ring.next();
+        ++u;
+      }
+      if (ok && L::RopeBufs == 1) load_rope();
       if (!ok) break;
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar, __popc(have >> entry & ((1u << parts) - 1u)) * tok * (kKv4CodeBytes + kKv4Blocks));
-      __syncwarp();
-      if (copies && uid >= 0) bulk_load_1d(dst, from, bytes, what == 2 ? rope_bar : bar);
+      entry += entries;
     }
-    if (!ok) break;
-    rope.next();
   }
   if (!ok) {  // copies in flight land before the CTA ends
     auto drain = [&](uint32_t bar, uint32_t parity) {
@@ -158,45 +182,50 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, AttShared<R>&
 #pragma unroll 1
     for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
 #pragma unroll 1
-    for (int i = max(0, k + 1 - L::RopeBufs); i <= k; ++i)
+    for (int i = max(0, k - L::RopeBufs); i < k; ++i)
       drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
   }
 }
 
 // --------------------------------------------------------------------------
-// Warp 15: scale bytes, one token per lane.  s_t = the largest of the 16;
+// Warp 23: scale bytes, one token per lane.  s_t = the largest of the 16;
 // s_t - s_j, at most 31, picks the row of the E4M3 table.  Bytes are taken as
 // pairs of 16-bit numbers; none of the differences borrows.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
-__device__ __forceinline__ void att_scales(AttShared<R>& s, uint8_t* smem, uint32_t bars, int tiles) {
+__device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31;
   AttRing<L::Units> ring;
   for (int k = 0; k < tiles; ++k) {
     const int kb = k % kAttScaleTiles;
 #pragma unroll 1
-    for (int q = 0; q < kAttUnits; ++q, ring.next()) {
+    for (int q = 0; q < L::PerTile; ++q, ring.next()) {
       const int st = ring.at;
       if (!att_wait(bars + 8 * (L::RawFull + st), ring.parity, s)) return;
-      const uint4 x = *reinterpret_cast<const uint4*>(smem + L::Raw + st * kUnitBytes + kUnitCodes + lane * kKv4Blocks);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t e[4], o[4];
-      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] = w[i] & 0x00FF00FFu;
-        o[i] = (w[i] >> 8) & 0x00FF00FFu;
-        m = __vmaxu2(m, __vmaxu2(e[i], o[i]));
+      for (int g = 0; g < L::Unit / 32; ++g) {
+        const int tok = 32 * g + lane;
+        const uint4 x =
+            *reinterpret_cast<const uint4*>(smem + L::Raw + st * L::UnitBytes + L::UnitCodes + tok * kKv4Blocks);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t e[4], o[4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = w[i] & 0x00FF00FFu;
+          o[i] = (w[i] >> 8) & 0x00FF00FFu;
+          m = __vmaxu2(m, __vmaxu2(e[i], o[i]));
+        }
+        m = max(m & 0xFFFFu, m >> 16);
+        const uint32_t mm = m * 0x00010001u;
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          r[i] = __vminu2(mm - e[i], 0x001F001Fu) | (__vminu2(mm - o[i], 0x001F001Fu) << 8);
+        *reinterpret_cast<uint4*>(&s.rel[(st * L::Unit + tok) * kKv4Blocks]) = make_uint4(r[0], r[1], r[2], r[3]);
+        s.smax[kb][L::Unit * q + tok] = static_cast<uint8_t>(m);
       }
-      m = max(m & 0xFFFFu, m >> 16);
-      const uint32_t mm = m * 0x00010001u;
-      uint32_t r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = __vminu2(mm - e[i], 0x001F001Fu) | (__vminu2(mm - o[i], 0x001F001Fu) << 8);
-      *reinterpret_cast<uint4*>(&s.rel[st][lane * kKv4Blocks]) = make_uint4(r[0], r[1], r[2], r[3]);
-      s.smax[kb][kAttUnit * q + lane] = static_cast<uint8_t>(m);
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (L::ScaleFull + st));
     }
@@ -204,21 +233,22 @@ __device__ __forceinline__ void att_scales(AttShared<R>& s, uint8_t* smem, uint3
 }
 
 // --------------------------------------------------------------------------
-// Warps 4-11: codes -> E4M3 tile.  A lane takes one block of 32 latents of
-// one token, half a warp a token, a warp four tokens of each copy unit.
+// Warps 4-19: codes -> E4M3 tile.  A lane takes one block of 32 latents of
+// one token, half a warp a token, a warp four tokens of a 64-token unit.
 // Bound by the ALU pipe (six operations a word of eight codes).
 // --------------------------------------------------------------------------
 template <int R, bool E4>
-__device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint32_t bars, int tiles) {
+__device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
   const int j = lane & 15;
   const int first_half = (j >> 2) & 1;
-  const int tok0 = 4 * dw + (lane >> 4);  // and tok0 + 2
-  // places of the two 16-byte chunks of both tokens in a tile
-  uint32_t to[2][2];
+  constexpr int N = L::Unit / (2 * kAttDequantWarps);  // tokens of a unit per half warp
+  const int tok0 = N * 2 * dw + (lane >> 4);  // and every second one from there
+  // places of the two 16-byte chunks of a token in a tile, by its row & 6
+  uint32_t to[N][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = tok0 + 2 * i;
@@ -226,18 +256,19 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
     }
   // The next unit's codes are fetched while this one's are looked up.
   struct Unit {
-    uint4 w[2];
-    uint32_t rel[2];
+    uint4 w[N];
+    uint32_t rel[N];
   };
   AttRing<L::Units> ring;
   auto fetch = [&](Unit& x) -> bool {
     const int st = ring.at;
     // the scale warp has seen the copies land
     if (!att_wait(bars + 8 * (L::ScaleFull + st), ring.parity, s)) return false;
-    const uint8_t* raw = smem + L::Raw + st * kUnitBytes + tok0 * kKv4CodeBytes + 16 * j;
+    const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok0 * kKv4CodeBytes + 16 * j;
+    const uint8_t* rel = s.rel + (st * L::Unit + tok0) * kKv4Blocks + j;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x.rel[i] = s.rel[st][(tok0 + 2 * i) * kKv4Blocks + j];
+    for (int i = 0; i < N; ++i) {
+      x.rel[i] = rel[2 * i * kKv4Blocks];
       x.w[i] = *reinterpret_cast<const uint4*>(raw + 2 * i * kKv4CodeBytes);
     }
     __syncwarp();
@@ -246,20 +277,22 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
     return true;
   };
   Unit cur, nxt;
-  uint2 lut[2];
   if (!fetch(cur)) return;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
+#pragma unroll 1
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
-    if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b), (k / 2 - 1) & 1, s)) return;
     uint8_t* tile = smem + L::K8 + b * kK8Tile;
 #pragma unroll 1
-    for (int q = 0; q < kAttUnits; ++q) {
-      const bool more = q + 1 < kAttUnits || k + 1 < tiles;
+    for (int q = 0; q < L::PerTile; ++q, tile += L::Unit * 128) {
+      // these tokens of the tile two before have been multiplied
+      if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b * L::PerTile + q), (k / 2 - 1) & 1, s)) return;
+      uint2 lut[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
+      const bool more = q + 1 < L::PerTile || k + 1 < tiles;
       if (more && !fetch(nxt)) return;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < N; ++i) {
         auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
           const uint32_t m = c & 0x77777777u;
           lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
@@ -270,14 +303,10 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
         word(cur.w[i].y, a.z, a.w);
         word(cur.w[i].z, c.x, c.y);
         word(cur.w[i].w, c.z, c.w);
-        *reinterpret_cast<uint4*>(tile + to[i][0] + q * kAttUnit * 128) = a;
-        *reinterpret_cast<uint4*>(tile + to[i][1] + q * kAttUnit * 128) = c;
+        *reinterpret_cast<uint4*>(tile + to[i][0]) = a;
+        *reinterpret_cast<uint4*>(tile + to[i][1]) = c;
       }
-      if (more) {
-        cur = nxt;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
-      }
+      cur = nxt;
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -286,7 +315,7 @@ __device__ __forceinline__ void att_dequant(AttShared<R>& s, uint8_t* smem, uint
 }
 
 // --------------------------------------------------------------------------
-// Warps 13 and 14: one thread each issues the MMAs of the scores and of the
+// Warps 21 and 22: one thread each issues the MMAs of the scores and of the
 // output.  Two threads, because each product has to go as soon as its
 // operands are there: with one thread in program order, the output product
 // that frees a K8 tile waited behind the scores of the next one, and the
@@ -302,7 +331,7 @@ __device__ __forceinline__ void att_drain(uint32_t bar) {
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_scores(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
+__device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
                                                int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
@@ -314,7 +343,7 @@ __device__ __forceinline__ void att_mma_scores(AttShared<R>& s, uint32_t smem, u
     t += it.count;
     ok = att_wait_one(bars + 8 * L::QFull, item & 1, s);
     for (int n = 0; ok && n < it.count; ++n, ++k) {
-      const int b = k & 1, rb = k % L::RopeBufs, sb = k % L::SBufs;
+      const int b = k & 1, sb = k % L::SBufs, rb = k % L::RopeBufs;
       if (k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
       if (ok) ok = att_wait_one(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
       if (!ok) break;
@@ -344,7 +373,7 @@ __device__ __forceinline__ void att_mma_scores(AttShared<R>& s, uint32_t smem, u
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_output(AttShared<R>& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
+__device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
                                                int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
@@ -359,17 +388,21 @@ __device__ __forceinline__ void att_mma_output(AttShared<R>& s, uint32_t smem, u
       if (!ok) break;
       tc_fence_after();
       const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
+      // 32 tokens after 32 tokens, so that the first ones' places can be
+      // filled again while the others are multiplied
 #pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt)
+      for (int ks = 0; ks < kAttTile / 32; ++ks) {
 #pragma unroll
-        for (int ks = 0; ks < kAttTile / 32; ++ks) {
+        for (int mt = 0; mt < 4; ++mt) {
           // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
           const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
           // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
           const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
           umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (n == 0 && ks == 0) ? 0u : 1u);
         }
-      umma_commit(bars + 8 * (L::K8Empty + (k & 1)));
+        if ((ks + 1) % (L::Unit / 32) == 0)
+          umma_commit(bars + 8 * (L::K8Empty + (k & 1) * L::PerTile + ks / (L::Unit / 32)));
+      }
       umma_commit(bars + 8 * L::PvDone);
     }
   }
@@ -383,7 +416,7 @@ __device__ __forceinline__ void att_mma_output(AttShared<R>& s, uint32_t smem, u
 // Queries of row group v into shared memory, and what its rows need (turn:
 // which of the two copies).
 template <int R, bool E4>
-__device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>& s, uint8_t* smem, uint32_t bars, int v,
+__device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int v,
                                           int turn) {
   using L = AttPlan<R, E4>;
   constexpr int TPR = 128 / R;  // threads per row
@@ -490,7 +523,7 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, AttShared<R>
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, AttShared<R>& s, uint8_t* smem, uint32_t bars,
+__device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars,
                                             uint32_t tmem, int V, int t0, int t1) {
   using L = AttPlan<R, E4>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -761,10 +794,16 @@ __device__ __forceinline__ void att_empty_rows(const Kv4AttendParams& p, const A
 template <int R, bool E4>
 __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
   using L = AttPlan<R, E4>;
-  extern __shared__ uint8_t smem_raw[];
-  // by an offset, so that the compiler still sees shared memory
-  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
-  AttShared<R>& s = *reinterpret_cast<AttShared<R>*>(smem + L::Misc);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // The MMA tiles need a 1024-byte boundary.  Dynamic shared memory begins on
+  // one where a kernel has no other (it does, behind the first KB of the
+  // window, on sm_103), and there is no room to round up.
+  uint8_t* smem = smem_raw;
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(&g_device_status, kDevStatusWaitTimeout);
+    return;
+  }
+  typename L::Shared& s = *reinterpret_cast<typename L::Shared*>(smem + L::Misc);
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t bars = smem_u32(s.bars);
   if (tid < L::BarCount) {
@@ -794,14 +833,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   const bool mine = static_cast<int>(blockIdx.x) < active;
   const int t0 = mine ? att_begin(total, blockIdx.x, active) : 0, t1 = mine ? att_begin(total, blockIdx.x + 1, active) : 0;
   const uint32_t base = smem_u32(smem);
-  // Registers of the four warpgroups (128 at launch): softmax, codes twice,
-  // copies and MMAs.
+  // every warpgroup does this, and the shares fit what the launch has
   if (warp < kAttSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SoftRegs));
   } else if (warp < kAttLoadWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::CodeRegs));
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::OtherRegs));
   }
   if (warp < kAttSoftWarps) {
     att_empty_rows<R>(p, s, V);

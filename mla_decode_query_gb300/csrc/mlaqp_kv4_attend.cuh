@@ -35,13 +35,13 @@
 // in the workspace and the join kernel adds the pieces in order.
 //
 // A CTA is a pipeline of warps:
-//   warp 12      copies pages into shared memory (bulk copies: codes and
-//                scales in units of 32 tokens, rope rows straight into the
+//   warp 20      copies pages into shared memory (bulk copies: codes and
+//                scales in units of 64 tokens, rope rows straight into the
 //                swizzled tile, the cache's layout being that of the tile);
-//   warp 15      scale bytes -> s_t and s_t - s_j, a token per lane;
-//   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
+//   warp 23      scale bytes -> s_t and s_t - s_j, a token per lane;
+//   warps 4-19   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
-//   warps 13, 14 one thread each issues the MMAs of scores and output;
+//   warps 21, 22 one thread each issues the MMAs of scores and output;
 //   warps 0-3    queries, softmax (one token per thread), rescaling, output.
 // O stays in tensor memory; it is rescaled only when a row's maximum has
 // grown by more than 2^3.
@@ -53,19 +53,16 @@
 
 namespace mlaqp {
 
-constexpr int kAttThreads = 512;
+constexpr int kAttThreads = 768;
 constexpr int kAttSoftWarps = 4;
-constexpr int kAttDequantWarps = 8;
-constexpr int kAttLoadWarp = 12;
-constexpr int kAttScoreWarp = 13;
-constexpr int kAttOutputWarp = 14;
-constexpr int kAttScaleWarp = 15;
+constexpr int kAttDequantWarps = 16;
+constexpr int kAttLoadWarp = kAttSoftWarps + kAttDequantWarps;
+constexpr int kAttScoreWarp = kAttLoadWarp + 1;
+constexpr int kAttOutputWarp = kAttLoadWarp + 2;
+constexpr int kAttScaleWarp = kAttLoadWarp + 3;
 constexpr int kAttTile = 128;   // tokens per tile (MMA M of the scores)
-constexpr int kAttUnit = 32;    // tokens per copy unit
-constexpr int kAttUnits = kAttTile / kAttUnit;
-constexpr int kAttMaxUnits = 4;    // copy units in flight at most
-// Tiles whose scales are kept: the scale warp runs up to four units ahead of
-// the code warps, these up to two tiles ahead of the softmax.
+// Tiles whose scales are kept: the scale warp runs up to three copy units
+// ahead of the code warps, these up to two tiles ahead of the softmax.
 constexpr int kAttScaleTiles = 4;
 constexpr int kAttMaskTiles = 8;   // the same for what the copying warp notes, which is ahead of both
 constexpr int kAttMaxSeqs = 256;  // sequences x row groups of a call
@@ -75,8 +72,6 @@ constexpr float kAttShift = 12.f; // 2^(12+3) stays inside E5M2 and FP16
 // Reference of a row that has seen no token: whatever it sees first is above.
 constexpr float kAttUnseen = -1e30f;
 
-constexpr int kUnitCodes = kAttUnit * kKv4CodeBytes;
-constexpr int kUnitBytes = kUnitCodes + kAttUnit * kKv4Blocks;
 constexpr int kRopeTile = kAttTile * kKv4RopeBytes;
 constexpr int kK8Block = kAttTile * 128;  // 128 latents of a tile
 constexpr int kK8Tile = 4 * kK8Block;
@@ -89,11 +84,11 @@ struct AttSchedule {
   int fail;
 };
 
-template <int R>
+template <int R, int Ring>  // Ring: tokens of all copy units in flight
 struct AttShared : AttSchedule {
   uint32_t tmem;
   alignas(8) uint32_t lut[32][2];           // E4M3 of the 8 magnitudes * 2^(6-k)
-  alignas(16) uint8_t rel[kAttMaxUnits][kAttUnit * kKv4Blocks];  // s_t - s_j of a copy unit, at most 31
+  alignas(16) uint8_t rel[Ring * kKv4Blocks];  // s_t - s_j of the copy units, at most 31
   alignas(16) float wmax[kAttSoftWarps][R];
   alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12, or kAttUnseen
   alignas(16) float alpha[kAttSoftWarps][R];
@@ -109,7 +104,9 @@ struct AttShared : AttSchedule {
 };
 
 // Shared memory and tensor memory of a variant: R query rows, E4M3 or BF16
-// queries.  RopeBufs / Units fill what the K8 tiles, queries and P leave.
+// queries.  Units copy units of Unit tokens take what the K8 tiles, queries
+// and P leave: 64 tokens a unit where two of them fit, because a warp that
+// works alone needs some hundred cycles a unit whatever its size.
 template <int R, bool E4>
 struct AttPlan {
   static constexpr int QTerms = E4 ? 1 : 2;
@@ -119,7 +116,12 @@ struct AttPlan {
   static constexpr int SBufs = (R == 32 && !E4) ? 1 : 2;
   static constexpr int OCol = SBufs * SCols;
   static constexpr int RopeBufs = (R == 32 && !E4) ? 1 : 2;
-  static constexpr int Units = R == 16 ? 4 : 3;
+  static constexpr int Unit = R == 32 ? 32 : 64;
+  static constexpr int Units = R == 32 ? 3 : 2;
+  static constexpr int PerTile = kAttTile / Unit;
+  static constexpr int UnitCodes = Unit * kKv4CodeBytes;
+  static constexpr int UnitBytes = UnitCodes + Unit * kKv4Blocks;
+  using Shared = AttShared<R, Unit * Units>;
   static constexpr int K8 = 0;
   static constexpr int Rope = K8 + 2 * kK8Tile;
   static constexpr int Q = Rope + RopeBufs * kRopeTile;
@@ -128,15 +130,18 @@ struct AttPlan {
   static constexpr int P = QPe + R * 128;
   static constexpr int PChunk = 16 * kAttTile;     // 16 rows of P
   static constexpr int Raw = P + NP / 16 * PChunk;
-  static constexpr int Misc = Raw + Units * kUnitBytes;
-  static constexpr int Bytes = Misc + static_cast<int>(sizeof(AttShared<R>)) + 1024;
+  static constexpr int Misc = Raw + Units * UnitBytes;
+  static constexpr int Bytes = Misc + static_cast<int>(sizeof(Shared));
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
+  // registers of the softmax, code and other warps; (80 x 6 warpgroups at launch)
+  static constexpr int SoftRegs = R == 16 ? 152 : 200, CodeRegs = R == 16 ? 64 : 56, OtherRegs = R == 16 ? 72 : 56;
+  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 480, "registers");
   // barrier indexes
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
                        RopeFull = ScaleFull + Units,
-                       RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,
-                       SFull = K8Empty + 2, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
+                       RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,  // per part of a tile
+                       SFull = K8Empty + 2 * PerTile, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
                        QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, BarCount = Drain + 2;
   static_assert(BarCount <= 40, "barriers");
 };
