@@ -96,10 +96,48 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   const uint32_t rope_plane = kv4_rope_off(0, shift), rope_bytes = kKv4RopeBytes << shift;
   const unsigned tile_pages = (1u << entries) - 1u;
 
-  bool ok = true;
-  int k = 0, u = 0;
+  // Rope rows of tile kr, a page per lane.  Their buffer comes free when the
+  // tile's scores begin, the codes' when those have been fetched, so neither
+  // waits behind the other: the warp polls for both.
+  int k = 0, u = 0, kr = 0;
   AttRing<L::Units> ring;
-  AttRing<L::RopeBufs> rope;
+  auto load_rope = [&]() {
+    const int page = lane < entries ? s.pages[kr % kAttPageTiles][lane] : -1;
+    const uint32_t bar = bars + 8 * L::RopeFull;
+    const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * rope_bytes);
+    __syncwarp();
+    if (page >= 0)
+      bulk_load_1d(smem + L::Rope + lane * rope_bytes, cache + page * page_stride + rope_plane, rope_bytes, bar);
+    ++kr;
+  };
+  auto rope_free = [&]() { return kr == 0 || mbar_test(bars + 8 * L::RopeEmpty, (kr - 1) & 1); };
+  // Rope rows of all tiles up to `tile`.
+  auto finish_rope = [&](int tile) -> bool {
+#pragma unroll 1
+    while (kr <= tile) {
+      if (kr > 0 && !att_wait(bars + 8 * L::RopeEmpty, (kr - 1) & 1, s)) return false;
+      load_rope();
+    }
+    return true;
+  };
+  // The copy stage at hand is empty (or a wait ran out: false); tiles up to
+  // `tile` may have their rope rows copied meanwhile.
+  auto wait_stage = [&](int tile) -> bool {
+    const unsigned long long t_in = globaltimer_ns();
+#pragma unroll 1
+    while (true) {
+      const bool rope = kr <= tile && rope_free();
+      const bool stage = u < L::Units || mbar_test(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1);
+      if (__all_sync(0xffffffffu, rope)) load_rope();
+      if (__all_sync(0xffffffffu, stage)) return true;
+      const bool late = globaltimer_ns() - t_in > kAttWaitNs;
+      if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
+      if (late) *reinterpret_cast<volatile int*>(&s.fail) = 1;
+      if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(&s.fail))) return false;
+    }
+  };
+  bool ok = true;
   for (int t = t0; ok && t < t1;) {
     const AttItem it = att_item(s.prefix, V, t, t1);
     t += it.count;
@@ -109,7 +147,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     const int32_t* row = p.block_table + (p.seqs ? p.seqs[it.v / groups] : it.v / groups) * p.table_stride;
     const int64_t len = s.len[it.v];
     int64_t at = (static_cast<int64_t>(it.first) << 7 >> shift) + lane;  // of the entries loaded last
-    int entry = 0, raw = -1;
+    int entry = 0, raw = -1, id = -1;
     unsigned have = 0;
     uint64_t addr = 0;
     bool in = at << shift < len;
@@ -121,24 +159,16 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
         if (in && !good) atomicOr(&g_device_status, kDevStatusBadIndex);
         addr = good ? reinterpret_cast<uint64_t>(cache) + static_cast<uint64_t>(raw) * page_stride : 0;
         have = __ballot_sync(0xffffffffu, good);
+        id = good ? raw : -1;
         at += 32;
         in = at << shift < len;
         if (in) raw = row[at];
         entry = 0;
       }
       const unsigned pages = have >> entry & tile_pages;
-      auto load_rope = [&]() {
-        if (k >= L::RopeBufs) ok = att_wait(bars + 8 * (L::RopeEmpty + rope.at), rope.parity ^ 1, s);
-        if (!ok) return;
-        const uint32_t bar = bars + 8 * (L::RopeFull + rope.at);
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages) * rope_bytes);
-        __syncwarp();
-        const int e = lane - entry;
-        if (e >= 0 && e < entries && addr)
-          bulk_load_1d(smem + L::Rope + rope.at * kRopeTile + e * rope_bytes,
-                       reinterpret_cast<const uint8_t*>(addr + rope_plane), rope_bytes, bar);
-        rope.next();
-      };
+      ok = finish_rope(k - kAttPageTiles);
+      if (!ok) break;
+      if (lane >= entry && lane < entry + entries) s.pages[k % kAttPageTiles][lane - entry] = id;
       if (lane == 0) {
         // copied 16-token parts of the tile, a bit each
         uint32_t mask = 0xFFu;
@@ -150,15 +180,14 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
         }
         s.tmask[k % kAttMaskTiles] = mask;
       }
-      if (L::RopeBufs == 2) load_rope();
+      __syncwarp();
 #pragma unroll 1
-      for (int q = 0; ok && q < L::PerTile; ++q) {
+      for (int q = 0; q < L::PerTile; ++q) {
         const int e = q << kLog >> shift;  // the (first) page of the unit in the tile
         const uint64_t page = __shfl_sync(0xffffffffu, addr, entry + e + part);
         const uint32_t off = plane + (static_cast<uint32_t>(q << kLog) & page_mask) * row_bytes;
         const uint32_t bar = bars + 8 * (L::RawFull + ring.at);
-        // the stage's fill before this one has been taken
-        if (u >= L::Units) ok = att_wait(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1, s);
+        ok = wait_stage(k);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages >> e & ((1u << parts) - 1u)) * unit_tx);
         __syncwarp();
@@ -167,11 +196,11 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
         ring.next();
         ++u;
       }
-      if (ok && L::RopeBufs == 1) load_rope();
       if (!ok) break;
       entry += entries;
     }
   }
+  if (ok) ok = finish_rope(k - 1);
   if (!ok) {  // copies in flight land before the CTA ends
     auto drain = [&](uint32_t bar, uint32_t parity) {
       const unsigned long long at = globaltimer_ns();
@@ -181,9 +210,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     };
 #pragma unroll 1
     for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
-#pragma unroll 1
-    for (int i = max(0, k - L::RopeBufs); i < k; ++i)
-      drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
+    if (kr > 0) drain(bars + 8 * L::RopeFull, (kr - 1) & 1);
   }
 }
 
@@ -227,90 +254,90 @@ __device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, u
         s.smax[kb][L::Unit * q + tok] = static_cast<uint8_t>(m);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (L::ScaleFull + st));
+      if (lane == 0) mbar_arrive(bars + 8 * (L::ScaleFull + (k & 1) * L::PerTile + q));
     }
   }
 }
 
 // --------------------------------------------------------------------------
-// Warps 4-19: codes -> E4M3 tile.  A lane takes one block of 32 latents of
-// one token, half a warp a token, a warp four tokens of a 64-token unit.
-// Bound by the ALU pipe (six operations a word of eight codes).
+// Warps 4-19: codes -> E4M3 tile.  Four warps take a block of 128 latents of
+// the tile each, a warp 32 tokens of it, a thread four blocks of 32 latents of
+// four tokens.  So the output product gives the tile back, and the score
+// product takes it, block by block, and a warp still has one wait, one fence
+// and one arrival a tile: all sixteen warps on one block after the other
+// spent 900 cycles a block, most of them there.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
-  const int j = lane & 15;
-  const int first_half = (j >> 2) & 1;
-  constexpr int N = L::Unit / (2 * kAttDequantWarps);  // tokens of a unit per half warp
-  const int tok0 = N * 2 * dw + (lane >> 4);  // and every second one from there
-  // places of the two 16-byte chunks of a token in a tile, by its row & 6
-  uint32_t to[N][2];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = tok0 + 2 * i;
-      to[i][h] = (j >> 2) * kK8Block + row * 128 + (((2 * (j & 3) + (first_half ^ h)) ^ (row & 7)) << 4);
-    }
-  // The next unit's codes are fetched while this one's are looked up.
-  struct Unit {
-    uint4 w[N];
-    uint32_t rel[N];
+  const int blk = dw >> 2, jj = lane & 3;              // 128 latents, 32 of them
+  const int row = 32 * (dw & 3) + (lane >> 2);         // first token of the tile; then every eighth
+  const int unit = 32 * (dw & 3) / L::Unit;            // its copy unit in the tile, and token there
+  const int tok = row % L::Unit;
+  // The two 16-byte chunks' places: the order of a block's halves alternates
+  // with the 128 latents.  Eight rows on, the swizzle is the same.
+  const uint32_t half = blk & 1;
+  const uint32_t at0 = blk * kK8Block + row * 128 + (((2 * jj + half) ^ (row & 7)) << 4);
+  const uint32_t at1 = blk * kK8Block + row * 128 + (((2 * jj + (half ^ 1)) ^ (row & 7)) << 4);
+  struct Codes {
+    uint4 w[4];
+    uint32_t rel[4];
   };
-  AttRing<L::Units> ring;
-  auto fetch = [&](Unit& x) -> bool {
-    const int st = ring.at;
-    // the scale warp has seen the copies land
-    if (!att_wait(bars + 8 * (L::ScaleFull + st), ring.parity, s)) return false;
-    const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok0 * kKv4CodeBytes + 16 * j;
-    const uint8_t* rel = s.rel + (st * L::Unit + tok0) * kKv4Blocks + j;
+  int st = unit % L::Units;  // every PerTile-th copy unit is the warp's
+  int kf = 0;                // tile fetched next
+  auto fetch = [&](Codes& x) -> bool {
+    // The scale warp has seen the copies land.  (Its barriers go by the
+    // unit's place in two tiles: a stage's own barrier would pass phases that
+    // this warp does not wait for.)
+    if (!att_wait(bars + 8 * (L::ScaleFull + (kf & 1) * L::PerTile + unit), (kf >> 1) & 1, s)) return false;
+    ++kf;
+    const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok * kKv4CodeBytes + 64 * blk + 16 * jj;
+    const uint8_t* rel = s.rel + (st * L::Unit + tok) * kKv4Blocks + 4 * blk + jj;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x.rel[i] = rel[2 * i * kKv4Blocks];
-      x.w[i] = *reinterpret_cast<const uint4*>(raw + 2 * i * kKv4CodeBytes);
+    for (int i = 0; i < 4; ++i) {
+      x.rel[i] = rel[8 * i * kKv4Blocks];
+      x.w[i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
-    ring.next();
+    st = (st + L::PerTile) % L::Units;
     return true;
   };
-  Unit cur, nxt;
+  Codes cur, nxt;
   if (!fetch(cur)) return;
 #pragma unroll 1
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
     uint8_t* tile = smem + L::K8 + b * kK8Tile;
-#pragma unroll 1
-    for (int q = 0; q < L::PerTile; ++q, tile += L::Unit * 128) {
-      // these tokens of the tile two before have been multiplied
-      if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + b * L::PerTile + q), (k / 2 - 1) & 1, s)) return;
-      uint2 lut[N];
+    // The next tile's codes, ahead of this one's work, but for the first one:
+    // its successor is only being copied.
+    if (k > 0 && k + 1 < tiles && !fetch(nxt)) return;
+    // the block of the tile two before has been multiplied
+    if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + 4 * b + blk), (k / 2 - 1) & 1, s)) return;
+    uint2 lut[4];
 #pragma unroll
-      for (int i = 0; i < N; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
-      const bool more = q + 1 < L::PerTile || k + 1 < tiles;
-      if (more && !fetch(nxt)) return;
+    for (int i = 0; i < 4; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
-          const uint32_t m = c & 0x77777777u;
-          lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
-          hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
-        };
-        uint4 a, c;
-        word(cur.w[i].x, a.x, a.y);
-        word(cur.w[i].y, a.z, a.w);
-        word(cur.w[i].z, c.x, c.y);
-        word(cur.w[i].w, c.z, c.w);
-        *reinterpret_cast<uint4*>(tile + to[i][0]) = a;
-        *reinterpret_cast<uint4*>(tile + to[i][1]) = c;
-      }
-      cur = nxt;
+    for (int i = 0; i < 4; ++i) {
+      auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
+        const uint32_t m = c & 0x77777777u;
+        lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
+        hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
+      };
+      uint4 a, c;
+      word(cur.w[i].x, a.x, a.y);
+      word(cur.w[i].y, a.z, a.w);
+      word(cur.w[i].z, c.x, c.y);
+      word(cur.w[i].w, c.z, c.w);
+      *reinterpret_cast<uint4*>(tile + at0 + i * 1024) = a;
+      *reinterpret_cast<uint4*>(tile + at1 + i * 1024) = c;
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (L::K8Full + b));
+    if (lane == 0) mbar_arrive(bars + 8 * (L::K8Full + 4 * b + blk));
+    if (k == 0 && tiles > 1 && !fetch(nxt)) return;
+    cur = nxt;
   }
 }
 
@@ -343,29 +370,33 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
     t += it.count;
     ok = att_wait_one(bars + 8 * L::QFull, item & 1, s);
     for (int n = 0; ok && n < it.count; ++n, ++k) {
-      const int b = k & 1, sb = k % L::SBufs, rb = k % L::RopeBufs;
+      const int b = k & 1, sb = k % L::SBufs;
       if (k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
-      if (ok) ok = att_wait_one(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
+      if (ok) ok = att_wait_one(bars + 8 * L::RopeFull, k & 1, s);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + sb * L::SCols;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint64_t ad = smem_desc_sw128(smem + L::Rope + rb * kRopeTile + c * 32, 16, 1024);
+        const uint64_t ad = smem_desc_sw128(smem + L::Rope + c * 32, 16, 1024);
         const uint64_t bd = smem_desc_sw128(smem + L::QPe + c * 32, 16, 1024);
         umma_bf16(d + L::NQ, ad, bd, id_r, c > 0);
       }
-      umma_commit(bars + 8 * (L::RopeEmpty + rb));
-      ok = att_wait_one(bars + 8 * (L::K8Full + b), (k / 2) & 1, s);
-      if (!ok) break;
-      tc_fence_after();
+      umma_commit(bars + 8 * L::RopeEmpty);
       const uint32_t k8 = smem + L::K8 + b * kK8Tile;
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        const uint64_t ad = smem_desc_sw128(k8 + (c >> 2) * kK8Block + (c & 3) * 32, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(smem + L::Q + (c >> 2) * L::QBlock + (c & 3) * 32, 16, 1024);
-        umma_f8(d, ad, bd, id_s, c > 0);
+#pragma unroll 1
+      for (int i = 0; ok && i < 4; ++i) {
+        ok = att_wait_one(bars + 8 * (L::K8Full + 4 * b + i), (k / 2) & 1, s);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t ad = smem_desc_sw128(k8 + i * kK8Block + c * 32, 16, 1024);
+          const uint64_t bd = smem_desc_sw128(smem + L::Q + i * L::QBlock + c * 32, 16, 1024);
+          umma_f8(d, ad, bd, id_s, i + c > 0);
+        }
       }
+      if (!ok) break;
       umma_commit(bars + 8 * (L::SFull + sb));
     }
   }
@@ -388,20 +419,17 @@ __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& 
       if (!ok) break;
       tc_fence_after();
       const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
-      // 32 tokens after 32 tokens, so that the first ones' places can be
-      // filled again while the others are multiplied
 #pragma unroll 1
-      for (int ks = 0; ks < kAttTile / 32; ++ks) {
+      for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int ks = 0; ks < kAttTile / 32; ++ks) {
           // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
           const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
           // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
           const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
           umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (n == 0 && ks == 0) ? 0u : 1u);
         }
-        if ((ks + 1) % (L::Unit / 32) == 0)
-          umma_commit(bars + 8 * (L::K8Empty + (k & 1) * L::PerTile + ks / (L::Unit / 32)));
+        umma_commit(bars + 8 * (L::K8Empty + 4 * (k & 1) + mt));
       }
       umma_commit(bars + 8 * L::PvDone);
     }
@@ -556,41 +584,38 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       // the scores of the row group's last tile are in: its queries are done with
       if (n == it.count - 1 && next_t < t1) att_query<R, E4>(p, s, smem, bars, next.v, turn ^ 1);
       if (n < 0) continue;
-      att_wait(bars + 8 * (L::K8Full + (k & 1)), (k / 2) & 1, s);  // the tile's scales are in, too
       tc_fence_after();
+      // the scores, in flight while the scales are looked at
+      uint32_t v[R / 16][(L::QTerms + 1) * 16];
+#pragma unroll
+      for (int hb = 0; hb < R / 16; ++hb)
+#pragma unroll
+        for (int part = 0; part <= L::QTerms; ++part)
+          tmem_ld16_begin(tmem + lanes + sb * L::SCols + 16 * hb + part * R, &v[hb][16 * part]);
+      att_wait(bars + 8 * (L::K8Full + 4 * (k & 1)), (k / 2) & 1, s);  // the tile's scales are in, too
       const uint32_t sm = s.smax[kb][tid];
       const float ts = sm == kKv4ScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((sm - 6u) << 23);
       const float its = __uint_as_float((260u - sm) << 23);
       const float et = static_cast<float>(static_cast<int>(sm) - 133);
       const int64_t tile_tok = static_cast<int64_t>(it.first + n) * kAttTile;
       const uint32_t mask = s.tmask[k % kAttMaskTiles];
-      const bool whole = mask == 0xFFu &&
-                         tile_tok + kAttTile <= s.limit[turn][0];
+      const bool whole = mask == 0xFFu && tile_tok + kAttTile <= s.limit[turn][0];
       const bool here = mask >> (tid >> 4) & 1;
       float y[R];
 #pragma unroll
-      for (int hb = 0; hb < R; hb += 16) {
-        float w[16];
-        const uint32_t d = tmem + lanes + sb * L::SCols + hb;
-        if constexpr (E4) {
-          uint32_t v[32];
-          tmem_ld2x16(d, d + R, v);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) w[r] = fmaf(__uint_as_float(v[r]), ts, __uint_as_float(v[16 + r]));
-        } else {
-          uint32_t v[48];
-          tmem_ld3x16(d, d + R, d + 2 * R, v);
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            w[r] = fmaf(fmaf(__uint_as_float(v[16 + r]), 0.0625f, __uint_as_float(v[r])), ts, __uint_as_float(v[32 + r]));
-        }
+      for (int hb = 0; hb < R / 16; ++hb) {
+        tmem_ld_end(v[hb]);
 #pragma unroll
         for (int r = 0; r < 16; r += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&s.cr[turn][hb + r]);
-          y[hb + r] = fmaf(w[r], c.x, et);
-          y[hb + r + 1] = fmaf(w[r + 1], c.y, et);
-          y[hb + r + 2] = fmaf(w[r + 2], c.z, et);
-          y[hb + r + 3] = fmaf(w[r + 3], c.w, et);
+          const float4 c = *reinterpret_cast<const float4*>(&s.cr[turn][16 * hb + r]);
+          const float cc[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* w = &v[hb][r + q];
+            float d = __uint_as_float(w[0]);
+            if constexpr (!E4) d = fmaf(__uint_as_float(w[16]), 0.0625f, d);  // the second query term
+            y[16 * hb + r + q] = fmaf(fmaf(d, ts, __uint_as_float(w[16 * L::QTerms])), cc[q], et);
+          }
         }
       }
       tc_fence_before();
@@ -709,7 +734,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
       if (lane == r) mine = v;
     }
-    if (lane < R) s.lsum[warp][lane] = mine;
+    if (lane < R) s.wmax[warp][lane] = mine;
     soft_barrier();
     const bool done = att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
     if (!done || *reinterpret_cast<volatile int*>(&s.fail)) {
@@ -725,7 +750,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     }
     __syncwarp();
     if (lane < R) {
-      const float sum = (s.lsum[0][lane] + s.lsum[1][lane]) + (s.lsum[2][lane] + s.lsum[3][lane]);
+      const float sum = (s.wmax[0][lane] + s.wmax[1][lane]) + (s.wmax[2][lane] + s.wmax[3][lane]);
       const float m = mref[lane];
       const int64_t xo = s.xoff[turn][lane];
       if (complete) {
@@ -808,8 +833,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   const uint32_t bars = smem_u32(s.bars);
   if (tid < L::BarCount) {
     uint32_t count = 1;
-    if ((tid >= L::RawEmpty && tid < L::ScaleFull) || tid == L::K8Full || tid == L::K8Full + 1) count = kAttDequantWarps;
-    if ((tid >= L::SEmpty && tid < L::PFull) || tid == L::PFull || tid == L::QFull || tid == L::OEmpty) count = 128;
+    if (tid >= L::RawEmpty && tid < L::ScaleFull) count = L::UnitWarps;
+    if (tid >= L::K8Full && tid < L::K8Empty) count = kAttDequantWarps / 4;
+    if ((tid >= L::SEmpty && tid <= L::PFull) || tid == L::QFull || tid == L::OEmpty) count = 128;
     mbar_init(bars + 8 * tid, count);
     fence_barrier_init();
   }
@@ -1003,6 +1029,9 @@ cudaError_t kv4_attend_setup() {
   for (const AttKernels& k : all) {
     cudaError_t e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k.main);
+    // the warps share out what this many registers a thread make
+    if (e == cudaSuccess && a.numRegs < kAttRegs) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k.join);
     if (e != cudaSuccess) return e;
   }

@@ -54,6 +54,7 @@
 namespace mlaqp {
 
 constexpr int kAttThreads = 768;
+constexpr int kAttRegs = 80;    // a thread's at launch: 65536 / 768 in steps of 8
 constexpr int kAttSoftWarps = 4;
 constexpr int kAttDequantWarps = 16;
 constexpr int kAttLoadWarp = kAttSoftWarps + kAttDequantWarps;
@@ -61,9 +62,11 @@ constexpr int kAttScoreWarp = kAttLoadWarp + 1;
 constexpr int kAttOutputWarp = kAttLoadWarp + 2;
 constexpr int kAttScaleWarp = kAttLoadWarp + 3;
 constexpr int kAttTile = 128;   // tokens per tile (MMA M of the scores)
-// Tiles whose scales are kept: the scale warp runs up to three copy units
-// ahead of the code warps, these up to two tiles ahead of the softmax.
-constexpr int kAttScaleTiles = 4;
+// Tiles whose scales are kept.  While the softmax still reads those of tile
+// k-2, the code warps may have fetched tile k+1 and the scale warp be three
+// copy units, a tile and a half, ahead of them: k-2 .. k+3.
+constexpr int kAttScaleTiles = 6;
+constexpr int kAttPageTiles = 4;   // tiles whose rope rows may be outstanding
 constexpr int kAttMaskTiles = 8;   // the same for what the copying warp notes, which is ahead of both
 constexpr int kAttMaxSeqs = 256;  // sequences x row groups of a call
 constexpr float kAttSlack = 3.f;  // log2 growth of the maximum that is let pass
@@ -92,7 +95,6 @@ struct AttShared : AttSchedule {
   alignas(16) float wmax[kAttSoftWarps][R];
   alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12, or kAttUnseen
   alignas(16) float alpha[kAttSoftWarps][R];
-  float lsum[kAttSoftWarps][R];
   // of the row group at hand and the next one, by turns
   alignas(16) float cr[2][R];               // C_r
   int limit[2][R];                          // visible tokens of a row
@@ -100,6 +102,7 @@ struct AttShared : AttSchedule {
   int lseoff[2][R];
   uint8_t smax[kAttScaleTiles][kAttTile];   // s_t
   uint32_t tmask[kAttMaskTiles];            // 16-token parts of a tile that were copied, a bit each
+  int pages[kAttPageTiles][8];              // a tile's pages, -1: none
   alignas(8) uint64_t bars[40];
 };
 
@@ -115,16 +118,18 @@ struct AttPlan {
   static constexpr int SCols = NQ + R;             // scores + rope part
   static constexpr int SBufs = (R == 32 && !E4) ? 1 : 2;
   static constexpr int OCol = SBufs * SCols;
-  static constexpr int RopeBufs = (R == 32 && !E4) ? 1 : 2;
-  static constexpr int Unit = R == 32 ? 32 : 64;
-  static constexpr int Units = R == 32 ? 3 : 2;
+  static constexpr int Unit = (R == 32 && !E4) ? 32 : 64;
+  static constexpr int Units = (R == 32 && E4) ? 2 : 3;
   static constexpr int PerTile = kAttTile / Unit;
+  static_assert(Units <= 2 * PerTile, "the scale barriers are the units of two tiles, waited for once each");
+  static constexpr int UnitWarps = kAttDequantWarps / PerTile;  // code warps that read a unit
+  static_assert(UnitWarps % 4 == 0, "each block of latents, whole warps");
   static constexpr int UnitCodes = Unit * kKv4CodeBytes;
   static constexpr int UnitBytes = UnitCodes + Unit * kKv4Blocks;
   using Shared = AttShared<R, Unit * Units>;
   static constexpr int K8 = 0;
   static constexpr int Rope = K8 + 2 * kK8Tile;
-  static constexpr int Q = Rope + RopeBufs * kRopeTile;
+  static constexpr int Q = Rope + kRopeTile;
   static constexpr int QBlock = NQ * 128;          // 128 latents of the queries
   static constexpr int QPe = Q + 4 * QBlock;
   static constexpr int P = QPe + R * 128;
@@ -134,14 +139,15 @@ struct AttPlan {
   static constexpr int Bytes = Misc + static_cast<int>(sizeof(Shared));
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
-  // registers of the softmax, code and other warps; (80 x 6 warpgroups at launch)
-  static constexpr int SoftRegs = R == 16 ? 152 : 200, CodeRegs = R == 16 ? 64 : 56, OtherRegs = R == 16 ? 72 : 56;
-  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 480, "registers");
-  // barrier indexes
+  // registers of the softmax, code and other warps, of the six warpgroups' at launch
+  static constexpr int SoftRegs = R == 16 ? 120 : 152, CodeRegs = R == 16 ? 72 : 64, OtherRegs = 72;
+  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 6 * kAttRegs, "registers");
+  static_assert(SoftRegs >= kAttRegs && CodeRegs <= kAttRegs && OtherRegs <= kAttRegs, "raised for one, lowered for the others");
+  // barrier indexes; K8Full and K8Empty: 4 * tile buffer + block of 128 latents
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
-                       RopeFull = ScaleFull + Units,
-                       RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 2,  // per part of a tile
-                       SFull = K8Empty + 2 * PerTile, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
+                       RopeFull = ScaleFull + 2 * PerTile,
+                       RopeEmpty = RopeFull + 1, K8Full = RopeEmpty + 1, K8Empty = K8Full + 8,  // per 128 latents of a tile
+                       SFull = K8Empty + 8, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
                        QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, BarCount = Drain + 2;
   static_assert(BarCount <= 40, "barriers");
 };
@@ -178,17 +184,22 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
       "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),              \
       "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
 
-// 16 columns each from two or three places of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld2x16(uint32_t a, uint32_t b, uint32_t (&r)[32]) {
+// 16 columns of this thread's TMEM lane, not there before tmem_ld_end().
+__device__ __forceinline__ void tmem_ld16_begin(uint32_t a, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : MLAQP_R16(r, 0), MLAQP_R16(r, 16)
-      : "r"(a), "r"(b)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : MLAQP_R16(r, 0)
+      : "r"(a)
       : "memory");
 }
+// Waits for the loads begun and makes their registers depend on it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// 16 columns each from three places of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld3x16(uint32_t a, uint32_t b, uint32_t c, uint32_t (&r)[48]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
@@ -215,6 +226,19 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Whether the phase of that parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
