@@ -64,7 +64,7 @@ struct AttRing {
 };
 
 // --------------------------------------------------------------------------
-// Warp 20: pages into shared memory.
+// Warp 12: pages into shared memory.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, int V,
@@ -215,7 +215,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
 }
 
 // --------------------------------------------------------------------------
-// Warp 23: scale bytes, one token per lane.  s_t = the largest of the 16;
+// Warp 15: scale bytes, one token per lane.  s_t = the largest of the 16;
 // s_t - s_j, at most 31, picks the row of the E4M3 table.  Bytes are taken as
 // pairs of 16-bit numbers; none of the differences borrows.
 // --------------------------------------------------------------------------
@@ -260,48 +260,56 @@ __device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, u
 }
 
 // --------------------------------------------------------------------------
-// Warps 4-19: codes -> E4M3 tile.  Four warps take a block of 128 latents of
-// the tile each, a warp 32 tokens of it, a thread four blocks of 32 latents of
-// four tokens.  So the output product gives the tile back, and the score
+// Warps 4-11: codes -> E4M3 tile.  Two warps take a block of 128 latents of
+// the tile, a warp 64 tokens of it, a thread eight blocks of 32 latents of
+// eight tokens.  So the output product gives the tile back, and the score
 // product takes it, block by block, and a warp still has one wait, one fence
-// and one arrival a tile: all sixteen warps on one block after the other
-// spent 900 cycles a block, most of them there.
+// and one arrival a tile.  (All warps on one block after the other spent 900
+// cycles a block, mostly there; sixteen warps of half the work each spent
+// as many instructions around it as on it.)
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
-  const int blk = dw >> 2, jj = lane & 3;              // 128 latents, 32 of them
-  const int row = 32 * (dw & 3) + (lane >> 2);         // first token of the tile; then every eighth
-  const int unit = 32 * (dw & 3) / L::Unit;            // its copy unit in the tile, and token there
-  const int tok = row % L::Unit;
+  const int blk = dw >> 1, jj = lane & 3;              // 128 latents, 32 of them
+  constexpr int N = L::WarpTokens / 8;                 // tokens of a thread: every eighth
+  const int row = L::WarpTokens * (dw & 1) + (lane >> 2);
   // The two 16-byte chunks' places: the order of a block's halves alternates
   // with the 128 latents.  Eight rows on, the swizzle is the same.
   const uint32_t half = blk & 1;
   const uint32_t at0 = blk * kK8Block + row * 128 + (((2 * jj + half) ^ (row & 7)) << 4);
   const uint32_t at1 = blk * kK8Block + row * 128 + (((2 * jj + (half ^ 1)) ^ (row & 7)) << 4);
+  // The warp's tokens are UnitsEach copy units of the tile, or half of one.
+  constexpr int UnitsEach = L::WarpTokens / L::Unit;
+  static_assert(UnitsEach >= 1 && L::UnitWarps == 4, "a warp reads whole copy units");
+  const int unit0 = UnitsEach * (dw & 1);
   struct Codes {
-    uint4 w[4];
-    uint32_t rel[4];
+    uint4 w[N];
+    uint32_t rel[N];
   };
-  int st = unit % L::Units;  // every PerTile-th copy unit is the warp's
-  int kf = 0;                // tile fetched next
+  int st = unit0 % L::Units;
+  int kf = 0;  // tile fetched next
   auto fetch = [&](Codes& x) -> bool {
-    // The scale warp has seen the copies land.  (Its barriers go by the
-    // unit's place in two tiles: a stage's own barrier would pass phases that
-    // this warp does not wait for.)
-    if (!att_wait(bars + 8 * (L::ScaleFull + (kf & 1) * L::PerTile + unit), (kf >> 1) & 1, s)) return false;
-    ++kf;
-    const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok * kKv4CodeBytes + 64 * blk + 16 * jj;
-    const uint8_t* rel = s.rel + (st * L::Unit + tok) * kKv4Blocks + 4 * blk + jj;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x.rel[i] = rel[8 * i * kKv4Blocks];
-      x.w[i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
+    for (int c = 0; c < UnitsEach; ++c) {
+      // The scale warp has seen the copies land.  (Its barriers go by the
+      // unit's place in two tiles: a stage's own barrier would pass phases
+      // that this warp does not wait for.)
+      if (!att_wait(bars + 8 * (L::ScaleFull + (kf & 1) * L::PerTile + unit0 + c), (kf >> 1) & 1, s)) return false;
+      const int tok = lane >> 2;
+      const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok * kKv4CodeBytes + 64 * blk + 16 * jj;
+      const uint8_t* rel = s.rel + (st * L::Unit + tok) * kKv4Blocks + 4 * blk + jj;
+#pragma unroll
+      for (int i = 0; i < N / UnitsEach; ++i) {
+        x.rel[c * (N / UnitsEach) + i] = rel[8 * i * kKv4Blocks];
+        x.w[c * (N / UnitsEach) + i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+      st = (st + (c + 1 < UnitsEach ? 1 : L::PerTile - UnitsEach + 1)) % L::Units;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
-    st = (st + L::PerTile) % L::Units;
+    ++kf;
     return true;
   };
   Codes cur, nxt;
@@ -315,15 +323,13 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
     if (k > 0 && k + 1 < tiles && !fetch(nxt)) return;
     // the block of the tile two before has been multiplied
     if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + 4 * b + blk), (k / 2 - 1) & 1, s)) return;
-    uint2 lut[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
+      const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
       auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
         const uint32_t m = c & 0x77777777u;
-        lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
-        hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
+        lo = prmt(lut.x, lut.y, m) | (c & 0x80808080u);
+        hi = prmt(lut.x, lut.y, m >> 16) | ((c * 16u) & 0x80808080u);
       };
       uint4 a, c;
       word(cur.w[i].x, a.x, a.y);
@@ -342,99 +348,109 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
 }
 
 // --------------------------------------------------------------------------
-// Warps 21 and 22: one thread each issues the MMAs of the scores and of the
-// output.  Two threads, because each product has to go as soon as its
-// operands are there: with one thread in program order, the output product
-// that frees a K8 tile waited behind the scores of the next one, and the
-// pipeline took 5500 cycles a tile.
+// Warps 13 and 14 issue the MMAs of the scores and of the output.  Two warps,
+// because each product has to go as soon as its operands are there: from one
+// thread in program order, the output product that frees a K8 tile waited
+// behind the scores of the next one.  The whole warp goes through the loop and
+// one lane issues, so that descriptors are computed once a warp: a lone
+// thread's MMAs came 175 cycles apart.
 // --------------------------------------------------------------------------
 
 // What was issued completes before the CTA ends (bar: the warp's own).
-__device__ __forceinline__ void att_drain(uint32_t bar) {
-  umma_commit(bar);
+__device__ __forceinline__ void att_drain(uint32_t bar, bool leader) {
+  if (leader) umma_commit(bar);
   const unsigned long long at = globaltimer_ns();
+#pragma unroll 1
   while (!mbar_try_wait(bar, 0) && globaltimer_ns() - at < kAttWaitNs) {
   }
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
-                                               int t0, int t1) {
+__device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
+                                               uint32_t tmem, int V, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
   constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
+  const bool leader = elect_one();
+  // operands 32 bytes apart along the contraction, blocks of 128 latents behind each other
+  const uint64_t a_k8 = smem_desc_sw128(smem + L::K8, 16, 1024), b_q = smem_desc_sw128(smem + L::Q, 16, 1024);
+  const uint64_t a_rope = smem_desc_sw128(smem + L::Rope, 16, 1024), b_pe = smem_desc_sw128(smem + L::QPe, 16, 1024);
   bool ok = true;
   int k = 0, item = 0;
   for (int t = t0; ok && t < t1; ++item) {
     const AttItem it = att_item(s.prefix, V, t, t1);
     t += it.count;
-    ok = att_wait_one(bars + 8 * L::QFull, item & 1, s);
+    ok = att_wait(bars + 8 * L::QFull, item & 1, s);
+#pragma unroll 1
     for (int n = 0; ok && n < it.count; ++n, ++k) {
       const int b = k & 1, sb = k % L::SBufs;
-      if (k >= L::SBufs) ok = att_wait_one(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
-      if (ok) ok = att_wait_one(bars + 8 * L::RopeFull, k & 1, s);
+      if (k >= L::SBufs) ok = att_wait(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
+      if (ok) ok = att_wait(bars + 8 * L::RopeFull, k & 1, s);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + sb * L::SCols;
+      if (leader) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint64_t ad = smem_desc_sw128(smem + L::Rope + c * 32, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(smem + L::QPe + c * 32, 16, 1024);
-        umma_bf16(d + L::NQ, ad, bd, id_r, c > 0);
+        for (int c = 0; c < 4; ++c) umma_bf16(d + L::NQ, a_rope + 2 * c, b_pe + 2 * c, id_r, c > 0);
+        umma_commit(bars + 8 * L::RopeEmpty);
       }
-      umma_commit(bars + 8 * L::RopeEmpty);
-      const uint32_t k8 = smem + L::K8 + b * kK8Tile;
-#pragma unroll 1
-      for (int i = 0; ok && i < 4; ++i) {
-        ok = att_wait_one(bars + 8 * (L::K8Full + 4 * b + i), (k / 2) & 1, s);
+      const uint64_t a_tile = a_k8 + static_cast<uint64_t>(b * (kK8Tile >> 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ok = att_wait(bars + 8 * (L::K8Full + 4 * b + i), (k / 2) & 1, s);
         if (!ok) break;
         tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint64_t ad = smem_desc_sw128(k8 + i * kK8Block + c * 32, 16, 1024);
-          const uint64_t bd = smem_desc_sw128(smem + L::Q + i * L::QBlock + c * 32, 16, 1024);
-          umma_f8(d, ad, bd, id_s, i + c > 0);
+          for (int c = 0; c < 4; ++c)
+            umma_f8(d, a_tile + i * (kK8Block >> 4) + 2 * c, b_q + i * (L::QBlock >> 4) + 2 * c, id_s, i + c > 0);
         }
       }
       if (!ok) break;
-      umma_commit(bars + 8 * (L::SFull + sb));
+      if (leader) umma_commit(bars + 8 * (L::SFull + sb));
+      __syncwarp();
     }
   }
-  if (!ok) att_drain(bars + 8 * L::Drain);
+  if (!ok) att_drain(bars + 8 * L::Drain, leader);
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, uint32_t tmem, int V,
-                                               int t0, int t1) {
+__device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
+                                               uint32_t tmem, int V, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
+  const bool leader = elect_one();
+  // A: 128 latents, 32 tokens (8-token groups 1024 bytes apart) 4096 on;
+  // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
+  const uint64_t a_k8 = smem_desc_sw128(smem + L::K8, 16, 1024);
+  const uint64_t b_p = smem_desc_plain(smem + L::P, 128, L::PChunk);
   bool ok = true;
   int k = 0, item = 0;
   for (int t = t0; ok && t < t1; ++item) {
     const AttItem it = att_item(s.prefix, V, t, t1);
     t += it.count;
-    if (item > 0) ok = att_wait_one(bars + 8 * L::OEmpty, (item - 1) & 1, s);
+    if (item > 0) ok = att_wait(bars + 8 * L::OEmpty, (item - 1) & 1, s);
+#pragma unroll 1
     for (int n = 0; ok && n < it.count; ++n, ++k) {
-      ok = att_wait_one(bars + 8 * L::PFull, k & 1, s);
+      ok = att_wait(bars + 8 * L::PFull, k & 1, s);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t k8 = smem + L::K8 + (k & 1) * kK8Tile;
-#pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt) {
+      const uint64_t a_tile = a_k8 + static_cast<uint64_t>((k & 1) * (kK8Tile >> 4));
+      if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < kAttTile / 32; ++ks) {
-          // A: 128 latents, tokens 32*ks.. (8-token groups 1024 bytes apart)
-          const uint64_t ad = smem_desc_sw128(k8 + mt * kK8Block + ks * 4096, 16, 1024);
-          // B: 16-row chunks PChunk apart (SBO), 8-token groups 128 apart (LBO)
-          const uint64_t bd = smem_desc_plain(smem + L::P + ks * 512, 128, L::PChunk);
-          umma_f8(tmem + L::OCol + mt * L::NP, ad, bd, id_o, (n == 0 && ks == 0) ? 0u : 1u);
+        for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+          for (int ks = 0; ks < kAttTile / 32; ++ks)
+            umma_f8(tmem + L::OCol + mt * L::NP, a_tile + mt * (kK8Block >> 4) + ks * (4096 >> 4),
+                    b_p + ks * (512 >> 4), id_o, (n == 0 && ks == 0) ? 0u : 1u);
+          umma_commit(bars + 8 * (L::K8Empty + 4 * (k & 1) + mt));
         }
-        umma_commit(bars + 8 * (L::K8Empty + 4 * (k & 1) + mt));
+        umma_commit(bars + 8 * L::PvDone);
       }
-      umma_commit(bars + 8 * L::PvDone);
+      __syncwarp();
     }
   }
-  if (!ok) att_drain(bars + 8 * (L::Drain + 1));
+  if (!ok) att_drain(bars + 8 * (L::Drain + 1), leader);
 }
 
 // --------------------------------------------------------------------------
@@ -573,9 +589,12 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     AttItem next = it;
     if (next_t < t1) next = att_item(s.prefix, V, next_t, t1);
     float top = -INFINITY;  // M of row `lane`
-    float l[R];
+    float l[R], cr[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) l[r] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      l[r] = 0.f;
+      cr[r] = s.cr[turn][r];
+    }
     if (lane < R) mref[lane] = kAttUnseen;
     __syncwarp();
     for (int n = item < 0 ? -1 : 0; n < it.count; ++n) {
@@ -606,16 +625,11 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       for (int hb = 0; hb < R / 16; ++hb) {
         tmem_ld_end(v[hb]);
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(&s.cr[turn][16 * hb + r]);
-          const float cc[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* w = &v[hb][r + q];
-            float d = __uint_as_float(w[0]);
-            if constexpr (!E4) d = fmaf(__uint_as_float(w[16]), 0.0625f, d);  // the second query term
-            y[16 * hb + r + q] = fmaf(fmaf(d, ts, __uint_as_float(w[16 * L::QTerms])), cc[q], et);
-          }
+        for (int r = 0; r < 16; ++r) {
+          const uint32_t* w = &v[hb][r];
+          float d = __uint_as_float(w[0]);
+          if constexpr (!E4) d = fmaf(__uint_as_float(w[16]), 0.0625f, d);  // the second query term
+          y[16 * hb + r] = fmaf(fmaf(d, ts, __uint_as_float(w[16 * L::QTerms])), cr[16 * hb + r], et);
         }
       }
       tc_fence_before();
@@ -627,16 +641,12 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       }
       // Has any row outgrown its reference?  Mostly not: then one barrier
       // tells, and no maximum is taken.
-      bool grown = false;
+      float ref[R], high = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&mref[r]);
-        grown |= y[r] > m.x + (kAttShift + kAttSlack);
-        grown |= y[r + 1] > m.y + (kAttShift + kAttSlack);
-        grown |= y[r + 2] > m.z + (kAttShift + kAttSlack);
-        grown |= y[r + 3] > m.w + (kAttShift + kAttSlack);
-      }
-      if (soft_barrier_any(grown || n == 0)) {
+      for (int r = 0; r < R; r += 4) *reinterpret_cast<float4*>(&ref[r]) = *reinterpret_cast<const float4*>(&mref[r]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) high = fmaxf(high, y[r] - ref[r]);
+      if (soft_barrier_any(high > kAttShift + kAttSlack || n == 0)) {
 #pragma unroll
         for (int r = 0; r < R; r += 4) {
           const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
@@ -660,6 +670,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
           l[r + 1] *= a.y;
           l[r + 2] *= a.z;
           l[r + 3] *= a.w;
+          *reinterpret_cast<float4*>(&ref[r]) = *reinterpret_cast<const float4*>(&mref[r]);
         }
         if (n > 0) {
           att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
@@ -683,9 +694,8 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
         uint32_t t[3][4];
 #pragma unroll
         for (int r = 0; r < 16; r += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&mref[hb + r]);
-          const float e0 = ex2(y[hb + r] - m.x), e1 = ex2(y[hb + r + 1] - m.y), e2 = ex2(y[hb + r + 2] - m.z),
-                      e3 = ex2(y[hb + r + 3] - m.w);
+          const float e0 = ex2(y[hb + r] - ref[hb + r]), e1 = ex2(y[hb + r + 1] - ref[hb + r + 1]),
+                      e2 = ex2(y[hb + r + 2] - ref[hb + r + 2]), e3 = ex2(y[hb + r + 3] - ref[hb + r + 3]);
           l[hb + r] = fmaf(e0, its, l[hb + r]);
           l[hb + r + 1] = fmaf(e1, its, l[hb + r + 1]);
           l[hb + r + 2] = fmaf(e2, its, l[hb + r + 2]);
@@ -861,11 +871,11 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   const uint32_t base = smem_u32(smem);
   // every warpgroup does this, and the shares fit what the launch has
   if (warp < kAttSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SoftRegs));
+    att_set_regs<L::SoftRegs>();
   } else if (warp < kAttLoadWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::CodeRegs));
+    att_set_regs<L::CodeRegs>();
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::OtherRegs));
+    att_set_regs<L::OtherRegs>();
   }
   if (warp < kAttSoftWarps) {
     att_empty_rows<R>(p, s, V);
@@ -878,9 +888,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     } else if (warp == kAttScaleWarp) {
       att_scales<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttScoreWarp) {
-      if ((tid & 31) == 0) att_mma_scores<R, E4>(s, base, bars, tmem, V, t0, t1);
+      att_mma_scores<R, E4>(s, base, bars, tmem, V, t0, t1);
     } else if (warp == kAttOutputWarp) {
-      if ((tid & 31) == 0) att_mma_output<R, E4>(s, base, bars, tmem, V, t0, t1);
+      att_mma_output<R, E4>(s, base, bars, tmem, V, t0, t1);
     }
   }
   tc_fence_before();

@@ -35,13 +35,13 @@
 // in the workspace and the join kernel adds the pieces in order.
 //
 // A CTA is a pipeline of warps:
-//   warp 20      copies pages into shared memory (bulk copies: codes and
+//   warp 12      copies pages into shared memory (bulk copies: codes and
 //                scales in units of 64 tokens, rope rows straight into the
 //                swizzled tile, the cache's layout being that of the tile);
-//   warp 23      scale bytes -> s_t and s_t - s_j, a token per lane;
-//   warps 4-19   codes -> E4M3: a byte permute looks four magnitudes up in
+//   warp 15      scale bytes -> s_t and s_t - s_j, a token per lane;
+//   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
-//   warps 21, 22 one thread each issues the MMAs of scores and output;
+//   warps 13, 14 one thread each issues the MMAs of scores and output;
 //   warps 0-3    queries, softmax (one token per thread), rescaling, output.
 // O stays in tensor memory; it is rescaled only when a row's maximum has
 // grown by more than 2^3.
@@ -53,10 +53,10 @@
 
 namespace mlaqp {
 
-constexpr int kAttThreads = 768;
-constexpr int kAttRegs = 80;    // a thread's at launch: 65536 / 768 in steps of 8
+constexpr int kAttThreads = 512;
+constexpr int kAttRegs = 128;   // a thread's at launch: 65536 / 512
 constexpr int kAttSoftWarps = 4;
-constexpr int kAttDequantWarps = 16;
+constexpr int kAttDequantWarps = 8;
 constexpr int kAttLoadWarp = kAttSoftWarps + kAttDequantWarps;
 constexpr int kAttScoreWarp = kAttLoadWarp + 1;
 constexpr int kAttOutputWarp = kAttLoadWarp + 2;
@@ -122,8 +122,9 @@ struct AttPlan {
   static constexpr int Units = (R == 32 && E4) ? 2 : 3;
   static constexpr int PerTile = kAttTile / Unit;
   static_assert(Units <= 2 * PerTile, "the scale barriers are the units of two tiles, waited for once each");
-  static constexpr int UnitWarps = kAttDequantWarps / PerTile;  // code warps that read a unit
-  static_assert(UnitWarps % 4 == 0, "each block of latents, whole warps");
+  static constexpr int UnitWarps = 4;  // code warps that read a unit: one for each 128 latents
+  static constexpr int WarpTokens = kAttTile / (kAttDequantWarps / 4);  // tokens of a code warp: its share of a block
+
   static constexpr int UnitCodes = Unit * kKv4CodeBytes;
   static constexpr int UnitBytes = UnitCodes + Unit * kKv4Blocks;
   using Shared = AttShared<R, Unit * Units>;
@@ -139,10 +140,9 @@ struct AttPlan {
   static constexpr int Bytes = Misc + static_cast<int>(sizeof(Shared));
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
-  // registers of the softmax, code and other warps, of the six warpgroups' at launch
-  static constexpr int SoftRegs = R == 16 ? 120 : 152, CodeRegs = R == 16 ? 72 : 64, OtherRegs = 72;
-  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 6 * kAttRegs, "registers");
-  static_assert(SoftRegs >= kAttRegs && CodeRegs <= kAttRegs && OtherRegs <= kAttRegs, "raised for one, lowered for the others");
+  // registers of the softmax, code and other warps, of the four warpgroups' at launch
+  static constexpr int SoftRegs = R == 16 ? 128 : 176, CodeRegs = R == 16 ? 128 : 120, OtherRegs = R == 16 ? 128 : 96;
+  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 4 * kAttRegs, "registers");
   // barrier indexes; K8Full and K8Empty: 4 * tile buffer + block of 128 latents
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
                        RopeFull = ScaleFull + 2 * PerTile,
@@ -224,8 +224,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A warpgroup's registers a thread from here on (kAttRegs before).
+template <int N>
+__device__ __forceinline__ void att_set_regs() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "registers");
+  if constexpr (N > kAttRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < kAttRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// True for one lane of the (whole) warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
 }
 
 // Whether the phase of that parity has completed; does not wait.
