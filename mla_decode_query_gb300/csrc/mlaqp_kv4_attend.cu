@@ -64,7 +64,7 @@ struct AttRing {
 };
 
 // --------------------------------------------------------------------------
-// Warp 12: pages into shared memory.
+// Warp 24: pages into shared memory.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, int V,
@@ -215,7 +215,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
 }
 
 // --------------------------------------------------------------------------
-// Warp 15: scale bytes, one token per lane.  s_t = the largest of the 16;
+// Warp 27: scale bytes, one token per lane.  s_t = the largest of the 16;
 // s_t - s_j, at most 31, picks the row of the E4M3 table.  Bytes are taken as
 // pairs of 16-bit numbers; none of the differences borrows.
 // --------------------------------------------------------------------------
@@ -260,95 +260,75 @@ __device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, u
 }
 
 // --------------------------------------------------------------------------
-// Warps 4-11: codes -> E4M3 tile.  Two warps take a block of 128 latents of
-// the tile, a warp 64 tokens of it, a thread eight blocks of 32 latents of
-// eight tokens.  So the output product gives the tile back, and the score
+// Warps 8-23: codes -> E4M3 tile.  Four warps take a block of 128 latents of
+// the tile, a warp 32 tokens of it, a thread four blocks of 32 latents of
+// four tokens.  So the output product gives the tile back, and the score
 // product takes it, block by block, and a warp still has one wait, one fence
-// and one arrival a tile.  (All warps on one block after the other spent 900
-// cycles a block, mostly there; sixteen warps of half the work each spent
-// as many instructions around it as on it.)
+// and one arrival a tile.  (All sixteen warps on one block after the other
+// spent 900 cycles a block, mostly there.)
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
-  const int blk = dw >> 1, jj = lane & 3;              // 128 latents, 32 of them
-  constexpr int N = L::WarpTokens / 8;                 // tokens of a thread: every eighth
-  const int row = L::WarpTokens * (dw & 1) + (lane >> 2);
+  const int blk = dw >> 2, jj = lane & 3;       // 128 latents, 32 of them
+  const int row = 32 * (dw & 3) + (lane >> 2);  // first token of the tile; then every eighth
+  const int unit = 32 * (dw & 3) / L::Unit;     // its copy unit in the tile, and token there
+  const int tok = row % L::Unit;
   // The two 16-byte chunks' places: the order of a block's halves alternates
   // with the 128 latents.  Eight rows on, the swizzle is the same.
   const uint32_t half = blk & 1;
   const uint32_t at0 = blk * kK8Block + row * 128 + (((2 * jj + half) ^ (row & 7)) << 4);
   const uint32_t at1 = blk * kK8Block + row * 128 + (((2 * jj + (half ^ 1)) ^ (row & 7)) << 4);
-  // The warp's tokens are UnitsEach copy units of the tile, or half of one.
-  constexpr int UnitsEach = L::WarpTokens / L::Unit;
-  static_assert(UnitsEach >= 1 && L::UnitWarps == 4, "a warp reads whole copy units");
-  const int unit0 = UnitsEach * (dw & 1);
-  struct Codes {
-    uint4 w[N];
-    uint32_t rel[N];
-  };
-  int st = unit0 % L::Units;
-  int kf = 0;  // tile fetched next
-  auto fetch = [&](Codes& x) -> bool {
-#pragma unroll
-    for (int c = 0; c < UnitsEach; ++c) {
-      // The scale warp has seen the copies land.  (Its barriers go by the
-      // unit's place in two tiles: a stage's own barrier would pass phases
-      // that this warp does not wait for.)
-      if (!att_wait(bars + 8 * (L::ScaleFull + (kf & 1) * L::PerTile + unit0 + c), (kf >> 1) & 1, s)) return false;
-      const int tok = lane >> 2;
-      const uint8_t* raw = smem + L::Raw + st * L::UnitBytes + tok * kKv4CodeBytes + 64 * blk + 16 * jj;
-      const uint8_t* rel = s.rel + (st * L::Unit + tok) * kKv4Blocks + 4 * blk + jj;
-#pragma unroll
-      for (int i = 0; i < N / UnitsEach; ++i) {
-        x.rel[c * (N / UnitsEach) + i] = rel[8 * i * kKv4Blocks];
-        x.w[c * (N / UnitsEach) + i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
-      st = (st + (c + 1 < UnitsEach ? 1 : L::PerTile - UnitsEach + 1)) % L::Units;
-    }
-    ++kf;
-    return true;
-  };
-  Codes cur, nxt;
-  if (!fetch(cur)) return;
+  const uint32_t raw0 = L::Raw + tok * kKv4CodeBytes + 64 * blk + 16 * jj, rel0 = tok * kKv4Blocks + 4 * blk + jj;
+  int st = unit % L::Units;  // every PerTile-th copy unit is the warp's
 #pragma unroll 1
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
     uint8_t* tile = smem + L::K8 + b * kK8Tile;
-    // The next tile's codes, ahead of this one's work, but for the first one:
-    // its successor is only being copied.
-    if (k > 0 && k + 1 < tiles && !fetch(nxt)) return;
+    // The scale warp has seen the copies land.  (Its barriers go by the
+    // unit's place in two tiles: a stage's own barrier would pass phases that
+    // this warp does not wait for.)
+    if (!att_wait(bars + 8 * (L::ScaleFull + b * L::PerTile + unit), (k >> 1) & 1, s)) return;
+    uint4 w[4];
+    uint32_t rel[4];
+    const uint8_t* raw = smem + raw0 + st * L::UnitBytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rel[i] = s.rel[st * L::Unit * kKv4Blocks + rel0 + 8 * i * kKv4Blocks];
+      w[i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+    st = (st + L::PerTile) % L::Units;
+    uint2 lut[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[rel[i]]);
     // the block of the tile two before has been multiplied
     if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + 4 * b + blk), (k / 2 - 1) & 1, s)) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint2 lut = *reinterpret_cast<const uint2*>(s.lut[cur.rel[i]]);
+    for (int i = 0; i < 4; ++i) {
       auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
         const uint32_t m = c & 0x77777777u;
-        lo = prmt(lut.x, lut.y, m) | (c & 0x80808080u);
-        hi = prmt(lut.x, lut.y, m >> 16) | ((c * 16u) & 0x80808080u);
+        lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
+        hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
       };
       uint4 a, c;
-      word(cur.w[i].x, a.x, a.y);
-      word(cur.w[i].y, a.z, a.w);
-      word(cur.w[i].z, c.x, c.y);
-      word(cur.w[i].w, c.z, c.w);
+      word(w[i].x, a.x, a.y);
+      word(w[i].y, a.z, a.w);
+      word(w[i].z, c.x, c.y);
+      word(w[i].w, c.z, c.w);
       *reinterpret_cast<uint4*>(tile + at0 + i * 1024) = a;
       *reinterpret_cast<uint4*>(tile + at1 + i * 1024) = c;
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::K8Full + 4 * b + blk));
-    if (k == 0 && tiles > 1 && !fetch(nxt)) return;
-    cur = nxt;
   }
 }
 
 // --------------------------------------------------------------------------
-// Warps 13 and 14 issue the MMAs of the scores and of the output.  Two warps,
+// Warps 25 and 26 issue the MMAs of the scores and of the output.  Two warps,
 // because each product has to go as soon as its operands are there: from one
 // thread in program order, the output product that frees a K8 tile waited
 // behind the scores of the next one.  The whole warp goes through the loop and
@@ -454,7 +434,7 @@ __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& 
 }
 
 // --------------------------------------------------------------------------
-// Warps 0-3
+// Warps 0-7
 // --------------------------------------------------------------------------
 
 // Queries of row group v into shared memory, and what its rows need (turn:
@@ -463,7 +443,7 @@ template <int R, bool E4>
 __device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int v,
                                           int turn) {
   using L = AttPlan<R, E4>;
-  constexpr int TPR = 128 / R;  // threads per row
+  constexpr int TPR = 128 / L::HalfRows;  // threads per row; each group of four warps sees to its own rows
   const int tid = threadIdx.x;
   const int r = tid / TPR, sub = tid % TPR;
   const int rows = p.q_len * p.H;
@@ -570,8 +550,11 @@ template <int R, bool E4>
 __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars,
                                             uint32_t tmem, int V, int t0, int t1) {
   using L = AttPlan<R, E4>;
+  constexpr int HR = L::HalfRows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+  const int group = warp >> 2, tok = tid & 127;  // half of the rows, token of the tile
+  const int row0 = group * HR;
+  const uint32_t here = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + row0;  // first row's columns
   float* mref = s.mref[warp];
   float* alpha = s.alpha[warp];
   // A wait that runs out (then all later ones do at once) does not end the
@@ -584,77 +567,77 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     const int turn = item & 1;
     // every warp has left the row group before (what follows reuses its
     // places), and this one's rows are known
-    soft_barrier();
+    soft_barrier(group);
     const int next_t = t + it.count;
     AttItem next = it;
     if (next_t < t1) next = att_item(s.prefix, V, next_t, t1);
     float top = -INFINITY;  // M of row `lane`
-    float l[R], cr[R];
+    float l[HR], cr[HR];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < HR; ++r) {
       l[r] = 0.f;
-      cr[r] = s.cr[turn][r];
+      cr[r] = s.cr[turn][row0 + r];
     }
-    if (lane < R) mref[lane] = kAttUnseen;
+    if (lane < HR) mref[lane] = kAttUnseen;
     __syncwarp();
     for (int n = item < 0 ? -1 : 0; n < it.count; ++n) {
-      const int kb = k % kAttScaleTiles, sb = k % L::SBufs;
+      const int sb = k % L::SBufs;
       if (n >= 0) att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s);
       // the scores of the row group's last tile are in: its queries are done with
       if (n == it.count - 1 && next_t < t1) att_query<R, E4>(p, s, smem, bars, next.v, turn ^ 1);
       if (n < 0) continue;
       tc_fence_after();
       // the scores, in flight while the scales are looked at
-      uint32_t v[R / 16][(L::QTerms + 1) * 16];
+      uint32_t v[(L::QTerms + 1) * HR];
 #pragma unroll
-      for (int hb = 0; hb < R / 16; ++hb)
-#pragma unroll
-        for (int part = 0; part <= L::QTerms; ++part)
-          tmem_ld16_begin(tmem + lanes + sb * L::SCols + 16 * hb + part * R, &v[hb][16 * part]);
+      for (int part = 0; part <= L::QTerms; ++part)
+        tmem_ld_begin<HR>(here + sb * L::SCols + part * R, &v[HR * part]);
       att_wait(bars + 8 * (L::K8Full + 4 * (k & 1)), (k / 2) & 1, s);  // the tile's scales are in, too
-      const uint32_t sm = s.smax[kb][tid];
+      const uint32_t sm = s.smax[k % kAttScaleTiles][tok];
       const float ts = sm == kKv4ScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((sm - 6u) << 23);
       const float its = __uint_as_float((260u - sm) << 23);
       const float et = static_cast<float>(static_cast<int>(sm) - 133);
       const int64_t tile_tok = static_cast<int64_t>(it.first + n) * kAttTile;
       const uint32_t mask = s.tmask[k % kAttMaskTiles];
-      const bool whole = mask == 0xFFu && tile_tok + kAttTile <= s.limit[turn][0];
-      const bool here = mask >> (tid >> 4) & 1;
-      float y[R];
+      const bool whole = mask == 0xFFu && tile_tok + kAttTile <= s.limit[turn][row0];
+      float y[HR];
+      tmem_ld_end(v);
 #pragma unroll
-      for (int hb = 0; hb < R / 16; ++hb) {
-        tmem_ld_end(v[hb]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const uint32_t* w = &v[hb][r];
-          float d = __uint_as_float(w[0]);
-          if constexpr (!E4) d = fmaf(__uint_as_float(w[16]), 0.0625f, d);  // the second query term
-          y[16 * hb + r] = fmaf(fmaf(d, ts, __uint_as_float(w[16 * L::QTerms])), cr[16 * hb + r], et);
-        }
+      for (int r = 0; r < HR; ++r) {
+        float d = __uint_as_float(v[r]);
+        if constexpr (!E4) d = fmaf(__uint_as_float(v[HR + r]), 0.0625f, d);  // the second query term
+        y[r] = fmaf(fmaf(d, ts, __uint_as_float(v[HR * L::QTerms + r])), cr[r], et);
       }
       tc_fence_before();
       mbar_arrive(bars + 8 * (L::SEmpty + sb));
       if (!whole) {
+        const bool copied = mask >> (tok >> 4) & 1;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (!here || tile_tok + tid >= s.limit[turn][r]) y[r] = -INFINITY;
+        for (int r = 0; r < HR; ++r)
+          if (!copied || tile_tok + tok >= s.limit[turn][row0 + r]) y[r] = -INFINITY;
       }
       // Has any row outgrown its reference?  Mostly not: then one barrier
       // tells, and no maximum is taken.
-      float ref[R], high = -INFINITY;
+      float x[HR], high = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < R; r += 4) *reinterpret_cast<float4*>(&ref[r]) = *reinterpret_cast<const float4*>(&mref[r]);
+      for (int r = 0; r < HR; r += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&mref[r]);
+        x[r] = y[r] - m.x;
+        x[r + 1] = y[r + 1] - m.y;
+        x[r + 2] = y[r + 2] - m.z;
+        x[r + 3] = y[r + 3] - m.w;
+        high = fmaxf(fmaxf(high, fmaxf(x[r], x[r + 1])), fmaxf(x[r + 2], x[r + 3]));
+      }
+      if (soft_barrier_any(group, high > kAttShift + kAttSlack || n == 0)) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) high = fmaxf(high, y[r] - ref[r]);
-      if (soft_barrier_any(high > kAttShift + kAttSlack || n == 0)) {
-#pragma unroll
-        for (int r = 0; r < R; r += 4) {
+        for (int r = 0; r < HR; r += 4) {
           const float4 m = make_float4(warp_max(y[r]), warp_max(y[r + 1]), warp_max(y[r + 2]), warp_max(y[r + 3]));
           if (lane == 0) *reinterpret_cast<float4*>(&s.wmax[warp][r]) = m;
         }
-        soft_barrier();
-        if (lane < R) {
-          const float tm = fmaxf(fmaxf(s.wmax[0][lane], s.wmax[1][lane]), fmaxf(s.wmax[2][lane], s.wmax[3][lane]));
+        soft_barrier(group);
+        if (lane < HR) {
+          const float(*wm)[HR] = &s.wmax[4 * group];
+          const float tm = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
           const bool up = tm > top;
           alpha[lane] = up ? (top == -INFINITY ? 0.f : ex2(top - tm)) : 1.f;
           if (up) {
@@ -664,64 +647,70 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
         }
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
+        for (int r = 0; r < HR; r += 4) {
           const float4 a = *reinterpret_cast<const float4*>(&alpha[r]);
+          const float4 m = *reinterpret_cast<const float4*>(&mref[r]);
           l[r] *= a.x;
           l[r + 1] *= a.y;
           l[r + 2] *= a.z;
           l[r + 3] *= a.w;
-          *reinterpret_cast<float4*>(&ref[r]) = *reinterpret_cast<const float4*>(&mref[r]);
+          x[r] = y[r] - m.x;
+          x[r + 1] = y[r + 1] - m.y;
+          x[r + 2] = y[r + 2] - m.z;
+          x[r + 3] = y[r + 3] - m.w;
         }
         if (n > 0) {
           att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4 * L::NP; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem + lanes + L::OCol + c, o);
-            const float* a = &alpha[c % R];
+          for (int c = 0; c < 12; ++c) {  // four blocks of latents, three terms
+            const uint32_t at = here + L::OCol + c * R;
+            uint32_t o[HR];
+            tmem_ld_begin<HR>(at, o);
+            tmem_ld_end(o);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * a[r]);
-            tmem_st16(tmem + lanes + L::OCol + c, o);
+            for (int r = 0; r < HR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+            tmem_st<HR>(at, o);
           }
           tmem_wait_st();
         }
       }
       if (k > 0) att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);  // P is free
-      uint8_t* ps = smem + L::P + tid * 16;
+      uint32_t terms[3][HR / 4];
 #pragma unroll
-      for (int hb = 0; hb < R; hb += 16) {
-        uint32_t t[3][4];
+      for (int r = 0; r < HR; r += 4) {
+        const float e0 = ex2(x[r]), e1 = ex2(x[r + 1]), e2 = ex2(x[r + 2]), e3 = ex2(x[r + 3]);
+        l[r] = fmaf(e0, its, l[r]);
+        l[r + 1] = fmaf(e1, its, l[r + 1]);
+        l[r + 2] = fmaf(e2, its, l[r + 2]);
+        l[r + 3] = fmaf(e3, its, l[r + 3]);
+        // three E5M2 terms: the top bytes of FP16 are E5M2, truncated; the
+        // differences are exact, the last term is rounded
+        __half2 a = __floats2half2_rn(e0, e1), c = __floats2half2_rn(e2, e3);
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float e0 = ex2(y[hb + r] - ref[hb + r]), e1 = ex2(y[hb + r + 1] - ref[hb + r + 1]),
-                      e2 = ex2(y[hb + r + 2] - ref[hb + r + 2]), e3 = ex2(y[hb + r + 3] - ref[hb + r + 3]);
-          l[hb + r] = fmaf(e0, its, l[hb + r]);
-          l[hb + r + 1] = fmaf(e1, its, l[hb + r + 1]);
-          l[hb + r + 2] = fmaf(e2, its, l[hb + r + 2]);
-          l[hb + r + 3] = fmaf(e3, its, l[hb + r + 3]);
-          // three E5M2 terms: the top bytes of FP16 are E5M2, truncated; the
-          // differences are exact, the last term is rounded
-          __half2 a = __floats2half2_rn(e0, e1), c = __floats2half2_rn(e2, e3);
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            uint32_t au = *reinterpret_cast<uint32_t*>(&a), cu = *reinterpret_cast<uint32_t*>(&c);
-            if (q == 2) {
-              au += 0x00800080u;
-              cu += 0x00800080u;
-            }
-            t[q][r / 4] = prmt(au, cu, 0x7531u);
-            if (q < 2) {
-              uint32_t ah = au & 0xFF00FF00u, ch = cu & 0xFF00FF00u;
-              a = __hsub2(a, *reinterpret_cast<__half2*>(&ah));
-              c = __hsub2(c, *reinterpret_cast<__half2*>(&ch));
-            }
+        for (int q = 0; q < 3; ++q) {
+          uint32_t au = *reinterpret_cast<uint32_t*>(&a), cu = *reinterpret_cast<uint32_t*>(&c);
+          if (q == 2) {
+            au += 0x00800080u;
+            cu += 0x00800080u;
+          }
+          terms[q][r / 4] = prmt(au, cu, 0x7531u);
+          if (q < 2) {
+            uint32_t ah = au & 0xFF00FF00u, ch = cu & 0xFF00FF00u;
+            a = __hsub2(a, *reinterpret_cast<__half2*>(&ah));
+            c = __hsub2(c, *reinterpret_cast<__half2*>(&ch));
           }
         }
+      }
+      // 16 rows of a token lie side by side: half of that, or one of two
+      uint8_t* ps = smem + L::P + tok * 16 + (HR == 8 ? group * 8 : group * L::PChunk);
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-          *reinterpret_cast<uint4*>(ps + (q * (R / 16) + hb / 16) * L::PChunk) =
-              make_uint4(t[q][0], t[q][1], t[q][2], t[q][3]);
+      for (int q = 0; q < 3; ++q) {
+        uint8_t* to = ps + q * (R / 16) * L::PChunk;
+        if constexpr (HR == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(terms[q][0], terms[q][1]);
+        else
+          *reinterpret_cast<uint4*>(to) = make_uint4(terms[q][0], terms[q][1], terms[q][HR / 4 - 2], terms[q][HR / 4 - 1]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -738,14 +727,15 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     const bool complete = it.count == tiles;
     float mine = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < HR; ++r) {
       float v = l[r];
 #pragma unroll
       for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
       if (lane == r) mine = v;
     }
-    if (lane < R) s.wmax[warp][lane] = mine;
-    soft_barrier();
+    soft_barrier(group);  // the maxima of the last tile have been read
+    if (lane < HR) s.wmax[warp][lane] = mine;
+    soft_barrier(group);
     const bool done = att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
     if (!done || *reinterpret_cast<volatile int*>(&s.fail)) {
       t = next_t;
@@ -759,46 +749,49 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       part = reinterpret_cast<float*>(p.ws) + slot * att_slot_floats<R>();
     }
     __syncwarp();
-    if (lane < R) {
-      const float sum = (s.wmax[0][lane] + s.wmax[1][lane]) + (s.wmax[2][lane] + s.wmax[3][lane]);
+    if (lane < HR) {
+      const float(*ws)[HR] = &s.wmax[4 * group];
+      const float sum = (ws[0][lane] + ws[1][lane]) + (ws[2][lane] + ws[3][lane]);
       const float m = mref[lane];
-      const int64_t xo = s.xoff[turn][lane];
+      const int row = row0 + lane;
+      const int64_t xo = s.xoff[turn][row];
+      const bool first = (warp & 3) == 0;
       if (complete) {
-        const bool none = s.limit[turn][lane] <= 0;
+        const bool none = s.limit[turn][row] <= 0;
         alpha[lane] = none ? 0.f : 1.f / sum;
-        if (warp == 0 && xo >= 0 && p.lse) p.lse[s.lseoff[turn][lane]] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-      } else if (warp == 0) {
-        part[R * kLatent + lane] = top == -INFINITY ? top : m;
-        part[R * kLatent + R + lane] = sum;
+        if (first && xo >= 0 && p.lse)
+          p.lse[s.lseoff[turn][row]] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      } else if (first) {
+        part[R * kLatent + row] = top == -INFINITY ? top : m;
+        part[R * kLatent + R + row] = sum;
       }
     }
     __syncwarp();
 #pragma unroll 1
     for (int mt = 0; mt < 4; ++mt) {
-      const int col = mt * 128 + 32 * warp + lane;
+      const int col = mt * 128 + 32 * (warp & 3) + lane;
+      uint32_t v[3 * HR];
+      const uint32_t d = here + L::OCol + mt * L::NP;
 #pragma unroll
-      for (int hb = 0; hb < R; hb += 16) {
-        uint32_t v[48];
-        const uint32_t d = tmem + lanes + L::OCol + mt * L::NP + hb;
-        tmem_ld3x16(d, d + R, d + 2 * R, v);
-        float o[16];
+      for (int q = 0; q < 3; ++q) tmem_ld_begin<HR>(d + q * R, &v[q * HR]);
+      tmem_ld_end(v);
+      float o[HR];
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          o[r] = __uint_as_float(v[r]) + (__uint_as_float(v[16 + r]) + __uint_as_float(v[32 + r]));
-        if (!complete) {
+      for (int r = 0; r < HR; ++r)
+        o[r] = __uint_as_float(v[r]) + (__uint_as_float(v[HR + r]) + __uint_as_float(v[2 * HR + r]));
+      if (!complete) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) part[(hb + r) * kLatent + col] = o[r];
-        } else {
-          // two rows at a time: even lanes take the first row's two latents, odd lanes the second's
+        for (int r = 0; r < HR; ++r) part[(row0 + r) * kLatent + col] = o[r];
+      } else {
+        // two rows at a time: even lanes take the first row's two latents, odd lanes the second's
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const float a = o[r] * alpha[hb + r], c = o[r + 1] * alpha[hb + r + 1];
-            const bool odd = lane & 1;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-            const int64_t xo = s.xoff[turn][hb + r + (odd ? 1 : 0)];
-            const uint32_t two = odd ? pack_bf16x2(c, got) : pack_bf16x2(got, a);
-            if (xo >= 0) *reinterpret_cast<uint32_t*>(p.x + xo + (col & ~1)) = two;
-          }
+        for (int r = 0; r < HR; r += 2) {
+          const float a = o[r] * alpha[r], c = o[r + 1] * alpha[r + 1];
+          const bool odd = lane & 1;
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+          const int64_t xo = s.xoff[turn][row0 + r + (odd ? 1 : 0)];
+          const uint32_t two = odd ? pack_bf16x2(c, got) : pack_bf16x2(got, a);
+          if (xo >= 0) *reinterpret_cast<uint32_t*>(p.x + xo + (col & ~1)) = two;
         }
       }
     }
@@ -817,7 +810,7 @@ __device__ __forceinline__ void att_empty_rows(const Kv4AttendParams& p, const A
   for (int v = blockIdx.x; v < V; v += gridDim.x) {
     if (s.prefix[v + 1] != s.prefix[v]) continue;
     const int r0 = (v % groups) * R, n = min(R, rows - r0);
-    for (int e = threadIdx.x; e < n * 64; e += 128) {
+    for (int e = threadIdx.x; e < n * 64; e += 32 * kAttSoftWarps) {
       const int rr = r0 + e / 64;
       const int64_t m = static_cast<int64_t>(v / groups) * p.q_len + rr / p.H;
       st_u128(p.x + m * p.x_ts + (rr % p.H) * kLatent + 8 * (e % 64), make_uint4(0, 0, 0, 0));
@@ -845,7 +838,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     uint32_t count = 1;
     if (tid >= L::RawEmpty && tid < L::ScaleFull) count = L::UnitWarps;
     if (tid >= L::K8Full && tid < L::K8Empty) count = kAttDequantWarps / 4;
-    if ((tid >= L::SEmpty && tid <= L::PFull) || tid == L::QFull || tid == L::OEmpty) count = 128;
+    if ((tid >= L::SEmpty && tid <= L::PFull) || tid == L::QFull || tid == L::OEmpty) count = 32 * kAttSoftWarps;
     mbar_init(bars + 8 * tid, count);
     fence_barrier_init();
   }

@@ -35,14 +35,15 @@
 // in the workspace and the join kernel adds the pieces in order.
 //
 // A CTA is a pipeline of warps:
-//   warp 12      copies pages into shared memory (bulk copies: codes and
+//   warp 24      copies pages into shared memory (bulk copies: codes and
 //                scales in units of 64 tokens, rope rows straight into the
 //                swizzled tile, the cache's layout being that of the tile);
-//   warp 15      scale bytes -> s_t and s_t - s_j, a token per lane;
-//   warps 4-11   codes -> E4M3: a byte permute looks four magnitudes up in
+//   warp 27      scale bytes -> s_t and s_t - s_j, a token per lane;
+//   warps 8-23   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
-//   warps 13, 14 one thread each issues the MMAs of scores and output;
-//   warps 0-3    queries, softmax (one token per thread), rescaling, output.
+//   warps 25, 26 issue the MMAs of scores and output;
+//   warps 0-7    queries, softmax (one token and half of the rows per
+//                thread), rescaling, output.
 // O stays in tensor memory; it is rescaled only when a row's maximum has
 // grown by more than 2^3.
 #pragma once
@@ -53,10 +54,10 @@
 
 namespace mlaqp {
 
-constexpr int kAttThreads = 512;
-constexpr int kAttRegs = 128;   // a thread's at launch: 65536 / 512
-constexpr int kAttSoftWarps = 4;
-constexpr int kAttDequantWarps = 8;
+constexpr int kAttThreads = 896;
+constexpr int kAttRegs = 72;    // a thread's at launch: 65536 / 896 in steps of 8
+constexpr int kAttSoftWarps = 8;   // two groups of four, each with half of the rows
+constexpr int kAttDequantWarps = 16;
 constexpr int kAttLoadWarp = kAttSoftWarps + kAttDequantWarps;
 constexpr int kAttScoreWarp = kAttLoadWarp + 1;
 constexpr int kAttOutputWarp = kAttLoadWarp + 2;
@@ -92,9 +93,10 @@ struct AttShared : AttSchedule {
   uint32_t tmem;
   alignas(8) uint32_t lut[32][2];           // E4M3 of the 8 magnitudes * 2^(6-k)
   alignas(16) uint8_t rel[Ring * kKv4Blocks];  // s_t - s_j of the copy units, at most 31
-  alignas(16) float wmax[kAttSoftWarps][R];
-  alignas(16) float mref[kAttSoftWarps][R];  // M_r - 12, or kAttUnseen
-  alignas(16) float alpha[kAttSoftWarps][R];
+  // by warp, for its half of the rows
+  alignas(16) float wmax[kAttSoftWarps][R / 2];
+  alignas(16) float mref[kAttSoftWarps][R / 2];  // M_r - 12, or kAttUnseen
+  alignas(16) float alpha[kAttSoftWarps][R / 2];
   // of the row group at hand and the next one, by turns
   alignas(16) float cr[2][R];               // C_r
   int limit[2][R];                          // visible tokens of a row
@@ -122,7 +124,8 @@ struct AttPlan {
   static constexpr int Units = (R == 32 && E4) ? 2 : 3;
   static constexpr int PerTile = kAttTile / Unit;
   static_assert(Units <= 2 * PerTile, "the scale barriers are the units of two tiles, waited for once each");
-  static constexpr int UnitWarps = 4;  // code warps that read a unit: one for each 128 latents
+  static constexpr int UnitWarps = kAttDequantWarps / PerTile;  // code warps that read a unit
+  static constexpr int HalfRows = R / 2;                         // rows of a softmax warp
   static constexpr int WarpTokens = kAttTile / (kAttDequantWarps / 4);  // tokens of a code warp: its share of a block
 
   static constexpr int UnitCodes = Unit * kKv4CodeBytes;
@@ -140,9 +143,9 @@ struct AttPlan {
   static constexpr int Bytes = Misc + static_cast<int>(sizeof(Shared));
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
-  // registers of the softmax, code and other warps, of the four warpgroups' at launch
-  static constexpr int SoftRegs = R == 16 ? 128 : 176, CodeRegs = R == 16 ? 128 : 120, OtherRegs = R == 16 ? 128 : 96;
-  static_assert(SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 4 * kAttRegs, "registers");
+  // registers of the softmax, code and other warps, of the seven warpgroups' at launch
+  static constexpr int SoftRegs = R == 16 ? 96 : 120, CodeRegs = R == 16 ? 56 : 48, OtherRegs = R == 16 ? 88 : 72;
+  static_assert(2 * SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 7 * kAttRegs, "registers");
   // barrier indexes; K8Full and K8Empty: 4 * tile buffer + block of 128 latents
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
                        RopeFull = ScaleFull + 2 * PerTile,
@@ -179,49 +182,45 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
       : "memory");
 }
 
-#define MLAQP_R16(r, o)                                                                                               \
-  "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]),        \
-      "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),              \
-      "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
-
-// 16 columns of this thread's TMEM lane, not there before tmem_ld_end().
-__device__ __forceinline__ void tmem_ld16_begin(uint32_t a, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : MLAQP_R16(r, 0)
-      : "r"(a)
-      : "memory");
+// N (8 or 16) columns of this thread's TMEM lane: begun, not there before
+// tmem_ld_end(), which makes the registers depend on the wait.
+#define MLAQP_R8(c, r, o) \
+  c(r[o]), c(r[o + 1]), c(r[o + 2]), c(r[o + 3]), c(r[o + 4]), c(r[o + 5]), c(r[o + 6]), c(r[o + 7])
+template <int N>
+__device__ __forceinline__ void tmem_ld_begin(uint32_t a, uint32_t* r) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : MLAQP_R8("=r", r, 0)
+                 : "r"(a)
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : MLAQP_R8("=r", r, 0), MLAQP_R8("=r", r, 8)
+        : "r"(a)
+        : "memory");
 }
-// Waits for the loads begun and makes their registers depend on it.
 template <int N>
 __device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-// 16 columns each from three places of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld3x16(uint32_t a, uint32_t b, uint32_t c, uint32_t (&r)[48]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%48];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%49];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%50];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : MLAQP_R16(r, 0), MLAQP_R16(r, 16), MLAQP_R16(r, 32)
-      : "r"(a), "r"(b), "r"(c)
-      : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16, "columns");
+  if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::MLAQP_R8("r", r, 0), "r"(a)
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::MLAQP_R8("r", r, 0),
+        MLAQP_R8("r", r, 8), "r"(a)
+        : "memory");
 }
-#undef MLAQP_R16
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
+#undef MLAQP_R8
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A warpgroup's registers a thread from here on (kAttRegs before).
@@ -266,19 +265,21 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
-// Barrier of the four softmax warps; the second form tells whether any thread
-// says yes.  Every one of these warps passes every barrier, also after a wait
-// has run out.
-__device__ __forceinline__ void soft_barrier() { asm volatile("barrier.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool soft_barrier_any(bool mine) {
+// Barrier of a group of four softmax warps (group 0 or 1); the second form
+// tells whether any thread says yes.  Every one of these warps passes every
+// barrier, also after a wait has run out.
+__device__ __forceinline__ void soft_barrier(int group) {
+  asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+__device__ __forceinline__ bool soft_barrier_any(int group, bool mine) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.or.pred q, 1, 128, p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.red.or.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"(static_cast<uint32_t>(mine))
+      : "r"(1 + group), "r"(static_cast<uint32_t>(mine))
       : "memory");
   return any != 0;
 }
