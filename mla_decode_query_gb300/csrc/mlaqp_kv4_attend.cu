@@ -64,7 +64,7 @@ struct AttRing {
 };
 
 // --------------------------------------------------------------------------
-// Warp 24: pages into shared memory.
+// Warp 16: pages into shared memory.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, int V,
@@ -123,18 +123,22 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   };
   // The copy stage at hand is empty (or a wait ran out: false); tiles up to
   // `tile` may have their rope rows copied meanwhile.
+  auto stage_free = [&]() {
+    return u < L::Units || __all_sync(0xffffffffu, mbar_test(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1));
+  };
   auto wait_stage = [&](int tile) -> bool {
+    if (stage_free()) return true;
     const unsigned long long t_in = globaltimer_ns();
 #pragma unroll 1
-    while (true) {
-      const bool rope = kr <= tile && rope_free();
-      const bool stage = u < L::Units || mbar_test(bars + 8 * (L::RawEmpty + ring.at), ring.parity ^ 1);
-      if (__all_sync(0xffffffffu, rope)) load_rope();
-      if (__all_sync(0xffffffffu, stage)) return true;
-      const bool late = globaltimer_ns() - t_in > kAttWaitNs;
-      if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
-      if (late) *reinterpret_cast<volatile int*>(&s.fail) = 1;
-      if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(&s.fail))) return false;
+    for (int i = 1;; ++i) {
+      if (kr <= tile && __all_sync(0xffffffffu, rope_free())) load_rope();
+      if (stage_free()) return true;
+      if ((i & 63) == 0) {
+        const bool late = globaltimer_ns() - t_in > kAttWaitNs;
+        if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
+        if (late) *reinterpret_cast<volatile int*>(&s.fail) = 1;
+        if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(&s.fail))) return false;
+      }
     }
   };
   bool ok = true;
@@ -181,6 +185,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
         s.tmask[k % kAttMaskTiles] = mask;
       }
       __syncwarp();
+      if (__all_sync(0xffffffffu, rope_free())) load_rope();
 #pragma unroll 1
       for (int q = 0; q < L::PerTile; ++q) {
         const int e = q << kLog >> shift;  // the (first) page of the unit in the tile
@@ -215,7 +220,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
 }
 
 // --------------------------------------------------------------------------
-// Warp 27: scale bytes, one token per lane.  s_t = the largest of the 16;
+// Warp 19: scale bytes, one token per lane.  s_t = the largest of the 16;
 // s_t - s_j, at most 31, picks the row of the E4M3 table.  Bytes are taken as
 // pairs of 16-bit numbers; none of the differences borrows.
 // --------------------------------------------------------------------------
@@ -260,21 +265,23 @@ __device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, u
 }
 
 // --------------------------------------------------------------------------
-// Warps 8-23: codes -> E4M3 tile.  Four warps take a block of 128 latents of
-// the tile, a warp 32 tokens of it, a thread four blocks of 32 latents of
-// four tokens.  So the output product gives the tile back, and the score
-// product takes it, block by block, and a warp still has one wait, one fence
-// and one arrival a tile.  (All sixteen warps on one block after the other
-// spent 900 cycles a block, mostly there.)
+// Code warps: codes -> E4M3 tile.  A quarter of them takes a block of 128
+// latents of the tile, a warp WarpTokens of its tokens, a thread a block of 32
+// latents of every eighth token.  So the output product gives the tile back,
+// and the score product takes it, block by block, and a warp still has one
+// wait, one fence and one arrival a tile.  (All warps on one block after the
+// other spent 900 cycles a block, mostly there.)
 // --------------------------------------------------------------------------
 template <int R, bool E4>
 __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars, int tiles) {
   using L = AttPlan<R, E4>;
+  constexpr int N = L::WarpTokens / 8;                                      // tokens of a thread
+  constexpr int Parts = L::WarpTokens > L::Unit ? L::WarpTokens / L::Unit : 1;  // copy units of a warp
+  constexpr int Each = N / Parts;
   const int lane = threadIdx.x & 31, dw = (threadIdx.x >> 5) - kAttSoftWarps;
-  const int blk = dw >> 2, jj = lane & 3;       // 128 latents, 32 of them
-  const int row = 32 * (dw & 3) + (lane >> 2);  // first token of the tile; then every eighth
-  const int unit = 32 * (dw & 3) / L::Unit;     // its copy unit in the tile, and token there
-  const int tok = row % L::Unit;
+  const int blk = dw / (kAttDequantWarps / 4), jj = lane & 3;  // 128 latents, 32 of them
+  const int row = L::WarpTokens * (dw % (kAttDequantWarps / 4)) + (lane >> 2);
+  const int unit = row / L::Unit, tok = row % L::Unit;         // its (first) copy unit in the tile, token there
   // The two 16-byte chunks' places: the order of a block's halves alternates
   // with the 128 latents.  Eight rows on, the swizzle is the same.
   const uint32_t half = blk & 1;
@@ -286,40 +293,46 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
   for (int k = 0; k < tiles; ++k) {
     const int b = k & 1;
     uint8_t* tile = smem + L::K8 + b * kK8Tile;
-    // The scale warp has seen the copies land.  (Its barriers go by the
-    // unit's place in two tiles: a stage's own barrier would pass phases that
-    // this warp does not wait for.)
-    if (!att_wait(bars + 8 * (L::ScaleFull + b * L::PerTile + unit), (k >> 1) & 1, s)) return;
-    uint4 w[4];
-    uint32_t rel[4];
-    const uint8_t* raw = smem + raw0 + st * L::UnitBytes;
+    uint4 w[N];
+    uint32_t rel[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rel[i] = s.rel[st * L::Unit * kKv4Blocks + rel0 + 8 * i * kKv4Blocks];
-      w[i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
+    for (int c = 0; c < Parts; ++c) {
+      // The scale warp has seen the copies land.  (Its barriers go by the
+      // unit's place in two tiles: a stage's own barrier would pass phases
+      // that this warp does not wait for.)
+      if (!att_wait(bars + 8 * (L::ScaleFull + b * L::PerTile + unit + c), (k >> 1) & 1, s)) return;
+      const uint8_t* raw = smem + raw0 + st * L::UnitBytes;
+#pragma unroll
+      for (int i = 0; i < Each; ++i) {
+        rel[c * Each + i] = s.rel[st * L::Unit * kKv4Blocks + rel0 + 8 * i * kKv4Blocks];
+        w[c * Each + i] = *reinterpret_cast<const uint4*>(raw + 8 * i * kKv4CodeBytes);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
+      st = (st + (c + 1 < Parts ? 1 : L::PerTile - Parts + 1)) % L::Units;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (L::RawEmpty + st));
-    st = (st + L::PerTile) % L::Units;
-    uint2 lut[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[rel[i]]);
     // the block of the tile two before has been multiplied
     if (k >= 2 && !att_wait(bars + 8 * (L::K8Empty + 4 * b + blk), (k / 2 - 1) & 1, s)) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
-        const uint32_t m = c & 0x77777777u;
-        lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
-        hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
-      };
-      uint4 a, c;
-      word(w[i].x, a.x, a.y);
-      word(w[i].y, a.z, a.w);
-      word(w[i].z, c.x, c.y);
-      word(w[i].w, c.z, c.w);
-      *reinterpret_cast<uint4*>(tile + at0 + i * 1024) = a;
-      *reinterpret_cast<uint4*>(tile + at1 + i * 1024) = c;
+    for (int i0 = 0; i0 < N; i0 += 4) {
+      uint2 lut[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lut[i] = *reinterpret_cast<const uint2*>(s.lut[rel[i0 + i]]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        auto word = [&](uint32_t c, uint32_t& lo, uint32_t& hi) {
+          const uint32_t m = c & 0x77777777u;
+          lo = prmt(lut[i].x, lut[i].y, m) | (c & 0x80808080u);
+          hi = prmt(lut[i].x, lut[i].y, m >> 16) | ((c * 16u) & 0x80808080u);
+        };
+        uint4 a, c;
+        word(w[i0 + i].x, a.x, a.y);
+        word(w[i0 + i].y, a.z, a.w);
+        word(w[i0 + i].z, c.x, c.y);
+        word(w[i0 + i].w, c.z, c.w);
+        *reinterpret_cast<uint4*>(tile + at0 + (i0 + i) * 1024) = a;
+        *reinterpret_cast<uint4*>(tile + at1 + (i0 + i) * 1024) = c;
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -328,7 +341,7 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
 }
 
 // --------------------------------------------------------------------------
-// Warps 25 and 26 issue the MMAs of the scores and of the output.  Two warps,
+// Warps 17 and 18 issue the MMAs of the scores and of the output.  Two warps,
 // because each product has to go as soon as its operands are there: from one
 // thread in program order, the output product that frees a K8 tile waited
 // behind the scores of the next one.  The whole warp goes through the loop and

@@ -35,13 +35,13 @@
 // in the workspace and the join kernel adds the pieces in order.
 //
 // A CTA is a pipeline of warps:
-//   warp 24      copies pages into shared memory (bulk copies: codes and
+//   warp 16      copies pages into shared memory (bulk copies: codes and
 //                scales in units of 64 tokens, rope rows straight into the
 //                swizzled tile, the cache's layout being that of the tile);
-//   warp 27      scale bytes -> s_t and s_t - s_j, a token per lane;
-//   warps 8-23   codes -> E4M3: a byte permute looks four magnitudes up in
+//   warp 19      scale bytes -> s_t and s_t - s_j, a token per lane;
+//   warps 8-15   codes -> E4M3: a byte permute looks four magnitudes up in
 //                the eight values of their block's scale;
-//   warps 25, 26 issue the MMAs of scores and output;
+//   warps 17, 18 issue the MMAs of scores and output;
 //   warps 0-7    queries, softmax (one token and half of the rows per
 //                thread), rescaling, output.
 // O stays in tensor memory; it is rescaled only when a row's maximum has
@@ -54,10 +54,10 @@
 
 namespace mlaqp {
 
-constexpr int kAttThreads = 896;
-constexpr int kAttRegs = 72;    // a thread's at launch: 65536 / 896 in steps of 8
+constexpr int kAttThreads = 640;
+constexpr int kAttRegs = 96;    // a thread's at launch: 65536 / 640 in steps of 8
 constexpr int kAttSoftWarps = 8;   // two groups of four, each with half of the rows
-constexpr int kAttDequantWarps = 16;
+constexpr int kAttDequantWarps = 8;
 constexpr int kAttLoadWarp = kAttSoftWarps + kAttDequantWarps;
 constexpr int kAttScoreWarp = kAttLoadWarp + 1;
 constexpr int kAttOutputWarp = kAttLoadWarp + 2;
@@ -124,9 +124,9 @@ struct AttPlan {
   static constexpr int Units = (R == 32 && E4) ? 2 : 3;
   static constexpr int PerTile = kAttTile / Unit;
   static_assert(Units <= 2 * PerTile, "the scale barriers are the units of two tiles, waited for once each");
-  static constexpr int UnitWarps = kAttDequantWarps / PerTile;  // code warps that read a unit
+  static constexpr int WarpTokens = kAttTile / (kAttDequantWarps / 4);  // tokens of a code warp
+  static constexpr int UnitWarps = 4 * (Unit > WarpTokens ? Unit / WarpTokens : 1);  // code warps that read a unit
   static constexpr int HalfRows = R / 2;                         // rows of a softmax warp
-  static constexpr int WarpTokens = kAttTile / (kAttDequantWarps / 4);  // tokens of a code warp: its share of a block
 
   static constexpr int UnitCodes = Unit * kKv4CodeBytes;
   static constexpr int UnitBytes = UnitCodes + Unit * kKv4Blocks;
@@ -143,9 +143,9 @@ struct AttPlan {
   static constexpr int Bytes = Misc + static_cast<int>(sizeof(Shared));
   static_assert(OCol + 4 * NP <= 512, "tensor memory");
   static_assert(Bytes <= 232448, "shared memory");
-  // registers of the softmax, code and other warps, of the seven warpgroups' at launch
-  static constexpr int SoftRegs = R == 16 ? 96 : 120, CodeRegs = R == 16 ? 56 : 48, OtherRegs = R == 16 ? 88 : 72;
-  static_assert(2 * SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 7 * kAttRegs, "registers");
+  // registers of the softmax, code and other warps, of the five warpgroups' at launch
+  static constexpr int SoftRegs = R == 16 ? 96 : 112, CodeRegs = R == 16 ? 96 : 88, OtherRegs = R == 16 ? 96 : 80;
+  static_assert(2 * SoftRegs + kAttDequantWarps / 4 * CodeRegs + OtherRegs <= 5 * kAttRegs, "registers");
   // barrier indexes; K8Full and K8Empty: 4 * tile buffer + block of 128 latents
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
                        RopeFull = ScaleFull + 2 * PerTile,
