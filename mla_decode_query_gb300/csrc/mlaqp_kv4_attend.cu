@@ -908,33 +908,71 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 
 // --------------------------------------------------------------------------
 // Join: the pieces of a row group that several CTAs worked on, in their
-// order.  A job is a row and 128 of its latents; eight warps take the pieces
-// in turn.
+// order.  A job is a row, or 128 of its 512 latents where there are few rows;
+// the CTA's eight warps take the pieces in turn.  Bound by latency: lengths,
+// then M and l, then the sums of all pieces at once.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCtasPerSm = 4;
 
 struct JoinShared {
   AttSchedule s;
   int split[kAttMaxSeqs];
   int split_warp[8];
   float m[8];
+  float weight[256], l[256];  // of a piece: there are at most as many as SMs
   float wsum[8];
-  alignas(16) float part[8][128];
+  alignas(16) float part[8][kLatent];
 };
 
+// Sums of BL x 128 latents from `col`: the warp's pieces, then all warps'.
+template <int R, int BL, class Slot>
+__device__ __forceinline__ void join_sums(JoinShared& j, int np, int r, int col, const Slot& slot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float4 acc[BL];
+#pragma unroll
+  for (int b = 0; b < BL; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  constexpr int U = 8 / BL;  // pieces in flight
+  for (int c0 = warp; c0 < np; c0 += 8 * U) {
+    float4 o[U][BL];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < BL; ++b)
+        if (c0 + 8 * u < np)
+          o[u][b] = *reinterpret_cast<const float4*>(slot(c0 + 8 * u) + r * kLatent + col + 128 * b + 4 * lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + 8 * u >= np) break;
+      const float f = j.weight[c0 + 8 * u];
+      sum = fmaf(j.l[c0 + 8 * u], f, sum);
+#pragma unroll
+      for (int b = 0; b < BL; ++b) {
+        acc[b].x = fmaf(o[u][b].x, f, acc[b].x);
+        acc[b].y = fmaf(o[u][b].y, f, acc[b].y);
+        acc[b].z = fmaf(o[u][b].z, f, acc[b].z);
+        acc[b].w = fmaf(o[u][b].w, f, acc[b].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < BL; ++b) *reinterpret_cast<float4*>(&j.part[warp][128 * b + 4 * lane]) = acc[b];
+  if (lane == 0) j.wsum[warp] = sum;
+}
+
 template <int R>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     mlaqp_kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, const int grid) {
   extern __shared__ uint8_t smem_raw[];
   JoinShared& j = *reinterpret_cast<JoinShared*>(smem_raw);
-  pdl_launch_dependents();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // This kernel starts once every CTA of the attention kernel has passed its
+  // own wait, so the lengths, which that one does not write, may be read now.
   const int V = att_schedule(p, R, j.s, false);
   const int* prefix = j.s.prefix;
   const int total = prefix[V];
-  if (total == 0) return;
-  const int ctas = att_active(total, grid);
+  const int ctas = att_active(max(total, 1), grid);
   // the row groups that more than one CTA worked on, in order
   const bool split = tid < V && prefix[tid + 1] > prefix[tid] &&
                      att_owner(total, prefix[tid], ctas) != att_owner(total, prefix[tid + 1] - 1, ctas);
@@ -948,66 +986,61 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   if (split) j.split[rank] = tid;
   __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
   const int rows = p.q_len * p.H, groups = (rows + R - 1) / R;
-  const int jobs = n_split * R * 4;
+  const int per_group = min(R, rows);
+  const int cuts = n_split * per_group * 4 <= static_cast<int>(gridDim.x) ? 4 : 1;
+  const int jobs = n_split * per_group * cuts;
   for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
-    const int v = j.split[job / (R * 4)], r = job / 4 % R, quarter = job % 4;
+    const int v = j.split[job / (per_group * cuts)], r = job / cuts % per_group, col = job % cuts * 128;
     const int rr = (v % groups) * R + r;
     if (rr >= rows) continue;
-    const int c0 = att_owner(total, prefix[v], ctas), c1 = att_owner(total, prefix[v + 1] - 1, ctas);
-    auto slot = [&](int c) {
-      const int at = 2 * c + (c == c0 && prefix[v] > att_begin(total, c, ctas) ? 1 : 0);
-      return reinterpret_cast<const float*>(p.ws) + at * att_slot_floats<R>();
-    };
-    float top = -INFINITY;
-    for (int c = c0 + tid; c <= c1; c += kJoinThreads) top = fmaxf(top, slot(c)[R * kLatent + r]);
-    top = warp_max(top);
-    __syncthreads();
-    if (lane == 0) j.m[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, j.m[w]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int c = c0 + warp; c <= c1; c += 8) {
-      const float* q = slot(c);
-      const float f = ex2(q[R * kLatent + r] - top);
-      const float4 o = *reinterpret_cast<const float4*>(q + r * kLatent + 128 * quarter + 4 * lane);
-      sum = fmaf(q[R * kLatent + R + r], f, sum);
-      acc.x = fmaf(o.x, f, acc.x);
-      acc.y = fmaf(o.y, f, acc.y);
-      acc.z = fmaf(o.z, f, acc.z);
-      acc.w = fmaf(o.w, f, acc.w);
+    const int c0 = att_owner(total, prefix[v], ctas), np = att_owner(total, prefix[v + 1] - 1, ctas) - c0 + 1;
+    const bool inside = prefix[v] > att_begin(total, c0, ctas);  // the first piece begins inside its CTA's stretch
+    const float* const base = reinterpret_cast<const float*>(p.ws) + 2 * c0 * att_slot_floats<R>();
+    auto slot = [&](int c) { return base + (2 * c + (c == 0 && inside ? 1 : 0)) * att_slot_floats<R>(); };
+    float m = -INFINITY, l = 0.f;
+    if (tid < np) {
+      m = slot(tid)[R * kLatent + r];
+      l = slot(tid)[R * kLatent + R + r];
     }
-    *reinterpret_cast<float4*>(&j.part[warp][4 * lane]) = acc;
-    if (lane == 0) j.wsum[warp] = sum;
+    const float wm = warp_max(m);
+    if (lane == 0) j.m[warp] = wm;
     __syncthreads();
-    if (warp == 0) {
-      sum = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = j.m[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, j.m[w]);
+    if (tid < np) {
+      j.weight[tid] = ex2(m - top);
+      j.l[tid] = l;
+    }
+    __syncthreads();
+    if (cuts == 1) join_sums<R, 4>(j, np, r, 0, slot);
+    else join_sums<R, 1>(j, np, r, col, slot);
+    __syncthreads();
+    const int n = kLatent / cuts;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += j.wsum[w];
+    const int i = rr / p.H, h = rr % p.H;
+    const int64_t q = static_cast<int64_t>(v / groups) * p.q_len + i;
+    const bool none = j.s.len[v] - (p.q_len - 1 - i) <= 0;
+    const float inv = 1.f / sum;
+    if (2 * tid < n) {
+      float2 o = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(&j.part[w][4 * lane]);
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-        sum += j.wsum[w];
+        const float2 a = *reinterpret_cast<const float2*>(&j.part[w][2 * tid]);
+        o.x += a.x;
+        o.y += a.y;
       }
-      const int i = rr / p.H, h = rr % p.H;
-      const int64_t m = static_cast<int64_t>(v / groups) * p.q_len + i;
-      const bool none = j.s.len[v] - (p.q_len - 1 - i) <= 0;
-      const float inv = 1.f / sum;
-      uint2 o = make_uint2(0u, 0u);
-      if (!none) {
-        o.x = pack_bf16x2(acc.y * inv, acc.x * inv);
-        o.y = pack_bf16x2(acc.w * inv, acc.z * inv);
-      }
-      *reinterpret_cast<uint2*>(p.x + m * p.x_ts + h * kLatent + 128 * quarter + 4 * lane) = o;
-      if (lane == 0 && quarter == 0 && p.lse)
-        p.lse[m * p.H + h] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      *reinterpret_cast<uint32_t*>(p.x + q * p.x_ts + h * kLatent + col + 2 * tid) =
+          none ? 0u : pack_bf16x2(o.y * inv, o.x * inv);
     }
+    if (tid == 0 && col == 0 && p.lse)
+      p.lse[q * p.H + h] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    __syncthreads();
   }
 }
 
@@ -1036,7 +1069,8 @@ cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cuda
   void* args[2] = {const_cast<Kv4AttendParams*>(&p), &sm_count};
   const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(sm_count), kAttThreads, k.smem, stream, args);
   if (e != cudaSuccess) return e;
-  return kv4_launch(k.join, static_cast<unsigned>(2 * sm_count), kJoinThreads, sizeof(JoinShared), stream, args);
+  return kv4_launch(k.join, static_cast<unsigned>(kJoinCtasPerSm * sm_count), kJoinThreads, sizeof(JoinShared), stream,
+                    args);
 }
 
 cudaError_t kv4_attend_setup() {
