@@ -103,20 +103,22 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   AttRing<L::Units> ring;
   auto load_rope = [&]() {
     const int page = lane < entries ? s.pages[kr % kAttPageTiles][lane] : -1;
-    const uint32_t bar = bars + 8 * L::RopeFull;
+    const int rb = kr % L::RopeBufs;
+    const uint32_t bar = bars + 8 * (L::RopeFull + rb);
     const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(have) * rope_bytes);
     __syncwarp();
     if (page >= 0)
-      bulk_load_1d(smem + L::Rope + lane * rope_bytes, cache + page * page_stride + rope_plane, rope_bytes, bar);
+      bulk_load_1d(smem + L::Rope + rb * kRopeTile + lane * rope_bytes, cache + page * page_stride + rope_plane, rope_bytes, bar);
     ++kr;
   };
-  auto rope_free = [&]() { return kr == 0 || mbar_test(bars + 8 * L::RopeEmpty, (kr - 1) & 1); };
+  auto rope_empty = [&]() { return bars + 8 * (L::RopeEmpty + kr % L::RopeBufs); };
+  auto rope_free = [&]() { return kr < L::RopeBufs || mbar_test(rope_empty(), (kr / L::RopeBufs - 1) & 1); };
   // Rope rows of all tiles up to `tile`.
   auto finish_rope = [&](int tile) -> bool {
 #pragma unroll 1
     while (kr <= tile) {
-      if (kr > 0 && !att_wait(bars + 8 * L::RopeEmpty, (kr - 1) & 1, s)) return false;
+      if (kr >= L::RopeBufs && !att_wait(rope_empty(), (kr / L::RopeBufs - 1) & 1, s)) return false;
       load_rope();
     }
     return true;
@@ -215,7 +217,9 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     };
 #pragma unroll 1
     for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
-    if (kr > 0) drain(bars + 8 * L::RopeFull, (kr - 1) & 1);
+#pragma unroll 1
+    for (int i = max(0, kr - L::RopeBufs); i < kr; ++i)
+      drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
   }
 }
 
@@ -376,21 +380,23 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
     ok = att_wait(bars + 8 * L::QFull, item & 1, s);
 #pragma unroll 1
     for (int n = 0; ok && n < it.count; ++n, ++k) {
-      const int b = k & 1, sb = k % L::SBufs;
+      const int b = k & 1, sb = k % L::SBufs, rb = k % L::RopeBufs;
       if (k >= L::SBufs) ok = att_wait(bars + 8 * (L::SEmpty + sb), (k / L::SBufs - 1) & 1, s);
-      if (ok) ok = att_wait(bars + 8 * L::RopeFull, k & 1, s);
+      if (!ok) break;
+      const uint32_t d = tmem + sb * L::SCols;
+      ok = att_wait(bars + 8 * (L::RopeFull + rb), (k / L::RopeBufs) & 1, s);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + sb * L::SCols;
       if (leader) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) umma_bf16(d + L::NQ, a_rope + 2 * c, b_pe + 2 * c, id_r, c > 0);
-        umma_commit(bars + 8 * L::RopeEmpty);
+        for (int c = 0; c < 4; ++c)
+          umma_bf16(d + L::NQ, a_rope + rb * (kRopeTile >> 4) + 2 * c, b_pe + 2 * c, id_r, c > 0);
+        umma_commit(bars + 8 * (L::RopeEmpty + rb));
       }
       const uint64_t a_tile = a_k8 + static_cast<uint64_t>(b * (kK8Tile >> 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ok = att_wait(bars + 8 * (L::K8Full + 4 * b + i), (k / 2) & 1, s);
+        if (ok) ok = att_wait(bars + 8 * (L::K8Full + 4 * b + i), (k / 2) & 1, s);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -913,7 +919,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 // then M and l, then the sums of all pieces at once.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCtasPerSm = 4;
+constexpr int kJoinCtasPerSm = 2;
 
 struct JoinShared {
   AttSchedule s;

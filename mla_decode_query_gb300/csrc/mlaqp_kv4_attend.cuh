@@ -105,7 +105,7 @@ struct AttShared : AttSchedule {
   uint8_t smax[kAttScaleTiles][kAttTile];   // s_t
   uint32_t tmask[kAttMaskTiles];            // 16-token parts of a tile that were copied, a bit each
   int pages[kAttPageTiles][8];              // a tile's pages, -1: none
-  alignas(8) uint64_t bars[40];
+  alignas(8) uint64_t bars[42];
 };
 
 // Shared memory and tensor memory of a variant: R query rows, E4M3 or BF16
@@ -122,6 +122,7 @@ struct AttPlan {
   static constexpr int OCol = SBufs * SCols;
   static constexpr int Unit = (R == 32 && !E4) ? 32 : 64;
   static constexpr int Units = (R == 32 && E4) ? 2 : 3;
+  static constexpr int RopeBufs = 1;
   static constexpr int PerTile = kAttTile / Unit;
   static_assert(Units <= 2 * PerTile, "the scale barriers are the units of two tiles, waited for once each");
   static constexpr int WarpTokens = kAttTile / (kAttDequantWarps / 4);  // tokens of a code warp
@@ -133,7 +134,7 @@ struct AttPlan {
   using Shared = AttShared<R, Unit * Units>;
   static constexpr int K8 = 0;
   static constexpr int Rope = K8 + 2 * kK8Tile;
-  static constexpr int Q = Rope + kRopeTile;
+  static constexpr int Q = Rope + RopeBufs * kRopeTile;
   static constexpr int QBlock = NQ * 128;          // 128 latents of the queries
   static constexpr int QPe = Q + 4 * QBlock;
   static constexpr int P = QPe + R * 128;
@@ -149,10 +150,10 @@ struct AttPlan {
   // barrier indexes; K8Full and K8Empty: 4 * tile buffer + block of 128 latents
   static constexpr int RawFull = 0, RawEmpty = RawFull + Units, ScaleFull = RawEmpty + Units,
                        RopeFull = ScaleFull + 2 * PerTile,
-                       RopeEmpty = RopeFull + 1, K8Full = RopeEmpty + 1, K8Empty = K8Full + 8,  // per 128 latents of a tile
+                       RopeEmpty = RopeFull + RopeBufs, K8Full = RopeEmpty + RopeBufs, K8Empty = K8Full + 8,  // per 128 latents of a tile
                        SFull = K8Empty + 8, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
                        QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, BarCount = Drain + 2;
-  static_assert(BarCount <= 40, "barriers");
+  static_assert(BarCount <= 42, "barriers");
 };
 
 // Instruction descriptor: FP32 accumulator, operand formats and majors.
