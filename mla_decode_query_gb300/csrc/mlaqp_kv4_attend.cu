@@ -501,20 +501,19 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename Att
     }
     cr *= *p.q_scale;
   } else {
-    // Two passes over the row, the second from the caches: first its largest
-    // latent and rope element, then the terms.
+    constexpr int N = 64 / TPR;  // chunks of eight latents of a thread
     const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + at;
+    uint4 x[N], pe = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = real ? ld_u128(src + 8 * (n * TPR + sub)) : make_uint4(0, 0, 0, 0);
+    if (real && sub < 8) pe = ld_u128(src + kLatent + 8 * sub);  // TPR >= 8: one chunk of rope at most
     auto top = [](uint4 a) {
       const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu), __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
       return max(m & 0xFFFFu, m >> 16);
     };
-    uint32_t ml = 0, mp = 0;
-    if (real) {
-#pragma unroll 4
-      for (int c = sub; c < 64; c += TPR) ml = max(ml, top(ld_u128(src + 8 * c)));
-#pragma unroll 1
-      for (int c = sub; c < 8; c += TPR) mp = max(mp, top(ld_u128(src + kLatent + 8 * c)));
-    }
+    uint32_t ml = 0, mp = top(pe);
+#pragma unroll
+    for (int n = 0; n < N; ++n) ml = max(ml, top(x[n]));
 #pragma unroll
     for (int d = 1; d < TPR; d <<= 1) {
       ml = max(ml, __shfl_xor_sync(0xffffffffu, ml, d));
@@ -526,10 +525,10 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename Att
     const bool bad = ml >= 0x7F80u || mp >= 0x7F80u;  // NaN or infinity: the whole row
     const float f = bad ? __uint_as_float(0x7FC00000u) : exp2f(static_cast<float>(134 - e));
     cr *= exp2f(static_cast<float>(e - 134));
-#pragma unroll 1
-    for (int c = sub; c < 64; c += TPR) {  // elements 8c..8c+7: half of 16-byte E4M3 chunk c/2
-      const uint4 x = real ? ld_u128(src + 8 * c) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {  // elements 8c..8c+7: half of 16-byte E4M3 chunk c/2
+      const int c = n * TPR + sub;
+      const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
       uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -545,14 +544,12 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename Att
       *reinterpret_cast<uint2*>(to + r * 128) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(to + (R + r) * 128) = make_uint2(lo[0], lo[1]);
     }
-#pragma unroll 1
-    for (int c = sub; c < 8; c += TPR) {
-      const uint4 x = real ? ld_u128(src + kLatent + 8 * c) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (sub < 8) {
+      const uint32_t w[4] = {pe.x, pe.y, pe.z, pe.w};
       uint32_t o[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) o[g] = pack_bf16x2(bf16_hi(w[g]) * f, bf16_lo(w[g]) * f);
-      *reinterpret_cast<uint4*>(smem + L::QPe + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(smem + L::QPe + r * 128 + ((sub ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
   if (sub == 0) {
@@ -877,9 +874,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
   const int total = s.prefix[V];
-  const int active = att_active(total, gridDim.x);
-  const bool mine = static_cast<int>(blockIdx.x) < active;
-  const int t0 = mine ? att_begin(total, blockIdx.x, active) : 0, t1 = mine ? att_begin(total, blockIdx.x + 1, active) : 0;
+  const AttCut cut(total, gridDim.x);
+  const bool mine = total > 0 && static_cast<int>(blockIdx.x) < cut.n;
+  const int t0 = mine ? cut.begin(blockIdx.x) : 0, t1 = mine ? cut.begin(blockIdx.x + 1) : 0;
   const uint32_t base = smem_u32(smem);
   // every warpgroup does this, and the shares fit what the launch has
   if (warp < kAttSoftWarps) {
@@ -926,7 +923,7 @@ struct JoinShared {
   int split[kAttMaxSeqs];
   int split_warp[8];
   float m[8];
-  float weight[256], l[256];  // of a piece: there are at most as many as SMs
+  float weight[kAttMaxCtas], l[kAttMaxCtas];  // of a piece
   float wsum[8];
   alignas(16) float part[8][kLatent];
 };
@@ -978,10 +975,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   const int V = att_schedule(p, R, j.s, false);
   const int* prefix = j.s.prefix;
   const int total = prefix[V];
-  const int ctas = att_active(max(total, 1), grid);
+  const AttCut cut(total, grid);
   // the row groups that more than one CTA worked on, in order
-  const bool split = tid < V && prefix[tid + 1] > prefix[tid] &&
-                     att_owner(total, prefix[tid], ctas) != att_owner(total, prefix[tid + 1] - 1, ctas);
+  const bool split =
+      tid < V && prefix[tid + 1] > prefix[tid] && cut.owner(prefix[tid]) != cut.owner(prefix[tid + 1] - 1);
   const unsigned who = __ballot_sync(0xffffffffu, split);
   if (lane == 0) j.split_warp[warp] = __popc(who);
   __syncthreads();
@@ -1002,8 +999,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     const int v = j.split[job / (per_group * cuts)], r = job / cuts % per_group, col = job % cuts * 128;
     const int rr = (v % groups) * R + r;
     if (rr >= rows) continue;
-    const int c0 = att_owner(total, prefix[v], ctas), np = att_owner(total, prefix[v + 1] - 1, ctas) - c0 + 1;
-    const bool inside = prefix[v] > att_begin(total, c0, ctas);  // the first piece begins inside its CTA's stretch
+    const int c0 = cut.owner(prefix[v]), np = cut.owner(prefix[v + 1] - 1) - c0 + 1;
+    const bool inside = prefix[v] > cut.begin(c0);  // the first piece begins inside its CTA's stretch
     const float* const base = reinterpret_cast<const float*>(p.ws) + 2 * c0 * att_slot_floats<R>();
     auto slot = [&](int c) { return base + (2 * c + (c == 0 && inside ? 1 : 0)) * att_slot_floats<R>(); };
     float m = -INFINITY, l = 0.f;
@@ -1072,8 +1069,9 @@ AttKernels att_pick(int q_len, int H, bool e4m3) {
 
 cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream) {
   const AttKernels k = att_pick(p.q_len, p.H, q_e4m3);
-  void* args[2] = {const_cast<Kv4AttendParams*>(&p), &sm_count};
-  const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(sm_count), kAttThreads, k.smem, stream, args);
+  int ctas = sm_count < kAttMaxCtas ? sm_count : kAttMaxCtas;
+  void* args[2] = {const_cast<Kv4AttendParams*>(&p), &ctas};
+  const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(ctas), kAttThreads, k.smem, stream, args);
   if (e != cudaSuccess) return e;
   return kv4_launch(k.join, static_cast<unsigned>(kJoinCtasPerSm * sm_count), kJoinThreads, sizeof(JoinShared), stream,
                     args);

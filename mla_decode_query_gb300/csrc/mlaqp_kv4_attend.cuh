@@ -346,21 +346,26 @@ __device__ __forceinline__ int att_schedule(const Kv4AttendParams& p, int R, Att
   return V;
 }
 
-// CTAs that get tiles, one or more each.
-__device__ __forceinline__ int att_active(int total, int grid) { return min(total, grid); }
-
-// First tile of CTA c of n (c = n: the end).
-__device__ __forceinline__ int att_begin(int total, int c, int n) {
-  return static_cast<int>(static_cast<int64_t>(total) * c / n);
-}
-
-// The CTA whose stretch holds tile t.
-__device__ __forceinline__ int att_owner(int total, int t, int n) {
-  int c = static_cast<int>(static_cast<int64_t>(t) * n / total);
-  while (c + 1 < n && att_begin(total, c + 1, n) <= t) ++c;
-  while (c > 0 && att_begin(total, c, n) > t) --c;
-  return c;
-}
+// The line of `total` tiles cut into `n` stretches, one or more tiles each:
+// stretch c begins at floor(total * c / n), kept in 32 bits by the quotient
+// and remainder of total / n (n <= 256).
+struct AttCut {
+  int n, base, rem;
+  __device__ __forceinline__ AttCut(int total, int ctas) {
+    n = max(min(total, ctas), 1);
+    base = total / n;
+    rem = total - base * n;
+  }
+  __device__ __forceinline__ int begin(int c) const { return base * c + rem * c / n; }
+  // The stretch that holds tile t: a guess that is off by one at most, put right.
+  __device__ __forceinline__ int owner(int t) const {
+    int c = min(n - 1, static_cast<int>(static_cast<float>(t) / (static_cast<float>(base) + static_cast<float>(rem) / n)));
+    while (c + 1 < n && begin(c + 1) <= t) ++c;
+    while (c > 0 && begin(c) > t) --c;
+    return c;
+  }
+};
+constexpr int kAttMaxCtas = 256;
 
 // The row group that holds tile t.
 __device__ __forceinline__ int att_find(const int* prefix, int V, int t) {
