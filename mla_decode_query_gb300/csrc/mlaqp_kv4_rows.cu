@@ -17,6 +17,14 @@ namespace mlaqp {
 namespace {
 
 constexpr int kRowsThreads = 256;
+constexpr int kGatherTokens = 2;
+
+// Byte of this lane's k-th word (eight latents) among a token's codes: word
+// lane + 32k, blocks with bit 2 set having their halves swapped.
+__device__ __forceinline__ uint32_t rows_word(int k) {
+  const uint32_t lane = threadIdx.x & 31;
+  return 128 * k + 4 * (lane ^ ((lane >> 3) & 2));
+}
 
 __global__ void __launch_bounds__(kRowsThreads) mlaqp_kv4_append_kernel(const __grid_constant__ Kv4RowsParams p) {
   pdl_launch_dependents();
@@ -33,35 +41,34 @@ __global__ void __launch_bounds__(kRowsThreads) mlaqp_kv4_append_kernel(const __
   }
   const uint32_t pos = slot & ((1 << p.cache.shift) - 1);
   uint8_t* base = p.cache.base + page * p.cache.page_stride;
-  const uint16_t* src = p.latent + t * p.latent_ts + 16 * lane;
-  const uint4 v0 = ld_u128(src);
-  const uint4 v1 = ld_u128(src + 8);
+  const uint16_t* src = p.latent + t * p.latent_ts + 8 * lane;
+  const uint4 v[2] = {ld_u128(src), ld_u128(src + 256)};
   uint4 pe = make_uint4(0, 0, 0, 0);
   if (lane < 8) pe = ld_u128(p.k_pe + t * p.k_pe_ts + 8 * lane);
 
-  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  uint32_t amax = 0;  // BF16 bits of the largest magnitude; NaN bits lie above those of infinity
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // a block is two lanes
-  const bool bad = amax >= 0x7F80u;
-  // exponent - 2, one more when the significand exceeds 1.75 = 7/4
-  const int e = static_cast<int>((amax + 0x1Fu) >> 7) - 2;
-  const int s = min(max(e, kKv4ScaleMin), kKv4ScaleMax);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - s) << 23);
-  float a[8], b[8];
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t amax = 0;  // BF16 bits of the largest magnitude; NaN bits lie above those of infinity
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[2 * i] = bf16_lo(w[i]) * inv;
-    a[2 * i + 1] = bf16_hi(w[i]) * inv;
-    b[2 * i] = bf16_lo(w[4 + i]) * inv;
-    b[2 * i + 1] = bf16_hi(w[4 + i]) * inv;
+    for (int i = 0; i < 4; ++i) amax = max(amax, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // a block is four lanes
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const bool bad = amax >= 0x7F80u;
+    // exponent - 2, one more when the significand exceeds 1.75 = 7/4
+    const int e = static_cast<int>((amax + 0x1Fu) >> 7) - 2;
+    const int s = min(max(e, kKv4ScaleMin), kKv4ScaleMax);
+    const float inv = __uint_as_float(static_cast<uint32_t>(254 - s) << 23);
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[2 * i] = bf16_lo(w[i]) * inv;
+      a[2 * i + 1] = bf16_hi(w[i]) * inv;
+    }
+    *reinterpret_cast<uint32_t*>(base + kv4_code_off(pos) + rows_word(k)) = bad ? 0u : kv4_word(a);
+    if ((lane & 3) == 0)
+      base[kv4_scale_off(pos, p.cache.shift) + 8 * k + (lane >> 2)] = static_cast<uint8_t>(bad ? kKv4ScaleNan : s);
   }
-  uint2 codes = make_uint2(kv4_word(a), kv4_word(b));
-  if (bad) codes = make_uint2(0u, 0u);
-  const int j = lane >> 1, half = lane & 1;
-  *reinterpret_cast<uint2*>(base + kv4_code_off(pos) + 16 * j + 8 * (half ^ ((j >> 2) & 1))) = codes;
-  if (half == 0) base[kv4_scale_off(pos, p.cache.shift) + j] = static_cast<uint8_t>(bad ? kKv4ScaleNan : s);
   if (lane < 8) st_u128(base + kv4_rope_off(pos, p.cache.shift) + 16 * (lane ^ (pos & 7)), pe);
 }
 
@@ -69,50 +76,61 @@ __global__ void __launch_bounds__(kRowsThreads) mlaqp_kv4_gather_kernel(const __
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const int slot = p.slots[t];
-  const int page = slot >> p.cache.shift;
-  const bool ok = slot >= 0 && page < p.cache.num_pages;
-  if (slot >= 0 && !ok && lane == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
-  uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  uint4 pe = make_uint4(0, 0, 0, 0);
-  if (ok) {
-    const uint32_t pos = slot & ((1 << p.cache.shift) - 1);
-    const uint8_t* base = p.cache.base + page * p.cache.page_stride;
-    const int j = lane >> 1, half = lane & 1;
-    const uint2 codes =
-        *reinterpret_cast<const uint2*>(base + kv4_code_off(pos) + 16 * j + 8 * (half ^ ((j >> 2) & 1)));
-    const uint32_t s = kv4_scale_bf16x2(base[kv4_scale_off(pos, p.cache.shift) + j]);
-    if (lane < 8) pe = ld_u128(base + kv4_rope_off(pos, p.cache.shift) + 16 * (lane ^ (pos & 7)));
-    uint32_t a[4], b[4];
-    kv4_word_bf16(codes.x, a);
-    kv4_word_bf16(codes.y, b);
+  const int t0 = (blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * kGatherTokens;
+  uint32_t codes[kGatherTokens][2], scale[kGatherTokens][2];
+  uint4 pe[kGatherTokens];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = mul_bf16x2(a[i], s);
-      o[4 + i] = mul_bf16x2(b[i], s);
+  for (int n = 0; n < kGatherTokens; ++n) {
+    const int slot = t0 + n < p.T ? p.slots[t0 + n] : -1;
+    const int page = slot >> p.cache.shift;
+    const bool ok = slot >= 0 && page < p.cache.num_pages;
+    if (slot >= 0 && !ok && lane == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
+    pe[n] = make_uint4(0, 0, 0, 0);
+    codes[n][0] = codes[n][1] = scale[n][0] = scale[n][1] = 0;
+    if (ok) {
+      const uint32_t pos = slot & ((1 << p.cache.shift) - 1);
+      const uint8_t* base = p.cache.base + page * p.cache.page_stride;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        codes[n][k] = *reinterpret_cast<const uint32_t*>(base + kv4_code_off(pos) + rows_word(k));
+        scale[n][k] = base[kv4_scale_off(pos, p.cache.shift) + 8 * k + (lane >> 2)];
+      }
+      if (lane < 8) pe[n] = ld_u128(base + kv4_rope_off(pos, p.cache.shift) + 16 * (lane ^ (pos & 7)));
     }
   }
-  uint16_t* dst = p.out + t * p.out_ts;
-  st_u128(dst + 16 * lane, make_uint4(o[0], o[1], o[2], o[3]));
-  st_u128(dst + 16 * lane + 8, make_uint4(o[4], o[5], o[6], o[7]));
-  if (lane < 8) st_u128(dst + kLatent + 8 * lane, pe);
+#pragma unroll
+  for (int n = 0; n < kGatherTokens; ++n) {
+    if (t0 + n >= p.T) return;
+    uint16_t* dst = p.out + (t0 + n) * p.out_ts;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t o[4];
+      kv4_word_bf16(codes[n][k], o);
+      const uint32_t s = kv4_scale_bf16x2(scale[n][k]);
+      st_u128(dst + 256 * k + 8 * lane,
+              make_uint4(mul_bf16x2(o[0], s), mul_bf16x2(o[1], s), mul_bf16x2(o[2], s), mul_bf16x2(o[3], s)));
+    }
+    if (lane < 8) st_u128(dst + kLatent + 8 * lane, pe[n]);
+  }
 }
 
-unsigned rows_grid(int T) { return (static_cast<unsigned>(T) + kRowsThreads / 32 - 1) / (kRowsThreads / 32); }
+// CTAs for T tokens, `each` of them to a warp.
+unsigned rows_grid(int T, int each) {
+  const unsigned n = kRowsThreads / 32 * each;
+  return (static_cast<unsigned>(T) + n - 1) / n;
+}
 
 }  // namespace
 
 cudaError_t kv4_append(const Kv4RowsParams& p, int, cudaStream_t stream) {
   void* args[1] = {const_cast<Kv4RowsParams*>(&p)};
-  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_append_kernel), rows_grid(p.T), kRowsThreads, 0, stream,
+  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_append_kernel), rows_grid(p.T, 1), kRowsThreads, 0, stream,
                     args);
 }
 
 cudaError_t kv4_gather(const Kv4RowsParams& p, int, cudaStream_t stream) {
   void* args[1] = {const_cast<Kv4RowsParams*>(&p)};
-  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_gather_kernel), rows_grid(p.T), kRowsThreads, 0, stream,
+  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_gather_kernel), rows_grid(p.T, kGatherTokens), kRowsThreads, 0, stream,
                     args);
 }
 
