@@ -40,10 +40,15 @@
  * mlaqp_last_error() as in mlaqp.h.  What only the device can see is recorded
  * in the word of mlaqp_device_status():
  *   MLAQP_DEVSTATUS_BAD_INDEX     a page, slot or sequence index out of range,
- *                                 a length beyond its table row, a child that
- *                                 is not empty: that item was left out
+ *                                 a length beyond its table row or the pool's
+ *                                 num_pages*page_size tokens, a child that is
+ *                                 not empty: that item was left out
  *   MLAQP_DEVSTATUS_OUT_OF_PAGES  a fork or extension found no free page: that
  *                                 sequence was left as it was
+ *   MLAQP_DEVSTATUS_WAIT_TIMEOUT  (as in mlaqp.h) the attention kernel waited
+ *                                 a second for one of its own copies or
+ *                                 products and gave up: that call's x and lse
+ *                                 mean nothing
  */
 #ifndef MLAQP_KV4_H_
 #define MLAQP_KV4_H_
@@ -106,8 +111,11 @@ int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int 
  * so the last query token sees the whole sequence and the ones before it one
  * token less each (the cache already holds the query tokens' own entries).
  * A row that sees nothing (n <= 0) gets x = 0 and lse = -infinity.  Scores,
- * softmax and sums are FP32; a NaN anywhere in a row's visible tokens or in
- * its q makes that row NaN, what lies beyond the visible tokens is never
+ * softmax and sums are FP32; latents are used exactly where the block's scale
+ * byte is at most 14 below the largest of its token, in steps of 2^-15 of
+ * that largest scale where it is further below, probabilities with 8 bits or
+ * more; a NaN anywhere in a row's visible tokens, or a
+ * NaN or an infinity in its q, makes that row NaN; what lies beyond the visible tokens is never
  * used.
  *   q          BF16 (MLAQP_OUT_BF16) or E4M3 (MLAQP_OUT_E4M3, value =
  *              code * *q_scale, q_scale one FP32 in device memory, NULL for

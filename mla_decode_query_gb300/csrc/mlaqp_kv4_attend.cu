@@ -254,13 +254,20 @@ __device__ __forceinline__ void att_scales(typename AttPlan<R, E4>::Shared& s, u
           m = __vmaxu2(m, __vmaxu2(e[i], o[i]));
         }
         m = max(m & 0xFFFFu, m >> 16);
+        const bool nan = m == kKv4ScaleNan;
+        m = min(max(m, kKv4ScaleMin), kKv4ScaleMax);
         const uint32_t mm = m * 0x00010001u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the differences cannot borrow: no byte above mm
+          e[i] = __vminu2(__vmaxu2(e[i], kKv4ScaleMin * 0x00010001u), mm);
+          o[i] = __vminu2(__vmaxu2(o[i], kKv4ScaleMin * 0x00010001u), mm);
+        }
         uint32_t r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           r[i] = __vminu2(mm - e[i], 0x001F001Fu) | (__vminu2(mm - o[i], 0x001F001Fu) << 8);
         *reinterpret_cast<uint4*>(&s.rel[(st * L::Unit + tok) * kKv4Blocks]) = make_uint4(r[0], r[1], r[2], r[3]);
-        s.smax[kb][L::Unit * q + tok] = static_cast<uint8_t>(m);
+        s.smax[kb][L::Unit * q + tok] = static_cast<uint8_t>(nan ? kKv4ScaleNan : m);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (L::ScaleFull + (k & 1) * L::PerTile + q));

@@ -241,13 +241,15 @@ class Case:
                 m = b * self.q_len + i
                 self.compare(x[m], lse[m], self.q[m], keys[:n], f"sequence {b} token {i} of {n}")
 
-    def compare(self, x, lse, q, keys, where):
+    def compare(self, x, lse, q, keys, where, small_blocks=None):
         wx, wl = ko.attend(q, keys, self.scale)
         if keys.shape[0] == 0:
             assert not x.any() and np.isneginf(lse).all(), where
             return
         p = np.exp(q @ keys.T * self.scale - wl[:, None])
         bound = 2.0 ** -8 * np.abs(wx) + 2.0 ** -8 * (p @ np.abs(keys[:, :512])) + 1e-30
+        if small_blocks is not None:  # the tokens' largest block scales
+            bound = bound + 2.0 ** -16 * (p @ small_blocks)[:, None]
         err = np.abs(x - wx)
         assert (err <= bound).all(), f"{where}: x off by {np.nanmax(err / bound)} of its bound"
         lb = 2.0 ** -15 * self.scale * (np.abs(q) @ np.abs(keys).T).max(1) + 1e-5
@@ -520,3 +522,49 @@ def test_projection_to_attention_to_v_up(cuda_device, dtype):
     _, acc = oracle.mla_v_up(to_host_bits(c.x, np.uint16).reshape(B, H, 512), dv["weight"], None, "bf16")
     got = oracle.bf16_to_f64(to_host_bits(y, np.uint16))
     assert (np.abs(got - acc) <= 1e-2 * np.abs(acc) + 1e-3).all()
+
+
+@pytest.mark.parametrize("fill", [0, 5, 6, 86, 168, 254])
+def test_bytes_behind_a_sequence_are_never_used(cuda_device, fill):
+    # whatever byte stands in the scales behind the last token
+    c = Case([1, 100, 130], P=32, H=8, q_len=2, seed=fill)
+    c.cache.buf.fill_(fill)
+    c.cache.append(c.rows, np.concatenate(c.slots))
+    _ok(c.run())
+    c.check()
+
+
+def _largest_scale(c, b):
+    """2^(s_t-127) of a sequence's tokens."""
+    host = c.cache.host()
+    at = c.slots[b]
+    byte = [host[t // c.P, c.P * 384 + t % c.P * 16:][:16].max() for t in at]
+    return np.array([ko.scale_value(v) for v in byte])
+
+
+def test_scale_bytes_out_of_range_read_as_the_nearest(cuda_device):
+    c = Case([70, 140], P=64, H=8, seed=21)
+    page = c.table[0, 0]
+    scales = c.cache.buf[page, 64 * 384:64 * 400].view(64, 16)
+    scales[3, 2], scales[4, 15], scales[5, :], scales[6, 1:] = 0, 86, 5, 12
+    page = c.table[1, 1]
+    scales = c.cache.buf[page, 64 * 384:64 * 400].view(64, 16)
+    scales[9, 4], scales[10, :] = 168, 254
+    _ok(c.run())
+    x, lse = c.outputs()
+    for b in range(2):
+        c.compare(x[b], lse[b], c.q[b], c.keys(b), f"sequence {b}", small_blocks=_largest_scale(c, b))
+
+
+def test_blocks_far_below_the_largest_of_their_token(cuda_device):
+    # octaves between the blocks of a token, up to the 80 that the cache holds
+    def rows(rng, T):
+        r = rng.standard_normal((T, 576))
+        r[:, :512] *= (2.0 ** rng.integers(-38, 38, (T, 16))).repeat(32, 1)
+        return _bits(r)
+
+    c = Case([1] * 40, P=16, H=3, rows=rows, seed=6, scale=2.0 ** -40)
+    _ok(c.run())
+    x, lse = c.outputs()
+    for b in range(40):
+        c.compare(x[b], lse[b], c.q[b], c.keys(b), f"sequence {b}", small_blocks=_largest_scale(c, b))
