@@ -935,23 +935,44 @@ struct JoinShared {
   alignas(16) float part[8][kLatent];
 };
 
-// Sums of BL x 128 latents from `col`: the warp's pieces, then all warps'.
+// One row's pieces: their weights into j.weight, their l into j.l, and the sums
+// of BL x 128 latents from `col`, by warp, into j.part and j.wsum.  The first
+// pieces' sums are asked for before M and l.  Returns the largest M.
 template <int R, int BL, class Slot>
-__device__ __forceinline__ void join_sums(JoinShared& j, int np, int r, int col, const Slot& slot) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float4 acc[BL];
-#pragma unroll
-  for (int b = 0; b < BL; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
+__device__ __forceinline__ float join_sums(JoinShared& j, int np, int r, int col, const Slot& slot) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int U = 8 / BL;  // pieces in flight
-  for (int c0 = warp; c0 < np; c0 += 8 * U) {
-    float4 o[U][BL];
+  float4 o[U][BL];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int b = 0; b < BL; ++b)
         if (c0 + 8 * u < np)
           o[u][b] = *reinterpret_cast<const float4*>(slot(c0 + 8 * u) + r * kLatent + col + 128 * b + 4 * lane);
+  };
+  float m = -INFINITY, l = 0.f;
+  if (tid < np) {
+    m = slot(tid)[R * kLatent + r];
+    l = slot(tid)[R * kLatent + R + r];
+  }
+  load(warp);
+  const float wm = warp_max(m);
+  if (lane == 0) j.m[warp] = wm;
+  __syncthreads();
+  float top = j.m[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) top = fmaxf(top, j.m[w]);
+  if (tid < np) {
+    j.weight[tid] = ex2(m - top);
+    j.l[tid] = l;
+  }
+  __syncthreads();
+  float4 acc[BL];
+#pragma unroll
+  for (int b = 0; b < BL; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int c0 = warp; c0 < np;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (c0 + 8 * u >= np) break;
@@ -965,10 +986,13 @@ __device__ __forceinline__ void join_sums(JoinShared& j, int np, int r, int col,
         acc[b].w = fmaf(o[u][b].w, f, acc[b].w);
       }
     }
+    c0 += 8 * U;
+    load(c0);
   }
 #pragma unroll
   for (int b = 0; b < BL; ++b) *reinterpret_cast<float4*>(&j.part[warp][128 * b + 4 * lane]) = acc[b];
   if (lane == 0) j.wsum[warp] = sum;
+  return top;
 }
 
 template <int R>
@@ -1010,24 +1034,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     const bool inside = prefix[v] > cut.begin(c0);  // the first piece begins inside its CTA's stretch
     const float* const base = reinterpret_cast<const float*>(p.ws) + 2 * c0 * att_slot_floats<R>();
     auto slot = [&](int c) { return base + (2 * c + (c == 0 && inside ? 1 : 0)) * att_slot_floats<R>(); };
-    float m = -INFINITY, l = 0.f;
-    if (tid < np) {
-      m = slot(tid)[R * kLatent + r];
-      l = slot(tid)[R * kLatent + R + r];
-    }
-    const float wm = warp_max(m);
-    if (lane == 0) j.m[warp] = wm;
-    __syncthreads();
-    float top = j.m[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, j.m[w]);
-    if (tid < np) {
-      j.weight[tid] = ex2(m - top);
-      j.l[tid] = l;
-    }
-    __syncthreads();
-    if (cuts == 1) join_sums<R, 4>(j, np, r, 0, slot);
-    else join_sums<R, 1>(j, np, r, col, slot);
+    const float top = cuts == 1 ? join_sums<R, 4>(j, np, r, 0, slot) : join_sums<R, 1>(j, np, r, col, slot);
     __syncthreads();
     const int n = kLatent / cuts;
     float sum = 0.f;
