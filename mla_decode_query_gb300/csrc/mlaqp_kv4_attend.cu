@@ -42,9 +42,11 @@ struct AttItem {
   int count;  // tiles here
 };
 
-__device__ __forceinline__ AttItem att_item(const int* prefix, int V, int t, int end) {
+// The one that holds tile t, v or one behind it.
+__device__ __forceinline__ AttItem att_item(const int* prefix, int v, int t, int end) {
+  while (prefix[v + 1] <= t) ++v;
   AttItem it;
-  it.v = att_find(prefix, V, t);
+  it.v = v;
   it.first = t - prefix[it.v];
   it.count = min(prefix[it.v + 1], end) - t;
   return it;
@@ -67,7 +69,7 @@ struct AttRing {
 // Warp 16: pages into shared memory.
 // --------------------------------------------------------------------------
 template <int R, bool E4>
-__device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars, int V,
+__device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
                                          int t0, int t1) {
   using L = AttPlan<R, E4>;
   const int lane = threadIdx.x & 31;
@@ -144,9 +146,10 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     }
   };
   bool ok = true;
-  for (int t = t0; ok && t < t1;) {
-    const AttItem it = att_item(s.prefix, V, t, t1);
+  for (int t = t0, v = s.group; ok && t < t1;) {
+    const AttItem it = att_item(s.prefix, v, t, t1);
     t += it.count;
+    v = it.v;
     // Each lane holds one entry of the table row and the page's address (0:
     // no page); the entries after these are loaded long before their turn,
     // so that a tile costs this warp, alone with its latencies, little.
@@ -371,7 +374,7 @@ __device__ __forceinline__ void att_drain(uint32_t bar, bool leader) {
 
 template <int R, bool E4>
 __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
-                                               uint32_t tmem, int V, int t0, int t1) {
+                                               uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
   constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
@@ -381,9 +384,10 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
   const uint64_t a_rope = smem_desc_sw128(smem + L::Rope, 16, 1024), b_pe = smem_desc_sw128(smem + L::QPe, 16, 1024);
   bool ok = true;
   int k = 0, item = 0;
-  for (int t = t0; ok && t < t1; ++item) {
-    const AttItem it = att_item(s.prefix, V, t, t1);
+  for (int t = t0, v = s.group; ok && t < t1; ++item) {
+    const AttItem it = att_item(s.prefix, v, t, t1);
     t += it.count;
+    v = it.v;
     ok = att_wait(bars + 8 * L::QFull, item & 1, s);
 #pragma unroll 1
     for (int n = 0; ok && n < it.count; ++n, ++k) {
@@ -422,7 +426,7 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
 
 template <int R, bool E4>
 __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
-                                               uint32_t tmem, int V, int t0, int t1) {
+                                               uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
   const bool leader = elect_one();
@@ -432,9 +436,10 @@ __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& 
   const uint64_t b_p = smem_desc_plain(smem + L::P, 128, L::PChunk);
   bool ok = true;
   int k = 0, item = 0;
-  for (int t = t0; ok && t < t1; ++item) {
-    const AttItem it = att_item(s.prefix, V, t, t1);
+  for (int t = t0, v = s.group; ok && t < t1; ++item) {
+    const AttItem it = att_item(s.prefix, v, t, t1);
     t += it.count;
+    v = it.v;
     if (item > 0) ok = att_wait(bars + 8 * L::OEmpty, (item - 1) & 1, s);
 #pragma unroll 1
     for (int n = 0; ok && n < it.count; ++n, ++k) {
@@ -571,7 +576,7 @@ __device__ __forceinline__ void att_query(const Kv4AttendParams& p, typename Att
 
 template <int R, bool E4>
 __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s, uint8_t* smem, uint32_t bars,
-                                            uint32_t tmem, int V, int t0, int t1) {
+                                            uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr int HR = L::HalfRows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -584,7 +589,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
   // warp here: it goes on with what is there, so that no other one is left
   // alone at a barrier, and writes nothing.
   // Row group -1 has no tiles: it only prepares the first one's queries.
-  AttItem it = {0, 0, 0};
+  AttItem it = {s.group, 0, 0};
   int k = 0;
   for (int t = t0, item = -1; t < t1; ++item) {
     const int turn = item & 1;
@@ -593,7 +598,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     soft_barrier(group);
     const int next_t = t + it.count;
     AttItem next = it;
-    if (next_t < t1) next = att_item(s.prefix, V, next_t, t1);
+    if (next_t < t1) next = att_item(s.prefix, it.v, next_t, t1);
     float top = -INFINITY;  // M of row `lane`
     float l[HR], cr[HR];
 #pragma unroll
@@ -875,15 +880,23 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   pdl_wait();
   if (warp == kAttScoreWarp) tmem_alloc(smem_u32(&s.tmem), 512);
   const int V = att_schedule(p, R, s, blockIdx.x == 0);
+  if (warp < kAttMaxSeqs / 32) {
+    // once for all warps: five of them share a scheduler
+    const AttCut cut(s.prefix[V], gridDim.x);
+    const bool mine = s.prefix[V] > 0 && static_cast<int>(blockIdx.x) < cut.n;
+    const int t0 = mine ? cut.begin(blockIdx.x) : 0;
+    if (tid < V && s.prefix[tid] <= t0 && t0 < s.prefix[tid + 1]) s.group = tid;
+    if (tid == 0) {
+      s.begin = t0;
+      s.end = mine ? cut.begin(blockIdx.x + 1) : 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
-  const int total = s.prefix[V];
-  const AttCut cut(total, gridDim.x);
-  const bool mine = total > 0 && static_cast<int>(blockIdx.x) < cut.n;
-  const int t0 = mine ? cut.begin(blockIdx.x) : 0, t1 = mine ? cut.begin(blockIdx.x + 1) : 0;
+  const int t0 = s.begin, t1 = s.end;
   const uint32_t base = smem_u32(smem);
   // every warpgroup does this, and the shares fit what the launch has
   if (warp < kAttSoftWarps) {
@@ -895,18 +908,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   }
   if (warp < kAttSoftWarps) {
     att_empty_rows<R>(p, s, V);
-    if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, V, t0, t1);
+    if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, t0, t1);
   } else if (t0 < t1) {
     if (warp < kAttLoadWarp) {
       att_dequant<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttLoadWarp) {
-      att_load<R, E4>(p, s, base, bars, V, t0, t1);
+      att_load<R, E4>(p, s, base, bars, t0, t1);
     } else if (warp == kAttScaleWarp) {
       att_scales<R, E4>(s, smem, bars, t1 - t0);
     } else if (warp == kAttScoreWarp) {
-      att_mma_scores<R, E4>(s, base, bars, tmem, V, t0, t1);
+      att_mma_scores<R, E4>(s, base, bars, tmem, t0, t1);
     } else if (warp == kAttOutputWarp) {
-      att_mma_output<R, E4>(s, base, bars, tmem, V, t0, t1);
+      att_mma_output<R, E4>(s, base, bars, tmem, t0, t1);
     }
   }
   tc_fence_before();

@@ -85,6 +85,7 @@ struct AttSchedule {
   int prefix[kAttMaxSeqs + 1];  // tiles before each row group
   int len[kAttMaxSeqs];
   int scan[8];
+  int begin, end, group;  // this CTA's tiles, the row group of the first
   int fail;
 };
 
@@ -366,16 +367,6 @@ struct AttCut {
   }
 };
 constexpr int kAttMaxCtas = 256;
-
-// The row group that holds tile t.
-__device__ __forceinline__ int att_find(const int* prefix, int V, int t) {
-  int lo = 0, hi = V;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 // Workspace: slot 2c for the piece that begins CTA c's stretch, 2c+1 for one
 // that begins inside it; R rows of 512 sums, then M and l of each row.
