@@ -931,9 +931,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 
 // --------------------------------------------------------------------------
 // Join: the pieces of a row group that several CTAs worked on, in their
-// order.  A job is a row, or 128 of its 512 latents where there are few rows;
-// the CTA's eight warps take the pieces in turn.  Bound by latency: lengths,
-// then M and l, then the sums of all pieces at once.
+// order, so that the result does not depend on which CTA was first.  A job is
+// a row, or 128 of its 512 latents where there are few rows; the CTA's eight
+// warps take the pieces in turn.  Bound by latency: M, l and the first pieces'
+// sums are asked for together, the lengths before the wait for the attention
+// kernel.  Two CTAs per SM: with one, 32 sequences of up to 8191 tokens take
+// 39.7 us instead of 35.1 (both kernels), with three 40.3.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtasPerSm = 2;
@@ -1086,7 +1089,9 @@ AttKernels att_kernels() {
                     reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), AttPlan<R, E4>::Bytes};
 }
 
-// 16 rows where all (query token, head) pairs of a sequence fit, else groups of 32.
+// 16 rows where all (query token, head) pairs of a sequence fit, else groups
+// of 32, each reading the cache once: tensor memory holds no more (three
+// terms of P, four blocks of latents, 32 rows: 384 columns, and the scores).
 AttKernels att_pick(int q_len, int H, bool e4m3) {
   if (q_len * H <= 16) return e4m3 ? att_kernels<16, true>() : att_kernels<16, false>();
   return e4m3 ? att_kernels<32, true>() : att_kernels<32, false>();

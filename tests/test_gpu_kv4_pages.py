@@ -232,3 +232,20 @@ def test_beam_step_in_a_graph(cuda_device):
     p.o.release([0, 1])
     np.testing.assert_array_equal(slots.cpu().numpy(), p.o.extend([3, 4, 5], [1, 1, 1], 1))
     p.check()
+
+
+@pytest.mark.parametrize("pages", [5, 127, 4099, 33000, 140001])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_counts_of_any_alignment(cuda_device, pages, offset):
+    # free pages are found wherever the counts begin and however many there are
+    p = Pool(4, pages, pages, 16, layers=0)
+    rng = np.random.default_rng(pages)
+    p.o.ref[:] = rng.integers(0, 2, pages) * rng.integers(1, 1 << 30, pages)
+    at = torch.zeros(pages + offset, dtype=torch.int32, device="cuda")
+    p.ref = at[offset:]
+    p.ref.copy_(_i32(p.o.ref))
+    free = int((p.o.ref == 0).sum())
+    take = [free // 3, 0, free // 2]
+    p.extend([2, 1, 0], [16 * n for n in take], 1 + 16 * max(take))
+    p.check(contents=False)
+    assert _device_status() == 0
