@@ -40,16 +40,32 @@ struct AttItem {
   int v;      // row group
   int first;  // its first tile here
   int count;  // tiles here
+  int next;   // place on the line behind it: of a row group's first tile, or the stretch's end
 };
 
-// The one that holds tile t, v or one behind it.
+// The one that holds the tile at place t, v or one behind it.
 __device__ __forceinline__ AttItem att_item(const int* prefix, int v, int t, int end) {
   while (prefix[v + 1] <= t) ++v;
   AttItem it;
   it.v = v;
-  it.first = t - prefix[it.v];
-  it.count = min(prefix[it.v + 1], end) - t;
+  it.first = t - prefix[v];
+  const int last = prefix[v + 1] - kAttEndTiles;
+  it.count = min(last, end) - t;
+  it.next = end < last ? end : prefix[v + 1];
   return it;
+}
+
+// Tiles of the stretch.
+__device__ __forceinline__ int att_tiles(const AttSchedule& s, int t, int end) {
+  int n = 0;
+#pragma unroll 1
+  for (int v = s.group; t < end;) {
+    const AttItem it = att_item(s.prefix, v, t, end);
+    n += it.count;
+    v = it.v;
+    t = it.next;
+  }
+  return n;
 }
 
 // Position in a ring of N buffers and the parity of its barriers' phase.
@@ -148,7 +164,7 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   bool ok = true;
   for (int t = t0, v = s.group; ok && t < t1;) {
     const AttItem it = att_item(s.prefix, v, t, t1);
-    t += it.count;
+    t = it.next;
     v = it.v;
     // Each lane holds one entry of the table row and the page's address (0:
     // no page); the entries after these are loaded long before their turn,
@@ -386,7 +402,7 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
   int k = 0, item = 0;
   for (int t = t0, v = s.group; ok && t < t1; ++item) {
     const AttItem it = att_item(s.prefix, v, t, t1);
-    t += it.count;
+    t = it.next;
     v = it.v;
     ok = att_wait(bars + 8 * L::QFull, item & 1, s);
 #pragma unroll 1
@@ -438,7 +454,7 @@ __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& 
   int k = 0, item = 0;
   for (int t = t0, v = s.group; ok && t < t1; ++item) {
     const AttItem it = att_item(s.prefix, v, t, t1);
-    t += it.count;
+    t = it.next;
     v = it.v;
     if (item > 0) ok = att_wait(bars + 8 * L::OEmpty, (item - 1) & 1, s);
 #pragma unroll 1
@@ -589,14 +605,14 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
   // warp here: it goes on with what is there, so that no other one is left
   // alone at a barrier, and writes nothing.
   // Row group -1 has no tiles: it only prepares the first one's queries.
-  AttItem it = {s.group, 0, 0};
+  AttItem it = {s.group, 0, 0, t0};
   int k = 0;
   for (int t = t0, item = -1; t < t1; ++item) {
     const int turn = item & 1;
     // every warp has left the row group before (what follows reuses its
     // places), and this one's rows are known
     soft_barrier(group);
-    const int next_t = t + it.count;
+    const int next_t = it.next;
     AttItem next = it;
     if (next_t < t1) next = att_item(s.prefix, it.v, next_t, t1);
     float top = -INFINITY;  // M of row `lane`
@@ -751,7 +767,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     }
 
     // The row group's end here: sums over the tokens, O from tensor memory.
-    const int tiles = s.prefix[it.v + 1] - s.prefix[it.v];
+    const int tiles = s.prefix[it.v + 1] - s.prefix[it.v] - kAttEndTiles;
     const bool complete = it.count == tiles;
     float mine = 0.f;
 #pragma unroll
@@ -773,7 +789,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     tc_fence_after();
     float* part = nullptr;
     if (!complete) {
-      const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
+      const int slot = 2 * blockIdx.x + (s.prefix[it.v] > s.cut ? 1 : 0);  // begun here or before
       part = reinterpret_cast<float*>(p.ws) + slot * att_slot_floats<R>();
     }
     __syncwarp();
@@ -885,10 +901,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     const AttCut cut(s.prefix[V], gridDim.x);
     const bool mine = s.prefix[V] > 0 && static_cast<int>(blockIdx.x) < cut.n;
     const int t0 = mine ? cut.begin(blockIdx.x) : 0;
-    if (tid < V && s.prefix[tid] <= t0 && t0 < s.prefix[tid + 1]) s.group = tid;
+    if (tid < V && s.prefix[tid] <= t0 && t0 < s.prefix[tid + 1]) {
+      s.group = tid;
+      s.begin = t0 < s.prefix[tid + 1] - kAttEndTiles ? t0 : s.prefix[tid + 1];
+    }
     if (tid == 0) {
-      s.begin = t0;
+      s.cut = t0;
       s.end = mine ? cut.begin(blockIdx.x + 1) : 0;
+      if (!mine) s.begin = 0;
     }
   }
   tc_fence_before();
@@ -911,11 +931,11 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, t0, t1);
   } else if (t0 < t1) {
     if (warp < kAttLoadWarp) {
-      att_dequant<R, E4>(s, smem, bars, t1 - t0);
+      att_dequant<R, E4>(s, smem, bars, att_tiles(s, t0, t1));
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, t0, t1);
     } else if (warp == kAttScaleWarp) {
-      att_scales<R, E4>(s, smem, bars, t1 - t0);
+      att_scales<R, E4>(s, smem, bars, att_tiles(s, t0, t1));
     } else if (warp == kAttScoreWarp) {
       att_mma_scores<R, E4>(s, base, bars, tmem, t0, t1);
     } else if (warp == kAttOutputWarp) {
@@ -1025,7 +1045,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   const AttCut cut(total, grid);
   // the row groups that more than one CTA worked on, in order
   const bool split =
-      tid < V && prefix[tid + 1] > prefix[tid] && cut.owner(prefix[tid]) != cut.owner(prefix[tid + 1] - 1);
+      tid < V && prefix[tid + 1] > prefix[tid] && cut.owner(prefix[tid]) != cut.owner(prefix[tid + 1] - kAttEndTiles - 1);
   const unsigned who = __ballot_sync(0xffffffffu, split);
   if (lane == 0) j.split_warp[warp] = __popc(who);
   __syncthreads();
@@ -1046,7 +1066,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     const int v = j.split[job / (per_group * cuts)], r = job / cuts % per_group, col = job % cuts * 128;
     const int rr = (v % groups) * R + r;
     if (rr >= rows) continue;
-    const int c0 = cut.owner(prefix[v]), np = cut.owner(prefix[v + 1] - 1) - c0 + 1;
+    const int c0 = cut.owner(prefix[v]), np = cut.owner(prefix[v + 1] - kAttEndTiles - 1) - c0 + 1;
     const bool inside = prefix[v] > cut.begin(c0);  // the first piece begins inside its CTA's stretch
     const float* const base = reinterpret_cast<const float*>(p.ws) + 2 * c0 * att_slot_floats<R>();
     auto slot = [&](int c) { return base + (2 * c + (c == 0 && inside ? 1 : 0)) * att_slot_floats<R>(); };
