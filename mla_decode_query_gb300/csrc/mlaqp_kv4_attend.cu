@@ -10,24 +10,27 @@ namespace mlaqp {
 
 namespace {
 
-constexpr unsigned long long kAttWaitNs = 1000000000ull;
+constexpr uint32_t kAttWaitNs = 1000000000u;
 
-// Bounded wait of one thread; gives up early once another one has.
+__device__ __forceinline__ uint32_t att_clock() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+// Bounded wait of one thread; gives up early once another one has.  (Kept
+// short: it is inlined some thirty times, and a larger kernel than the
+// instruction caches hold runs at half the speed.  So the host's word is set
+// once, at the kernel's end.)
 __device__ __forceinline__ bool att_wait_one(uint32_t bar, uint32_t parity, AttSchedule& s) {
   if (mbar_try_wait(bar, parity)) return true;
-  // (kept short: it is inlined some thirty times, and a larger kernel than
-  // the instruction caches hold runs at half the speed)
-  const unsigned long long t0 = globaltimer_ns();
+  const uint32_t t0 = att_clock();
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    const bool late = globaltimer_ns() - t0 > kAttWaitNs;
-    if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
-    if (late || *reinterpret_cast<volatile int*>(&s.fail)) {
-      *reinterpret_cast<volatile int*>(&s.fail) = 1;
-      return false;
-    }
-  }
-  return true;
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (att_clock() - t0 < kAttWaitNs && !*reinterpret_cast<volatile int*>(&s.fail));
+  *reinterpret_cast<volatile int*>(&s.fail) = 1;
+  return false;
 }
 
 // The same for a whole warp, with one answer for all its lanes.
@@ -148,16 +151,14 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   };
   auto wait_stage = [&](int tile) -> bool {
     if (stage_free()) return true;
-    const unsigned long long t_in = globaltimer_ns();
+    const uint32_t t_in = att_clock();
 #pragma unroll 1
     for (int i = 1;; ++i) {
       if (kr <= tile && __all_sync(0xffffffffu, rope_free())) load_rope();
       if (stage_free()) return true;
       if ((i & 63) == 0) {
-        const bool late = globaltimer_ns() - t_in > kAttWaitNs;
-        if (late) atomicOr(&g_device_status, kDevStatusWaitTimeout);
-        if (late) *reinterpret_cast<volatile int*>(&s.fail) = 1;
-        if (__any_sync(0xffffffffu, late || *reinterpret_cast<volatile int*>(&s.fail))) return false;
+        if (att_clock() - t_in > kAttWaitNs) *reinterpret_cast<volatile int*>(&s.fail) = 1;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s.fail))) return false;
       }
     }
   };
@@ -229,9 +230,9 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
   if (ok) ok = finish_rope(k - 1);
   if (!ok) {  // copies in flight land before the CTA ends
     auto drain = [&](uint32_t bar, uint32_t parity) {
-      const unsigned long long at = globaltimer_ns();
+      const uint32_t at = att_clock();
 #pragma unroll 1
-      while (!mbar_try_wait(bar, parity) && globaltimer_ns() - at < kAttWaitNs) {
+      while (!mbar_try_wait(bar, parity) && att_clock() - at < kAttWaitNs) {
       }
     };
 #pragma unroll 1
@@ -382,9 +383,9 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
 // What was issued completes before the CTA ends (bar: the warp's own).
 __device__ __forceinline__ void att_drain(uint32_t bar, bool leader) {
   if (leader) umma_commit(bar);
-  const unsigned long long at = globaltimer_ns();
+  const uint32_t at = att_clock();
 #pragma unroll 1
-  while (!mbar_try_wait(bar, 0) && globaltimer_ns() - at < kAttWaitNs) {
+  while (!mbar_try_wait(bar, 0) && att_clock() - at < kAttWaitNs) {
   }
 }
 
@@ -790,7 +791,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     float* part = nullptr;
     if (!complete) {
       const int slot = 2 * blockIdx.x + (s.prefix[it.v] > s.cut ? 1 : 0);  // begun here or before
-      part = reinterpret_cast<float*>(p.ws) + slot * att_slot_floats<R>();
+      part = reinterpret_cast<float*>(p.ws + kAttGroupBytes) + slot * att_slot_floats<R>();
     }
     __syncwarp();
     if (lane < HR) {
@@ -863,6 +864,22 @@ __device__ __forceinline__ void att_empty_rows(const Kv4AttendParams& p, const A
   }
 }
 
+// What the join kernel needs of the row groups, 32 groups a CTA: here, where a
+// warp has nothing to do yet, it costs nothing; in the join kernel, in every
+// CTA, the lengths' latency and these quotients were 2 us.
+__device__ __forceinline__ void att_groups(const Kv4AttendParams& p, const AttSchedule& s, int V) {
+  for (int v = 32 * blockIdx.x + (threadIdx.x & 31); v < V; v += 32 * gridDim.x) {
+    AttGroup g = {0, 0, s.len[v], 0};
+    if (s.prefix[v] < s.prefix[v + 1]) {
+      const AttCut cut(s.prefix[V], gridDim.x);
+      const int c = cut.owner(s.prefix[V], s.prefix[v]);
+      g.slot = 2 * c + (s.prefix[v] > cut.begin(c) ? 1 : 0);
+      g.pieces = cut.owner(s.prefix[V], s.prefix[v + 1] - kAttEndTiles - 1) - c + 1;
+    }
+    reinterpret_cast<AttGroup*>(p.ws)[v] = g;
+  }
+}
+
 template <int R, bool E4>
 __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
   using L = AttPlan<R, E4>;
@@ -929,13 +946,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   if (warp < kAttSoftWarps) {
     att_empty_rows<R>(p, s, V);
     if (t0 < t1) att_softmax<R, E4>(p, s, smem, bars, tmem, t0, t1);
+  } else if (warp == kAttScaleWarp) {
+    att_groups(p, s, V);
+    if (t0 < t1) att_scales<R, E4>(s, smem, bars, att_tiles(s, t0, t1));
   } else if (t0 < t1) {
     if (warp < kAttLoadWarp) {
       att_dequant<R, E4>(s, smem, bars, att_tiles(s, t0, t1));
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, t0, t1);
-    } else if (warp == kAttScaleWarp) {
-      att_scales<R, E4>(s, smem, bars, att_tiles(s, t0, t1));
     } else if (warp == kAttScoreWarp) {
       att_mma_scores<R, E4>(s, base, bars, tmem, t0, t1);
     } else if (warp == kAttOutputWarp) {
@@ -946,6 +964,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   __syncthreads();
   tc_fence_after();
   __syncwarp();
+  if (tid == 0 && s.fail) atomicOr(&g_device_status, kDevStatusWaitTimeout);
   if (warp == kAttScoreWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -953,16 +972,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 // Join: the pieces of a row group that several CTAs worked on, in their
 // order, so that the result does not depend on which CTA was first.  A job is
 // a row, or 128 of its 512 latents where there are few rows; the CTA's eight
-// warps take the pieces in turn.  Bound by latency: M, l and the first pieces'
-// sums are asked for together, the lengths before the wait for the attention
-// kernel.  Two CTAs per SM: with one, 32 sequences of up to 8191 tokens take
-// 39.7 us instead of 35.1 (both kernels), with three 40.3.
+// warps take the pieces in turn.  Bound by latency: what the attention kernel
+// noted of the row groups, then M, l and the first pieces' sums at once.  Two
+// CTAs per SM: with one, 32 sequences of up to 8191 tokens took 39.7 us
+// instead of 35.1 (both kernels), with three 40.3.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtasPerSm = 2;
 
 struct JoinShared {
-  AttSchedule s;
+  AttGroup group[kAttMaxSeqs];
   int split[kAttMaxSeqs];
   int split_warp[8];
   float m[8];
@@ -1033,19 +1052,24 @@ __device__ __forceinline__ float join_sums(JoinShared& j, int np, int r, int col
 
 template <int R>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
-    mlaqp_kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, const int grid) {
+    mlaqp_kv4_join_kernel(const __grid_constant__ Kv4AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   JoinShared& j = *reinterpret_cast<JoinShared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // This kernel starts once every CTA of the attention kernel has passed its
-  // own wait, so the lengths, which that one does not write, may be read now.
-  const int V = att_schedule(p, R, j.s, false);
-  const int* prefix = j.s.prefix;
-  const int total = prefix[V];
-  const AttCut cut(total, grid);
+  const int rows = p.q_len * p.H, groups = (rows + R - 1) / R, V = p.B * groups;
+  const int per_group = min(R, rows);
+  // (No early launch of what follows: with it, 64 sequences of up to 32768
+  // tokens took 164 us a call instead of 159, one call behind the other.)
+  pdl_wait();
+  static_assert(kJoinThreads == kAttMaxSeqs, "a thread a row group");
+  AttGroup mine = {0, 0, 0, 0};
+  if (tid < V) mine = reinterpret_cast<const AttGroup*>(p.ws)[tid];
+  // (an attention kernel that gave up before it noted anything)
+  if (mine.slot < 0 || mine.pieces > min(static_cast<int>(gridDim.x) / kJoinCtasPerSm, kAttMaxCtas) - (mine.slot >> 1))
+    mine.pieces = 0;
+  j.group[tid] = mine;
   // the row groups that more than one CTA worked on, in order
-  const bool split =
-      tid < V && prefix[tid + 1] > prefix[tid] && cut.owner(prefix[tid]) != cut.owner(prefix[tid + 1] - kAttEndTiles - 1);
+  const bool split = mine.pieces > 1;
   const unsigned who = __ballot_sync(0xffffffffu, split);
   if (lane == 0) j.split_warp[warp] = __popc(who);
   __syncthreads();
@@ -1056,20 +1080,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   }
   if (split) j.split[rank] = tid;
   __syncthreads();
-  pdl_launch_dependents();
-  pdl_wait();
-  const int rows = p.q_len * p.H, groups = (rows + R - 1) / R;
-  const int per_group = min(R, rows);
   const int cuts = n_split * per_group * 4 <= static_cast<int>(gridDim.x) ? 4 : 1;
   const int jobs = n_split * per_group * cuts;
   for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
     const int v = j.split[job / (per_group * cuts)], r = job / cuts % per_group, col = job % cuts * 128;
     const int rr = (v % groups) * R + r;
     if (rr >= rows) continue;
-    const int c0 = cut.owner(prefix[v]), np = cut.owner(prefix[v + 1] - kAttEndTiles - 1) - c0 + 1;
-    const bool inside = prefix[v] > cut.begin(c0);  // the first piece begins inside its CTA's stretch
-    const float* const base = reinterpret_cast<const float*>(p.ws) + 2 * c0 * att_slot_floats<R>();
-    auto slot = [&](int c) { return base + (2 * c + (c == 0 && inside ? 1 : 0)) * att_slot_floats<R>(); };
+    const int np = j.group[v].pieces, at = j.group[v].slot;
+    const float* const base = reinterpret_cast<const float*>(p.ws + kAttGroupBytes);
+    auto slot = [&](int c) { return base + (c == 0 ? at : (at & ~1) + 2 * c) * att_slot_floats<R>(); };
     const float top = cuts == 1 ? join_sums<R, 4>(j, np, r, 0, slot) : join_sums<R, 1>(j, np, r, col, slot);
     __syncthreads();
     const int n = kLatent / cuts;
@@ -1078,7 +1097,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     for (int w = 0; w < 8; ++w) sum += j.wsum[w];
     const int i = rr / p.H, h = rr % p.H;
     const int64_t q = static_cast<int64_t>(v / groups) * p.q_len + i;
-    const bool none = j.s.len[v] - (p.q_len - 1 - i) <= 0;
+    const bool none = j.group[v].len - (p.q_len - 1 - i) <= 0;
     const float inv = 1.f / sum;
     if (2 * tid < n) {
       float2 o = make_float2(0.f, 0.f);
@@ -1121,8 +1140,8 @@ AttKernels att_pick(int q_len, int H, bool e4m3) {
 
 cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream) {
   const AttKernels k = att_pick(p.q_len, p.H, q_e4m3);
-  int ctas = sm_count < kAttMaxCtas ? sm_count : kAttMaxCtas;
-  void* args[2] = {const_cast<Kv4AttendParams*>(&p), &ctas};
+  const int ctas = sm_count < kAttMaxCtas ? sm_count : kAttMaxCtas;
+  void* args[1] = {const_cast<Kv4AttendParams*>(&p)};
   const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(ctas), kAttThreads, k.smem, stream, args);
   if (e != cudaSuccess) return e;
   return kv4_launch(k.join, static_cast<unsigned>(kJoinCtasPerSm * sm_count), kJoinThreads, sizeof(JoinShared), stream,
@@ -1146,7 +1165,7 @@ cudaError_t kv4_attend_setup() {
 
 int64_t kv4_attend_workspace(int, int q_len, int H, int sm_count) {
   const int64_t slot = q_len * H <= 16 ? att_slot_floats<16>() : att_slot_floats<32>();
-  return 2 * sm_count * slot * 4;
+  return kAttGroupBytes + 2 * sm_count * slot * 4;
 }
 
 cudaError_t device_status_kv4_attend(unsigned int* value, bool reset) { return read_device_status(value, reset); }

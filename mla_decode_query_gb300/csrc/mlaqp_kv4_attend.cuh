@@ -321,7 +321,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // Everything that follows from the lengths: the tiles of each row group and
-// the stretch of this CTA.  All kAttThreads (or more than 256) threads call.
+// the stretch of this CTA.  All threads call.
 __device__ __forceinline__ int att_schedule(const Kv4AttendParams& p, int R, AttSchedule& s, bool tell) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = (p.q_len * p.H + R - 1) / R;
@@ -380,18 +380,23 @@ struct AttCut {
     rem = total - base * n;
   }
   __device__ __forceinline__ int begin(int c) const { return base * c + rem * c / n; }
-  // The stretch that holds tile t: a guess that is off by one at most, put right.
-  __device__ __forceinline__ int owner(int t) const {
-    int c = min(n - 1, static_cast<int>(static_cast<float>(t) / (static_cast<float>(base) + static_cast<float>(rem) / n)));
-    while (c + 1 < n && begin(c + 1) <= t) ++c;
-    while (c > 0 && begin(c) > t) --c;
-    return c;
+  // The stretch that holds place t: the last c with total * c / n < t + 1.
+  __device__ __forceinline__ int owner(int total, int t) const {
+    return static_cast<int>((static_cast<uint64_t>(t + 1) * n - 1) / static_cast<uint32_t>(total));
   }
 };
 constexpr int kAttMaxCtas = 256;
 
-// Workspace: slot 2c for the piece that begins CTA c's stretch, 2c+1 for one
-// that begins inside it; R rows of 512 sums, then M and l of each row.
+// Workspace: for each row group, what the join kernel has to know of it; then
+// the pieces, slot 2c for the one that begins CTA c's stretch, 2c+1 for one
+// that begins inside it: R rows of 512 sums, then M and l of each row.
+struct alignas(16) AttGroup {
+  int slot;    // of its first piece; the others are slots 2c of the CTAs that follow
+  int pieces;  // 0: no tile, 1: written by its CTA
+  int len;     // of its sequence
+  int unused;
+};
+constexpr int kAttGroupBytes = kAttMaxSeqs * static_cast<int>(sizeof(AttGroup));
 template <int R>
 __host__ __device__ constexpr int64_t att_slot_floats() { return R * (kLatent + 2); }
 
