@@ -931,7 +931,6 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
   const int t0 = s.begin, t1 = s.end;
   const uint32_t base = smem_u32(smem);
@@ -1058,8 +1057,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = p.q_len * p.H, groups = (rows + R - 1) / R, V = p.B * groups;
   const int per_group = min(R, rows);
-  // (No early launch of what follows: with it, 64 sequences of up to 32768
-  // tokens took 164 us a call instead of 159, one call behind the other.)
+  // Neither kernel lets the one behind it start early: its CTAs would find no
+  // room beside the attention's, and calls one behind the other took longer
+  // (64 sequences of up to 32768 tokens 164 us instead of 159, one of 131071
+  // 26.5 instead of 25.0).
   pdl_wait();
   static_assert(kJoinThreads == kAttMaxSeqs, "a thread a row group");
   AttGroup mine = {0, 0, 0, 0};
