@@ -729,16 +729,15 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
         l[r + 1] = fmaf(e1, its, l[r + 1]);
         l[r + 2] = fmaf(e2, its, l[r + 2]);
         l[r + 3] = fmaf(e3, its, l[r + 3]);
-        // three E5M2 terms: the top bytes of FP16 are E5M2, truncated; the
-        // differences are exact, the last term is rounded
+        // three E5M2 terms: the top bytes of FP16, rounded, are E5M2 and the
+        // differences exact.  Rounding to nearest leaves at most half a step,
+        // so three terms of 3 bits hold FP16's 11 (truncated, they held 9:
+        // up to 2^-9.2 off).  A NaN may round to zero here: it is in l.
         __half2 a = __floats2half2_rn(e0, e1), c = __floats2half2_rn(e2, e3);
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-          uint32_t au = *reinterpret_cast<uint32_t*>(&a), cu = *reinterpret_cast<uint32_t*>(&c);
-          if (q == 2) {
-            au += 0x00800080u;
-            cu += 0x00800080u;
-          }
+          const uint32_t au = *reinterpret_cast<uint32_t*>(&a) + 0x00800080u;
+          const uint32_t cu = *reinterpret_cast<uint32_t*>(&c) + 0x00800080u;
           terms[q][r / 4] = prmt(au, cu, 0x7531u);
           if (q < 2) {
             uint32_t ah = au & 0xFF00FF00u, ch = cu & 0xFF00FF00u;

@@ -23,9 +23,11 @@
 //       E4M3 terms hi + lo/16: a BF16 significand has 8 bits, two terms of 4
 //       hold it, elements below 2^-20 of the row's maximum lose their tail.
 //       E4M3 queries are used as they are.  The terms are extra N rows.
-//   P   FP16 (11 bits), cut into three E5M2 terms, again extra N rows: 9
-//       bits or more down to 2^-20 of the maximum, and absolute steps of 2^-28
-//       below, so that 2^17 tokens far below the maximum still add up.
+//   P   FP16 (11 bits) as three E5M2 terms, each rounded to nearest, again
+//       extra N rows: together exactly that FP16 number down to 2^-18 of the
+//       maximum (of p_t * 2^s_t over the tokens), and absolute steps of 2^-28
+//       below, so that 2^17 tokens far below the maximum still add up.  l sums
+//       the FP32 values: statistics keep 32 bits.
 // The MMAs cost what the A tile's reads from shared memory cost, so the
 // extra rows are free.
 //
