@@ -1,7 +1,11 @@
-"""Attention over the 4-bit cache where its arithmetic can be told closely:
-probabilities keep FP16's 11 bits.
+"""Attention over the 4-bit cache where its arithmetic can be told to a token:
+every visible token counts once wherever the work is cut, and probabilities
+keep FP16's 11 bits.
 
 Tolerances, from the number formats:
+  every token once   with queries of zero all weights are 1/n and every code
+                     and sum is exact in FP32, so x is off by its rounding to
+                     BF16 alone: 2^-9 |x|, doubled.  lse is ln n: 1e-5.
   probabilities      2^-9 |x| for BF16, and 2^-11 sum_t p |K| for FP16
                      probabilities; 2^-14 sum_t p |K| covers the scores (sums
                      of four products, a factor of log2 e rounded to FP32) and
@@ -12,9 +16,39 @@ import numpy as np
 import pytest
 
 from oracle import kv4_oracle as ko
-from test_gpu_kv4_attend import Case, _bits, _ok
+from test_gpu_kv4_attend import Case, _bits, _device_status, _ok
 
 pytestmark = pytest.mark.gpu
+
+
+def _one_column_a_token(rng, T):
+    """Token t holds 1.0 in latent 37 t mod 512 and nothing else."""
+    r = np.zeros((T, 576), dtype=np.float32)
+    t = np.arange(T)
+    r[t, 37 * t % 512] = 1.0
+    return _bits(r)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len,H", [(1, 16), (1, 5), (2, 16), (7, 8)])
+@pytest.mark.parametrize("lens", [[20000], [9000, 40, 5000], [40001, 129], [127, 128, 129, 383, 385], [3000] * 9])
+def test_every_token_counts_once(cuda_device, lens, q_len, H, dtype):
+    c = Case(lens, P=64, q_len=q_len, H=H, dtype=dtype, rows=_one_column_a_token, q=lambda rng, M, H: np.zeros((M, H, 576)))
+    _device_status()
+    _ok(c.run())
+    x, lse = c.outputs()
+    assert _device_status() == 0
+    first = 0
+    for b, length in enumerate(lens):
+        for i in range(q_len):
+            n = length - (q_len - 1 - i)
+            count = np.bincount(37 * (first + np.arange(n)) % 512, minlength=512)
+            want = count / n
+            assert count.max() < 2 ** 7  # so that a token more or less shows beside 2^-8 of its column
+            m = b * q_len + i
+            assert (np.abs(x[m] - want) <= 2.0 ** -8 * want).all(), (b, i)
+            assert (np.abs(lse[m] - np.log(n)) <= 1e-5).all(), (b, i)
+        first += length
 
 
 def balanced(lens, H, q_len, seed):
