@@ -110,7 +110,8 @@ int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int 
  *
  * so the last query token sees the whole sequence and the ones before it one
  * token less each (the cache already holds the query tokens' own entries).
- * A row that sees nothing (n <= 0) gets x = 0 and lse = -infinity.  Scores,
+ * A row that sees nothing (n <= 0, or all of its tokens left out, see below)
+ * gets x = 0 and lse = -infinity.  Scores,
  * softmax and sums are FP32; latents are used exactly where the block's scale
  * byte is at most 14 below the largest of its token, in steps of 2^-15 of
  * that largest scale where it is further below, probabilities with 8 bits or

@@ -801,7 +801,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
       const int64_t xo = s.xoff[turn][row];
       const bool first = (warp & 3) == 0;
       if (complete) {
-        const bool none = s.limit[turn][row] <= 0;
+        const bool none = sum == 0.f;  // no token, or none whose page is there (a NaN is not 0)
         alpha[lane] = none ? 0.f : 1.f / sum;
         if (first && xo >= 0 && p.lse)
           p.lse[s.lseoff[turn][row]] = none ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
@@ -868,7 +868,7 @@ __device__ __forceinline__ void att_empty_rows(const Kv4AttendParams& p, const A
 // CTA, the lengths' latency and these quotients were 2 us.
 __device__ __forceinline__ void att_groups(const Kv4AttendParams& p, const AttSchedule& s, int V) {
   for (int v = 32 * blockIdx.x + (threadIdx.x & 31); v < V; v += 32 * gridDim.x) {
-    AttGroup g = {0, 0, s.len[v], 0};
+    AttGroup g = {0, 0};
     if (s.prefix[v] < s.prefix[v + 1]) {
       const AttCut cut(s.prefix[V], gridDim.x);
       const int c = cut.owner(s.prefix[V], s.prefix[v]);
@@ -1017,7 +1017,7 @@ __device__ __forceinline__ float join_sums(JoinShared& j, int np, int r, int col
 #pragma unroll
   for (int w = 1; w < 8; ++w) top = fmaxf(top, j.m[w]);
   if (tid < np) {
-    j.weight[tid] = ex2(m - top);
+    j.weight[tid] = m == -INFINITY ? 0.f : ex2(m - top);  // nothing summed: also where that is all pieces'
     j.l[tid] = l;
   }
   __syncthreads();
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   // 26.5 instead of 25.0).
   pdl_wait();
   static_assert(kJoinThreads == kAttMaxSeqs, "a thread a row group");
-  AttGroup mine = {0, 0, 0, 0};
+  AttGroup mine = {0, 0};
   if (tid < V) mine = reinterpret_cast<const AttGroup*>(p.ws)[tid];
   // (an attention kernel that gave up before it noted anything)
   if (mine.slot < 0 || mine.pieces > min(static_cast<int>(gridDim.x) / kJoinCtasPerSm, kAttMaxCtas) - (mine.slot >> 1))
@@ -1097,7 +1097,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     for (int w = 0; w < 8; ++w) sum += j.wsum[w];
     const int i = rr / p.H, h = rr % p.H;
     const int64_t q = static_cast<int64_t>(v / groups) * p.q_len + i;
-    const bool none = j.group[v].len - (p.q_len - 1 - i) <= 0;
+    const bool none = sum == 0.f;
     const float inv = 1.f / sum;
     if (2 * tid < n) {
       float2 o = make_float2(0.f, 0.f);

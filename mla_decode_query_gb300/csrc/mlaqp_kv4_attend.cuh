@@ -15,6 +15,7 @@
 //   y = (D * 2^(s_t-133) + Dr) * C_r + (s_t-133)      log2 units
 //   P = 2^(y - M_r + 12)     l_r += P * 2^(133-s_t)   M_r the running maximum
 //   x[r,n] = O[n,r] / l_r    lse_r = ln l_r + (M_r-12) ln 2
+//   (l_r = 0, no token there to be seen: 0 and -infinity)
 // Dr is the rope part, a BF16 product of its own; C_r holds the softmax
 // scale, log2 e and the row's power of two.
 //
@@ -391,11 +392,9 @@ constexpr int kAttMaxCtas = 256;
 // Workspace: for each row group, what the join kernel has to know of it; then
 // the pieces, slot 2c for the one that begins CTA c's stretch, 2c+1 for one
 // that begins inside it: R rows of 512 sums, then M and l of each row.
-struct alignas(16) AttGroup {
+struct alignas(8) AttGroup {
   int slot;    // of its first piece; the others are slots 2c of the CTAs that follow
   int pieces;  // 0: no tile, 1: written by its CTA
-  int len;     // of its sequence
-  int unused;
 };
 constexpr int kAttGroupBytes = kAttMaxSeqs * static_cast<int>(sizeof(AttGroup));
 template <int R>
