@@ -173,7 +173,9 @@ int mlaqp_kv4_extend(int32_t* block_table, int64_t block_table_stride, int num_s
  * pages are shared (their counts rise); of a partly filled last page the
  * tokens are copied into a new page in every layer, so parent and child can
  * both grow.  A parent may occur several times.  Lengths count as they were
- * before the call, so a child is an empty parent to the other items.
+ * before the call, so a child is an empty parent to the other items.  An item
+ * whose parent holds a page out of range is left out: its child stays empty and
+ * it takes no free page.
  */
 int mlaqp_kv4_fork(int32_t* block_table, int64_t block_table_stride, int num_seqs, int32_t* seq_lens,
                    int32_t* ref_count, int num_pages, int page_size, const int32_t* parents,

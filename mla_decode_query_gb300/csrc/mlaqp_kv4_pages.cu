@@ -220,6 +220,24 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_fork_kernel(const __gr
     tok[i] = ok ? len : -1;
   }
   __syncthreads();
+  // A parent with a page that is none is left out before free pages are
+  // counted: neither its child nor a count may learn of it halfway.
+  for (int i = warp; i < p.n; i += kPlanWarps) {
+    const int len = tok[i];
+    if (len <= 0) continue;
+    const int32_t* from = t.block_table + p.list_a[i] * t.stride;
+    const int pages = static_cast<int>((static_cast<int64_t>(len) + mask) >> t.shift);
+    bool bad = false;
+    for (int j = lane; j < pages; j += 32) {
+      const int pg = from[j];
+      bad |= pg < 0 || pg >= t.num_pages;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) {
+      report(kDevStatusBadIndex);
+      tok[i] = -1;
+    }
+  }
+  __syncthreads();
   int taken = 0;
   for (int base = 0; base < p.n; base += kPlanThreads) {
     const int i = base + tid;
@@ -249,15 +267,11 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_fork_kernel(const __gr
         for (int j = lane; j < full; j += 32) {
           const int pg = from[j];
           row[j] = pg;
-          if (pg >= 0 && pg < t.num_pages) atomicAdd(&t.ref_count[pg], 1); else report(kDevStatusBadIndex);
+          atomicAdd(&t.ref_count[pg], 1);
         }
         if (tail) {
           job_src = from[full];
           job_dst = kth_page(map, s.prefix, wpt, s.first[k]);
-          if (job_src < 0 || job_src >= t.num_pages) {
-            if (lane == 0) report(kDevStatusBadIndex);
-            job_src = -1;
-          }
         }
         if (lane == 0) {
           if (tail) {

@@ -141,6 +141,9 @@ class Tables:
         for p, c in zip(parents, children):
             if not (0 <= p < len(before)) or not (0 <= c < len(before)) or p == c or before[c] != 0:
                 continue
+            held = self.table[p, :self._pages(before[p])]
+            if ((held < 0) | (held >= len(self.ref))).any():
+                continue
             full, tail = divmod(int(before[p]), P)
             if tail:
                 asked += 1

@@ -1,11 +1,13 @@
 """What the device finds out of range is left out, reported, and nothing else
-changes: pages of the attention."""
+changes: pages of the attention, parents of a fork."""
 
 import numpy as np
 import pytest
+import torch
 
 import mla_decode_query_gb300 as mq
 from test_gpu_kv4_attend import Case, _device_status, _ok
+from test_gpu_kv4_pages import Pool, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +57,44 @@ def test_a_nan_beside_bad_pages_still_spoils_its_row(cuda_device):
         x, lse = c.outputs()
         assert np.isnan(x).all() and np.isnan(lse).all()
     _device_status()
+
+
+class Rows(Pool):
+    """A pool whose tables are written to on the device behind the oracle's back."""
+
+    def put(self, seq, j, page):
+        self.table[seq, j] = page
+        self.o.table[seq, j] = page
+
+
+@pytest.mark.parametrize("bad", [-1, 40, 1 << 26, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("at", [0, 2, 3])
+def test_a_fork_from_a_row_with_a_bad_page_is_left_out(cuda_device, at, bad):
+    # three full pages and a tail; the items around it go through, with the
+    # pages that they would get without it
+    p = Rows(8, 6, 40, 16)
+    p.extend([0, 1, 2], [53, 20, 37], 53)
+    p.put(0, at, bad)
+    _device_status()
+    before = p.table.clone()
+    _ok(mq.mlaqp_kv4_fork(*p.tables(), _i32([1, 0, 2, 0]), _i32([3, 4, 5, 6]), 4, *p.pool(), p.ws, p.ws.numel()))
+    assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
+    p.o.fork([1, 0, 2, 0], [3, 4, 5, 6], p.caches)
+    assert p.o.lens.tolist() == [53, 20, 37, 20, 0, 37, 0, 0]
+    p.check()
+    assert torch.equal(p.table[[4, 6]], before[[4, 6]])
+
+
+def test_a_fork_of_full_pages_only_checks_them_all(cuda_device):
+    p = Rows(4, 80, 100, 16)
+    p.extend([0], [64 * 16], 64 * 16)
+    p.put(0, 63, 100)
+    _device_status()
+    _ok(mq.mlaqp_kv4_fork(*p.tables(), _i32([0]), _i32([1]), 1, *p.pool(), p.ws, p.ws.numel()))
+    assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
+    p.check()
+    p.put(0, 63, p.o.table[0, 0])
+    p.put(0, 64, -1)  # behind its length: not looked at
+    p.fork([0], [1])
+    assert _device_status() == 0
+    p.check()
