@@ -301,14 +301,16 @@ __global__ void __launch_bounds__(128) mlaqp_kv4_release_kernel(const __grid_con
     if (threadIdx.x == 0) report(kDevStatusBadIndex);
     return;
   }
-  // the exchange lets a sequence that is listed twice go once only
-  if (threadIdx.x == 0) s_len = atomicExch(&t.seq_lens[seq], 0);
+  // The exchange lets a sequence that is listed twice go once only; a bad
+  // length stays as it is.
+  if (threadIdx.x == 0) {
+    const int len = t.seq_lens[seq];
+    const bool ok = len >= 0 && len <= t.stride << t.shift;
+    if (!ok) report(kDevStatusBadIndex);
+    s_len = ok && atomicCAS(&t.seq_lens[seq], len, 0) == len ? len : 0;
+  }
   __syncthreads();
   const int len = s_len;
-  if (len < 0 || len > t.stride << t.shift) {
-    if (threadIdx.x == 0) report(kDevStatusBadIndex);
-    return;
-  }
   const int pages = static_cast<int>((static_cast<int64_t>(len) + (1 << t.shift) - 1) >> t.shift);
   int32_t* row = t.block_table + seq * t.stride;
   for (int j = threadIdx.x; j < pages; j += blockDim.x) {

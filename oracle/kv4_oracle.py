@@ -163,6 +163,8 @@ class Tables:
 
     def release(self, seqs):
         for s in seqs:
+            if not 0 <= self.lens[s] <= self.table.shape[1] * self.page_size:
+                continue
             for j in range(self._pages(self.lens[s])):
                 self.ref[self.table[s, j]] -= 1
                 self.table[s, j] = -1

@@ -1,5 +1,6 @@
 """What the device finds out of range is left out, reported, and nothing else
-changes: pages of the attention, parents of a fork."""
+changes: pages of the attention, parents of a fork, lengths of a
+release."""
 
 import numpy as np
 import pytest
@@ -97,4 +98,18 @@ def test_a_fork_of_full_pages_only_checks_them_all(cuda_device):
     p.put(0, 64, -1)  # behind its length: not looked at
     p.fork([0], [1])
     assert _device_status() == 0
+    p.check()
+
+
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 6 * 16 + 1, 2 ** 31 - 1])
+def test_a_release_of_a_bad_length_is_left_out(cuda_device, length):
+    p = Pool(4, 6, 20, 16)
+    p.extend([0, 1, 2], [40, 16, 5], 40)
+    p.lens[1] = length
+    p.o.lens[1] = length
+    _device_status()
+    _ok(mq.mlaqp_kv4_release(*p.tables(), _i32([0, 1, 1, 2]), 4))
+    assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
+    p.o.release([0, 1, 1, 2])
+    assert p.o.lens.tolist() == [0, length, 0, 0]
     p.check()
