@@ -158,8 +158,9 @@ int64_t mlaqp_kv4_attend_workspace(int B, int q_len, int H, int device);
 /*
  * Grow sequences by new_tokens[i] (>= 0) tokens: take the pages this needs
  * and write the new tokens' slots to slots[i*max_new + k], k <
- * new_tokens[i] (-1 behind them).  new_tokens[i] > max_new, or a row too
- * short, is reported and leaves the sequence as it was.  Item i takes the
+ * new_tokens[i] (-1 behind them).  new_tokens[i] > max_new, a row too short,
+ * or new tokens that would begin in a page out of range, is reported and
+ * leaves the sequence as it was (its slots: -1).  Item i takes the
  * free pages behind those that the items before it ask for, so where pages
  * run out the items that still fit are the first ones.
  */

@@ -143,6 +143,10 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_extend_kernel(const __
         const int64_t end = static_cast<int64_t>(len) + add;
         ok = len >= 0 && end <= t.stride << t.shift && end <= 0x7fffffff;
       }
+      if (ok && add > 0 && (len & mask) != 0) {  // the page that the new tokens begin in
+        const int pg = t.block_table[seq * t.stride + (len >> t.shift)];
+        ok = pg >= 0 && pg < t.num_pages;
+      }
       if (ok) {
         // in 64 bits: a length near the int's end plus the page's mask
         need = static_cast<int>((static_cast<int64_t>(len) + add + mask) >> t.shift) -

@@ -121,6 +121,8 @@ class Tables:
             if not (0 <= s < len(self.lens)) or not (0 <= k <= max_new) or \
                     self.lens[s] + k > self.table.shape[1] * P:
                 continue
+            if k and self.lens[s] % P and not 0 <= self.table[s, self.lens[s] // P] < len(self.ref):
+                continue
             have, end = self._pages(self.lens[s]), self._pages(self.lens[s] + k)
             first, asked = asked, asked + end - have
             if end > have and asked > len(free):

@@ -1,6 +1,6 @@
 """What the device finds out of range is left out, reported, and nothing else
 changes: pages of the attention, parents of a fork, lengths of a
-release."""
+release, the page that an extension goes on in."""
 
 import numpy as np
 import pytest
@@ -112,4 +112,25 @@ def test_a_release_of_a_bad_length_is_left_out(cuda_device, length):
     assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
     p.o.release([0, 1, 1, 2])
     assert p.o.lens.tolist() == [0, length, 0, 0]
+    p.check()
+
+
+@pytest.mark.parametrize("bad", [-1, 20, 1 << 28, 2 ** 31 - 1])
+def test_an_extension_of_a_bad_page_is_left_out(cuda_device, bad):
+    p = Rows(5, 4, 20, 16)
+    p.extend([0, 1, 2, 3], [18, 16, 3, 18], 18)
+    p.put(0, 1, bad)
+    p.put(1, 0, bad)  # full: what is added begins a page of its own
+    p.put(3, 0, bad)  # not the page that goes on
+    _device_status()
+    slots = torch.full((5, 20), 77, dtype=torch.int32, device="cuda")
+    _ok(mq.mlaqp_kv4_extend(*p.tables(), _i32([0, 1, 2, 3, 4]), _i32([20, 2, 14, 1, 16]), 5, slots, 20))
+    assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
+    got = slots.cpu().numpy()
+    assert (got[0] == -1).all()
+    np.testing.assert_array_equal(got, p.o.extend([0, 1, 2, 3, 4], [20, 2, 14, 1, 16], 20))
+    assert p.o.lens.tolist() == [18, 18, 17, 19, 16]
+    p.check()
+    p.extend([0], [0], 1)  # nothing added: nothing to write to
+    assert _device_status() == 0
     p.check()
