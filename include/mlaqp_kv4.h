@@ -192,7 +192,8 @@ int mlaqp_kv4_release(int32_t* block_table, int64_t block_table_stride, int num_
 /*
  * Compact: with n pages live, the k-th free page below index n receives the
  * k-th live page at or above n, in every layer; tables and counts follow,
- * *n_live = n.  Afterwards pages n and above are free.
+ * *n_live = n.  Afterwards pages n and above are free.  A table entry at or
+ * above n whose page is out of range or counts 0 is reported and stays.
  */
 int mlaqp_kv4_compact(int32_t* block_table, int64_t block_table_stride, int num_seqs,
                       int32_t* seq_lens, int32_t* ref_count, int num_pages, int page_size, void* cache,

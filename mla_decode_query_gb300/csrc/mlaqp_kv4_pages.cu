@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(128) mlaqp_kv4_release_kernel(const __grid_con
   }
 }
 
-// Workspace of a compaction: src[half], dst[half], then remap[num_pages].
+// Workspace of a compaction: src[half], dst[half], then job[num_pages], which
+// move a page is part of (written for moved pages only).
 __host__ __device__ inline int compact_half(int num_pages) { return num_pages / 2 + 1; }
 
 __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_compact_kernel(const __grid_constant__ Kv4PagesParams p) {
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_compact_kernel(const _
   const unsigned long long at = block_exclusive(mine, s.scan64, &total);
   int32_t* src = p.ws + kJobsAt;
   int32_t* dst = src + compact_half(t.num_pages);
-  int32_t* remap = dst + compact_half(t.num_pages);
+  int32_t* job = dst + compact_half(t.num_pages);
   int h = static_cast<int>(at >> 32), m = static_cast<int>(at & 0xffffffffu);
   for (int w = w0; w < w1; ++w) {
     for (uint32_t b = ~map[w] & below(w); b; b &= b - 1) dst[h++] = 32 * w + __ffs(b) - 1;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_compact_kernel(const _
   const int moves = static_cast<int>(total & 0xffffffffu);
   for (int k = tid; k < moves; k += kPlanThreads) {
     const int a = src[k], b = dst[k];
-    remap[a] = b;
+    job[a] = k;
     t.ref_count[b] = t.ref_count[a];
     t.ref_count[a] = 0;
   }
@@ -371,15 +372,16 @@ __global__ void __launch_bounds__(kPlanThreads) mlaqp_kv4_compact_kernel(const _
 
 // Move page contents: job k copies the first tok[k] tokens (tok null: the
 // whole page) of page src[k] to page dst[k] in every layer; a negative index
-// is no job.  remap, when given, also rewrites the table entries that point
-// at or above *n_live.
+// is no job.  job, when given, also rewrites the table entries that point at
+// or above *n_live: those whose page is a job's source, so that what an earlier
+// call left in the workspace counts for nothing.
 struct CopyJobs {
   const int32_t* count;  // null: n
   int n;
   const int32_t* src;
   const int32_t* dst;
   const int32_t* tok;
-  const int32_t* remap;
+  const int32_t* job;
   const int32_t* n_live;
 };
 
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kCopyThreads)
         if (v0 + u * kCopyThreads < vecs) st_u128(to + off[u], v[u]);
     }
   }
-  if (jobs.remap == nullptr) return;
+  if (jobs.job == nullptr) return;
   const int live = *jobs.n_live;
   const int64_t entries = t.num_seqs * t.stride;
   for (int64_t i = blockIdx.x * kCopyThreads + threadIdx.x; i < entries; i += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
@@ -428,7 +430,8 @@ __global__ void __launch_bounds__(kCopyThreads)
     if ((i % t.stride) << t.shift >= len) continue;
     const int pg = t.block_table[i];
     if (pg < live) continue;  // in place, or none
-    if (pg < t.num_pages) t.block_table[i] = jobs.remap[pg]; else report(kDevStatusBadIndex);
+    const int k = pg < t.num_pages ? jobs.job[pg] : -1;
+    if (k >= 0 && k < n && jobs.src[k] == pg) t.block_table[i] = jobs.dst[k]; else report(kDevStatusBadIndex);
   }
 }
 
@@ -441,7 +444,7 @@ cudaError_t launch_copy(const Kv4PagesParams& p, const CopyJobs& jobs, int sm_co
   void* args[3] = {&c, &t, &j};
   const int64_t tasks = static_cast<int64_t>(jobs.n) * p.cache.layers;
   const int64_t most = 8ll * sm_count;
-  const int64_t work = jobs.remap ? most : (tasks < most ? tasks : most);
+  const int64_t work = jobs.job ? most : (tasks < most ? tasks : most);
   return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_copy_kernel), static_cast<unsigned>(work), kCopyThreads, 0,
                     stream, args);
 }

@@ -1,6 +1,6 @@
 """What the device finds out of range is left out, reported, and nothing else
 changes: pages of the attention, parents of a fork, lengths of a
-release, the page that an extension goes on in."""
+release, the page that an extension goes on in, table entries of a compaction."""
 
 import numpy as np
 import pytest
@@ -133,4 +133,22 @@ def test_an_extension_of_a_bad_page_is_left_out(cuda_device, bad):
     p.check()
     p.extend([0], [0], 1)  # nothing added: nothing to write to
     assert _device_status() == 0
+    p.check()
+
+
+@pytest.mark.parametrize("left", [-1, 0, 3])
+@pytest.mark.parametrize("bad", [15, 19, 20, 2 ** 31 - 1])
+def test_an_entry_that_no_live_page_stands_for_stays_in_a_compaction(cuda_device, bad, left):
+    # whatever an earlier call left in the workspace
+    p = Rows(5, 4, 20, 16)
+    p.extend([0, 1, 2, 3], [40, 33, 3, 48], 48)
+    p.release([1])  # pages 3, 4, 5 are free: 7, 8 and 9 move there, 10..19 are free
+    p.put(2, 0, bad)
+    p.o.ref[6] = 0
+    p.ref[6] = 0
+    p.ws.view(torch.int32).fill_(left)
+    _device_status()
+    p.compact()
+    assert _device_status() == mq.MLAQP_DEVSTATUS_BAD_INDEX
+    assert p.o.table[2, 0] == bad
     p.check()
