@@ -1,5 +1,5 @@
 // Host-side services of the library shared by its translation units: the
-// thread's error message, the device check and the launch of one kernel.
+// thread's error message and the device check.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -163,7 +163,7 @@ int mlaqp_kv4_append(const void* latent, int64_t latent_token_stride, const void
   p.k_pe_ts = k_pe_token_stride;
   p.slots = slots;
   p.T = T;
-  return launched(mlaqp::kv4_append(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(mlaqp::kv4_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int page_size, const int32_t* slots, int T,
@@ -187,7 +187,7 @@ int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int 
   p.out_ts = out_token_stride;
   p.slots = slots;
   p.T = T;
-  return launched(mlaqp::kv4_gather(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(mlaqp::kv4_gather(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 namespace {

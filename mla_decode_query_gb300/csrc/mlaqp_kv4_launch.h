@@ -43,8 +43,8 @@ struct Kv4RowsParams {
   const int32_t* slots;
   int T;
 };
-cudaError_t kv4_append(const Kv4RowsParams& p, int sm_count, cudaStream_t stream);
-cudaError_t kv4_gather(const Kv4RowsParams& p, int sm_count, cudaStream_t stream);
+cudaError_t kv4_append(const Kv4RowsParams& p, cudaStream_t stream);
+cudaError_t kv4_gather(const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t kv4_rows_setup();
 
 // The sequence tables that the page operations change.

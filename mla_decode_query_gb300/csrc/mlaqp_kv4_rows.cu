@@ -126,16 +126,16 @@ unsigned rows_grid(int T, int each) {
 
 }  // namespace
 
-cudaError_t kv4_append(const Kv4RowsParams& p, int, cudaStream_t stream) {
+cudaError_t kv4_append(const Kv4RowsParams& p, cudaStream_t stream) {
   void* args[1] = {const_cast<Kv4RowsParams*>(&p)};
   return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_append_kernel), rows_grid(p.T, 1), kRowsThreads, 0, stream,
                     args);
 }
 
-cudaError_t kv4_gather(const Kv4RowsParams& p, int, cudaStream_t stream) {
+cudaError_t kv4_gather(const Kv4RowsParams& p, cudaStream_t stream) {
   void* args[1] = {const_cast<Kv4RowsParams*>(&p)};
-  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_gather_kernel), rows_grid(p.T, kGatherTokens), kRowsThreads, 0, stream,
-                    args);
+  return kv4_launch(reinterpret_cast<const void*>(&mlaqp_kv4_gather_kernel), rows_grid(p.T, kGatherTokens), kRowsThreads,
+                    0, stream, args);
 }
 
 cudaError_t kv4_rows_setup() {
