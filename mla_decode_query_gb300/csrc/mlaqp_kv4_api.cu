@@ -21,28 +21,50 @@ using mlaqp::host_device;
 using mlaqp::host_fail;
 using mlaqp::host_fail_cuda;
 
+// Kernels whose attributes are set together.  A build in which one group
+// cannot run leaves the others usable.
+enum Group { kRowsGroup, kPagesGroup, kAttend16Group, kAttend32Group, kGroups };
+
 constexpr int kMaxDevices = 64;
-std::atomic<bool> g_ready[kMaxDevices];
+std::atomic<bool> g_ready[kMaxDevices][kGroups];
 std::mutex g_ready_mutex;
 
-// The current (or given) device checked and the cache kernels' attributes
-// set on it, once per device.
-int kv4_device(int device, int* sm_count) {
+cudaError_t set_up(Group group) {
+  switch (group) {
+    case kRowsGroup: return mlaqp::kv4_rows_setup();
+    case kPagesGroup: return mlaqp::kv4_pages_setup();
+    case kAttend16Group: return mlaqp::kv4_attend_setup(16);
+    default: return mlaqp::kv4_attend_setup(32);
+  }
+}
+
+Group attend_group(int q_len, int H) {
+  return mlaqp::kv4_attend_rows(q_len, H) == 16 ? kAttend16Group : kAttend32Group;
+}
+
+// The current (or given) device checked and the group's kernels made ready on
+// it, once per device.  The first call sees to all groups, so that others may
+// have their first call inside a graph capture.
+int kv4_device(int device, Group group, int* sm_count) {
   int dev = 0;
   const int st = host_device(device, &dev, sm_count);
   if (st != MLAQP_OK) return st;
-  if (!g_ready[dev].load(std::memory_order_acquire)) {
+  std::atomic<bool>& ready = g_ready[dev][group];
+  if (!ready.load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(g_ready_mutex);
-    if (!g_ready[dev].load(std::memory_order_acquire)) {
+    if (!ready.load(std::memory_order_acquire)) {
       int prev = -1;
       cudaError_t e = cudaGetDevice(&prev);
       if (e == cudaSuccess && prev != dev) e = cudaSetDevice(dev);
-      if (e == cudaSuccess) e = mlaqp::kv4_rows_setup();
-      if (e == cudaSuccess) e = mlaqp::kv4_pages_setup();
-      if (e == cudaSuccess) e = mlaqp::kv4_attend_setup();
+      for (int g = 0; g < kGroups && e == cudaSuccess; ++g) {
+        if (g_ready[dev][g].load(std::memory_order_relaxed)) continue;
+        const cudaError_t up = set_up(static_cast<Group>(g));
+        if (up == cudaSuccess) g_ready[dev][g].store(true, std::memory_order_release);
+        else if (g == group) e = up;
+        else cudaGetLastError();  // its own calls will say so
+      }
       if (prev >= 0 && prev != dev) cudaSetDevice(prev);
       if (e != cudaSuccess) return host_fail_cuda("preparing the 4-bit cache kernels", e);
-      g_ready[dev].store(true, std::memory_order_release);
     }
   }
   return MLAQP_OK;
@@ -155,7 +177,7 @@ int mlaqp_kv4_append(const void* latent, int64_t latent_token_stride, const void
       overlaps(c, span(slots, 4ull * T)))
     return bad_arg("the cache overlaps an input");
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kRowsGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.latent = static_cast<const uint16_t*>(latent);
   p.k_pe = static_cast<const uint16_t*>(k_pe);
@@ -181,7 +203,7 @@ int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int 
   const Range o = span(out, 2ull * ((T - 1) * static_cast<uint64_t>(out_token_stride) + 576));
   if (overlaps(o, cache_span(p.cache)) || overlaps(o, span(slots, 4ull * T))) return bad_arg("out overlaps an input");
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kRowsGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.out = static_cast<uint16_t*>(out);
   p.out_ts = out_token_stride;
@@ -248,7 +270,7 @@ int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const f
       if (overlaps(outs[i], outs[j])) return bad_arg("x, lse and workspace overlap");
   }
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, attend_group(q_len, H), &sms);
   if (st != MLAQP_OK) return st;
   if (!workspace || !aligned(workspace, 16)) return bad_arg("workspace must be a 16-byte aligned buffer");
   if (workspace_bytes < mlaqp::kv4_attend_workspace(B, q_len, H, sms))
@@ -275,7 +297,7 @@ int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const f
 int64_t mlaqp_kv4_attend_workspace(int B, int q_len, int H, int device) {
   if (check_attend_sizes(B, q_len, H) != MLAQP_OK) return -1;
   int sms = 0;
-  if (kv4_device(device, &sms) != MLAQP_OK) return -1;
+  if (kv4_device(device, attend_group(q_len, H), &sms) != MLAQP_OK) return -1;
   return mlaqp::kv4_attend_workspace(B, q_len, H, sms);
 }
 
@@ -291,7 +313,7 @@ int mlaqp_kv4_extend(int32_t* block_table, int64_t block_table_stride, int num_s
   if (n == 0) return MLAQP_OK;
   if (!slots || !aligned(slots, 4)) return bad_arg("slots must be a 4-byte aligned buffer");
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kPagesGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.list_a = seqs;
   p.list_b = new_tokens;
@@ -316,7 +338,7 @@ int mlaqp_kv4_fork(int32_t* block_table, int64_t block_table_stride, int num_seq
   if (workspace_bytes < mlaqp::kv4_pages_workspace(num_pages, n))
     return bad_arg("workspace is smaller than mlaqp_kv4_pages_workspace()");
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kPagesGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.list_a = parents;
   p.list_b = children;
@@ -334,7 +356,7 @@ int mlaqp_kv4_release(int32_t* block_table, int64_t block_table_stride, int num_
   if (st != MLAQP_OK) return st;
   if (n == 0) return MLAQP_OK;
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kPagesGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.list_a = seqs;
   p.n = n;
@@ -354,7 +376,7 @@ int mlaqp_kv4_compact(int32_t* block_table, int64_t block_table_stride, int num_
   if (workspace_bytes < mlaqp::kv4_pages_workspace(num_pages, 0))
     return bad_arg("workspace is smaller than mlaqp_kv4_pages_workspace()");
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kPagesGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.n_live = n_live;
   p.ws = static_cast<int32_t*>(workspace);
@@ -370,7 +392,7 @@ int mlaqp_kv4_copy_pages(void* cache, int64_t page_stride, int64_t layer_stride,
   if (st != MLAQP_OK) return st;
   if (n == 0) return MLAQP_OK;
   int sms = 0;
-  st = kv4_device(-1, &sms);
+  st = kv4_device(-1, kPagesGroup, &sms);
   if (st != MLAQP_OK) return st;
   p.list_a = src;
   p.list_b = dst;
@@ -387,8 +409,9 @@ int64_t mlaqp_kv4_pages_workspace(int num_pages, int n) {
 }
 
 int mlaqp_kv4_prewarm(int device) {
-  int sms = 0;
-  return kv4_device(device, &sms);
+  int sms = 0, st = MLAQP_OK;
+  for (int g = 0; g < kGroups && st == MLAQP_OK; ++g) st = kv4_device(device, static_cast<Group>(g), &sms);
+  return st;
 }
 
 }  // extern "C"

@@ -1120,19 +1120,21 @@ struct AttKernels {
   const void* main;
   const void* join;
   int smem;
+  bool splits_regs;  // its warps share the launch's registers out anew
 };
 
 template <int R, bool E4>
 AttKernels att_kernels() {
   return AttKernels{reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<R, E4>),
-                    reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), AttPlan<R, E4>::Bytes};
+                    reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), AttPlan<R, E4>::Bytes,
+                    AttPlan<R, E4>::SoftRegs != kAttRegs};
 }
 
 // 16 rows where all (query token, head) pairs of a sequence fit, else groups
 // of 32, each reading the cache once: tensor memory holds no more (three
 // terms of P, four blocks of latents, 32 rows: 384 columns, and the scores).
 AttKernels att_pick(int q_len, int H, bool e4m3) {
-  if (q_len * H <= 16) return e4m3 ? att_kernels<16, true>() : att_kernels<16, false>();
+  if (kv4_attend_rows(q_len, H) == 16) return e4m3 ? att_kernels<16, true>() : att_kernels<16, false>();
   return e4m3 ? att_kernels<32, true>() : att_kernels<32, false>();
 }
 
@@ -1148,15 +1150,17 @@ cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cuda
                     args);
 }
 
-cudaError_t kv4_attend_setup() {
-  const AttKernels all[4] = {att_kernels<16, false>(), att_kernels<16, true>(), att_kernels<32, false>(),
-                             att_kernels<32, true>()};
-  for (const AttKernels& k : all) {
+int kv4_attend_rows(int q_len, int H) { return q_len * H <= 16 ? 16 : 32; }
+
+cudaError_t kv4_attend_setup(int rows) {
+  const AttKernels both[2] = {rows == 16 ? att_kernels<16, false>() : att_kernels<32, false>(),
+                              rows == 16 ? att_kernels<16, true>() : att_kernels<32, true>()};
+  for (const AttKernels& k : both) {
     cudaError_t e = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     cudaFuncAttributes a;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k.main);
-    // the warps share out what this many registers a thread make
-    if (e == cudaSuccess && a.numRegs < kAttRegs) e = cudaErrorInvalidKernelImage;
+    // a split shares out what this many registers a thread make; with fewer it would wait for them for ever
+    if (e == cudaSuccess && k.splits_regs && a.numRegs < kAttRegs) e = cudaErrorInvalidKernelImage;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k.join);
     if (e != cudaSuccess) return e;
   }
@@ -1164,7 +1168,7 @@ cudaError_t kv4_attend_setup() {
 }
 
 int64_t kv4_attend_workspace(int, int q_len, int H, int sm_count) {
-  const int64_t slot = q_len * H <= 16 ? att_slot_floats<16>() : att_slot_floats<32>();
+  const int64_t slot = kv4_attend_rows(q_len, H) == 16 ? att_slot_floats<16>() : att_slot_floats<32>();
   return kAttGroupBytes + 2 * sm_count * slot * 4;
 }
 

@@ -94,7 +94,8 @@ struct Kv4AttendParams {
   uint8_t* ws;
 };
 cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream);
-cudaError_t kv4_attend_setup();
+cudaError_t kv4_attend_setup(int rows);  // 16 or 32: the kernels for that many rows
+int kv4_attend_rows(int q_len, int H);   // of a row group
 int64_t kv4_attend_workspace(int B, int q_len, int H, int sm_count);
 
 }  // namespace mlaqp
