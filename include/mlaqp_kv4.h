@@ -111,13 +111,21 @@ int mlaqp_kv4_gather(const void* cache, int64_t page_stride, int num_pages, int 
  * so the last query token sees the whole sequence and the ones before it one
  * token less each (the cache already holds the query tokens' own entries).
  * A row that sees nothing (n <= 0, or all of its tokens left out, see below)
- * gets x = 0 and lse = -infinity.  Scores,
- * softmax and sums are FP32; latents are used exactly where the block's scale
- * byte is at most 14 below the largest of its token, in steps of 2^-15 of
- * that largest scale where it is further below, probabilities with 8 bits or
- * more; a NaN anywhere in a row's visible tokens, or a
- * NaN or an infinity in its q, makes that row NaN; what lies beyond the visible tokens is never
- * used.
+ * gets x = 0 and lse = -infinity.  Scores
+ * are summed, and softmax, sums and lse held, in FP32, from operands of fewer
+ * bits:
+ *   - latents exactly where the block's scale byte is at most 14 below the
+ *     largest of its token, in steps of 2^-15 of that largest scale where it is
+ *     further below (mlaqp_kv4_gather reads those exactly);
+ *   - BF16 queries exactly down to 2^-13 of the row's largest magnitude among
+ *     its 512 (or 2^-40 of the largest among its last 64, if that is more), in
+ *     steps of 2^-20 of it below; E4M3 queries and rope parts exactly;
+ *   - probabilities p_t, where they weigh latents, with 11 bits while p_t times
+ *     the token's largest scale is at least 2^-18 of what that product comes to
+ *     in any of the row's tokens, in steps of 2^-28 of that below.  lse is of
+ *     the probabilities in FP32.
+ * A NaN anywhere in a row's visible tokens, or a NaN or an infinity in its q,
+ * makes that row NaN; what lies beyond the visible tokens is never used.
  *   q          BF16 (MLAQP_OUT_BF16) or E4M3 (MLAQP_OUT_E4M3, value =
  *              code * *q_scale, q_scale one FP32 in device memory, NULL for
  *              BF16): element (m,h,j) at q[m*q_token_stride + h*576 + j];

@@ -22,8 +22,10 @@
 // 8-bit operands without loss of the inputs' precision:
 //   Q   BF16 rows are scaled to a maximum in [128,256) and split into two
 //       E4M3 terms hi + lo/16: a BF16 significand has 8 bits, two terms of 4
-//       hold it, elements below 2^-20 of the row's maximum lose their tail.
-//       E4M3 queries are used as they are.  The terms are extra N rows.
+//       hold it down to E4M3's smallest normal in hi, 2^-13 of the maximum or
+//       less; below, steps of lo's smallest subnormal remain, 2^-20 of the
+//       maximum (a third term would want 8 KB of shared memory that is not
+//       there).  E4M3 queries are used as they are.  The terms are extra N rows.
 //   P   FP16 (11 bits) as three E5M2 terms, each rounded to nearest, again
 //       extra N rows: together exactly that FP16 number down to 2^-18 of the
 //       maximum (of p_t * 2^s_t over the tokens), and absolute steps of 2^-28

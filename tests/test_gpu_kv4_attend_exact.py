@@ -5,11 +5,17 @@ keep FP16's 11 bits.
 Tolerances, from the number formats:
   every token once   with queries of zero all weights are 1/n and every code
                      and sum is exact in FP32, so x is off by its rounding to
-                     BF16 alone: 2^-9 |x|, doubled.  lse is ln n: 1e-5.
-  probabilities      2^-9 |x| for BF16, and 2^-11 sum_t p |K| for FP16
-                     probabilities; 2^-14 sum_t p |K| covers the scores (sums
-                     of four products, a factor of log2 e rounded to FP32) and
-                     exp.
+                     BF16 alone: half a step, 2^-8 |x|.  lse is ln n: 1e-5.
+  probabilities      2^-11 sum_t p |K| for FP16 probabilities; 2^-14 sum_t p |K|
+                     covers the scores (sums of four products, a factor of log2 e
+                     rounded to FP32) and exp.  |x| is a small part of that sum
+                     here, so 2^-9 |x| beside it is enough for BF16.
+  small query elements  each up to half of a step of 2^-20 of the row's largest
+                     off, so a score by dS = 2^-21 largest scale sum |K|, a
+                     probability by a factor of exp(+-2 dS), lse by dS.
+  small p beside large scales  2^-8 |x| for BF16, 2^-11 and 2^-14 as above, and
+                     half of a step of 2^-28 of the largest p 2^s for each
+                     token, times codes of up to 6.
 """
 
 import numpy as np
@@ -92,3 +98,65 @@ def test_probabilities_keep_eleven_bits(cuda_device, q_len, dtype):
             want, bound = balanced_bound(c.q[m], keys[:len(keys) - (q_len - 1 - i)])
             err = np.abs(x[m] - want)
             assert (err <= bound).all(), f"sequence {b} token {i}: off by {(err / bound).max()} of the bound"
+
+
+@pytest.mark.parametrize("rope_top", [0.0, 2.0 ** 42])
+def test_query_elements_far_below_the_largest_of_their_row(cuda_device, rope_top):
+    # the largest meets latents of zero, so the small ones make the score
+    def rows(rng, T):
+        r = np.zeros((T, 576))
+        r[:, :512] = rng.choice([-6, -4, -3, -2, -1.5, -1, -0.5, 0.5, 1, 1.5, 2, 3, 4, 6], (T, 512))
+        r[:, :32] = 0.0
+        return _bits(r)
+
+    def q(rng, M, H):
+        v = rng.choice([-1, 1], (M, H, 576)) * rng.uniform(1, 2, (M, H, 576)) * 2.0 ** -rng.integers(10, 25, (M, H, 576))
+        v[:, :, :32] = 0.0
+        v[:, :, 7] = 1.0
+        v[:, :, 512:] = rope_top
+        return v
+
+    scale = 32.0
+    c = Case([200, 33, 128], P=64, H=16, rows=rows, q=q, scale=scale, seed=12)
+    _ok(c.run())
+    x, lse = c.outputs()
+    for b in range(3):
+        keys = c.keys(b)
+        wx, wl = ko.attend(c.q[b], keys, scale)
+        p = np.exp(c.q[b] @ keys.T * scale - wl[:, None])
+        ds = 2.0 ** -21 * max(1.0, 2.0 ** -40 * rope_top) * scale * np.abs(keys[:, :512]).sum(1).max()
+        assert ds < 0.25 and np.ptp(c.q[b] @ keys.T * scale, axis=1).min() > 4 * ds  # the scores are told apart
+        bound = 2.0 ** -9 * np.abs(wx) + (2.0 ** -11 + 2.0 ** -14 + np.expm1(2 * ds)) * (p @ np.abs(keys[:, :512]))
+        assert (np.abs(x[b] - wx) <= bound).all(), b
+        assert (np.abs(lse[b] - wl) <= ds + 1e-5).all(), b
+
+
+def test_small_probabilities_beside_large_scales(cuda_device):
+    # two tokens: the second is the likelier one, the first's latents are up
+    # to 2^30 times as large; they share no latent
+    octaves = list(range(0, 31))
+
+    def rows(rng, T):
+        r = np.zeros((T, 576))
+        r[0::2, :256] = 6.0 * 2.0 ** np.array(octaves)[:, None]
+        r[1::2, 256:512] = rng.choice([-6, -4, -3, -2, 2, 3, 4, 6], (T // 2, 256))
+        r[1::2, 512] = 1.0
+        return _bits(r)
+
+    def q(rng, M, H):
+        v = np.zeros((M, H, 576))
+        v[:, :, 512] = rng.uniform(1, 6, (M, H))
+        return v
+
+    c = Case([2] * len(octaves), P=16, H=16, rows=rows, q=q, scale=1.0, seed=13)
+    _ok(c.run())
+    x, lse = c.outputs()
+    for b, k in enumerate(octaves):
+        keys = c.keys(b)
+        wx, wl = ko.attend(c.q[b], keys, 1.0)
+        p = np.exp(c.q[b] @ keys.T - wl[:, None])
+        largest = np.maximum(p[:, 0] * 2.0 ** k, p[:, 1])
+        bound = (2.0 ** -8 * np.abs(wx) + (2.0 ** -11 + 2.0 ** -14) * (p @ np.abs(keys[:, :512]))
+                 + 2.0 ** -29 * 6.0 * largest[:, None])
+        assert (np.abs(x[b] - wx) <= bound).all(), k
+        assert (np.abs(lse[b] - wl) <= 1e-5).all(), k
