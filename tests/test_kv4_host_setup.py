@@ -76,8 +76,9 @@ def stand_in_library(tmp_path_factory):
     (d / "stand_ins.cpp").write_text(STAND_INS)
     cuda = Path(build.nvcc_path()).resolve().parent.parent / "include"
     so = d / "libkv4_host.so"
-    subprocess.run([shutil.which("g++"), "-std=c++17", "-shared", "-fPIC", f"-I{build.INCLUDE}", f"-I{build.CSRC}", f"-I{cuda}",
-                    "-x", "c++", str(build.CSRC / "mlaqp_kv4_api.cu"), str(d / "stand_ins.cpp"), "-o", str(so)], check=True)
+    # -Bsymbolic: its own stand-ins, not what libraries loaded before it export
+    subprocess.run([shutil.which("g++"), "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", f"-I{build.INCLUDE}",
+                    f"-I{build.CSRC}", f"-I{cuda}", "-x", "c++", str(build.CSRC / "mlaqp_kv4_api.cu"), str(d / "stand_ins.cpp"), "-o", str(so)], check=True)
     return so
 
 
