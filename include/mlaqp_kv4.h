@@ -155,6 +155,26 @@ int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const f
 int64_t mlaqp_kv4_attend_workspace(int B, int q_len, int H, int device);
 
 /*
+ * Test hook for the attention kernel's bounded waits: as mlaqp_kv4_attend,
+ * with their limit set to wait_limit_ns (1..10^9) and, for held > 0, one of the
+ * hand-overs between the kernel's warps never taking place: 1 copies landed,
+ * 2 copy units free, 3 scales, 4 rope rows landed, 5 rope rows free, 6 codes
+ * converted, 7 their tiles free, 8 scores, 9 scores read, 10 probabilities,
+ * 11 output products, 12 queries, 13 output read (2, 5, 7, 9 and 13 matter to
+ * CTAs with more than one tile or row group).  The kernel records
+ * MLAQP_DEVSTATUS_WAIT_TIMEOUT, waits for its own copies and products and
+ * returns; x, lse and the workspace hold nothing of use.  Not for production.
+ */
+#define MLAQP_KV4_ATTEND_STAGES 13
+int mlaqp_debug_kv4_attend_bounded_wait(const void* q, int64_t q_token_stride, int q_dtype, const float* q_scale,
+                                        const void* cache, int64_t page_stride, int num_pages, int page_size,
+                                        const int32_t* block_table, int64_t block_table_stride, int num_seqs,
+                                        const int32_t* seq_lens, const int32_t* seqs, int B, int q_len, int H,
+                                        float softmax_scale, void* x, int64_t x_token_stride, float* lse,
+                                        void* workspace, int64_t workspace_bytes, unsigned int wait_limit_ns, int held,
+                                        mlaqp_stream_t stream);
+
+/*
  * Page operations.  They work on the table rows named by a list of n
  * sequences (device int32, distinct) and, where pages are copied, on all
  * `layers` layers of the cache: page p of layer l is at

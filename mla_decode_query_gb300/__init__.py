@@ -29,6 +29,7 @@ from .mlaqp import (  # noqa: F401
     header_functions,
     load_library,
     mlaqp_can_implement,
+    mlaqp_debug_kv4_attend_bounded_wait,
     mlaqp_debug_launch_null,
     mlaqp_debug_plan,
     mlaqp_debug_run_arm,

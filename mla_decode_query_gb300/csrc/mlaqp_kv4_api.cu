@@ -224,11 +224,18 @@ int check_attend_sizes(int B, int q_len, int H) {
 
 }  // namespace
 
-int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const float* q_scale, const void* cache,
-                     int64_t page_stride, int num_pages, int page_size, const int32_t* block_table,
-                     int64_t block_table_stride, int num_seqs, const int32_t* seq_lens, const int32_t* seqs, int B,
-                     int q_len, int H, float softmax_scale, void* x, int64_t x_token_stride, float* lse,
-                     void* workspace, int64_t workspace_bytes, mlaqp_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+constexpr uint32_t kWaitNs = 1000000000u;
+static_assert(MLAQP_KV4_ATTEND_STAGES == mlaqp::kAttStages, "the public number of hand-overs");
+
+int attend_impl(const void* q, int64_t q_token_stride, int q_dtype, const float* q_scale, const void* cache,
+                int64_t page_stride, int num_pages, int page_size, const int32_t* block_table,
+                int64_t block_table_stride, int num_seqs, const int32_t* seq_lens, const int32_t* seqs, int B, int q_len,
+                int H, float softmax_scale, void* x, int64_t x_token_stride, float* lse, void* workspace,
+                int64_t workspace_bytes, uint32_t wait_ns, int held, mlaqp_stream_t stream) {
   mlaqp::Kv4AttendParams p = {};
   if (q_dtype != MLAQP_OUT_BF16 && q_dtype != MLAQP_OUT_E4M3) return bad_arg("unknown q_dtype");
   const bool e4m3 = q_dtype == MLAQP_OUT_E4M3;
@@ -291,7 +298,37 @@ int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const f
   p.x_ts = x_token_stride;
   p.lse = lse;
   p.ws = static_cast<uint8_t*>(workspace);
+  p.wait_ns = wait_ns;
+  p.held = held;
   return launched(mlaqp::kv4_attend(p, e4m3, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int mlaqp_kv4_attend(const void* q, int64_t q_token_stride, int q_dtype, const float* q_scale, const void* cache,
+                     int64_t page_stride, int num_pages, int page_size, const int32_t* block_table,
+                     int64_t block_table_stride, int num_seqs, const int32_t* seq_lens, const int32_t* seqs, int B,
+                     int q_len, int H, float softmax_scale, void* x, int64_t x_token_stride, float* lse,
+                     void* workspace, int64_t workspace_bytes, mlaqp_stream_t stream) {
+  return attend_impl(q, q_token_stride, q_dtype, q_scale, cache, page_stride, num_pages, page_size, block_table,
+                     block_table_stride, num_seqs, seq_lens, seqs, B, q_len, H, softmax_scale, x, x_token_stride, lse,
+                     workspace, workspace_bytes, kWaitNs, 0, stream);
+}
+
+int mlaqp_debug_kv4_attend_bounded_wait(const void* q, int64_t q_token_stride, int q_dtype, const float* q_scale,
+                                        const void* cache, int64_t page_stride, int num_pages, int page_size,
+                                        const int32_t* block_table, int64_t block_table_stride, int num_seqs,
+                                        const int32_t* seq_lens, const int32_t* seqs, int B, int q_len, int H,
+                                        float softmax_scale, void* x, int64_t x_token_stride, float* lse,
+                                        void* workspace, int64_t workspace_bytes, unsigned int wait_limit_ns, int held,
+                                        mlaqp_stream_t stream) {
+  if (wait_limit_ns == 0 || wait_limit_ns > kWaitNs) return bad_arg("wait_limit_ns must be in 1..10^9");
+  if (held < 0 || held > MLAQP_KV4_ATTEND_STAGES) return bad_arg("held must be in 0..MLAQP_KV4_ATTEND_STAGES");
+  return attend_impl(q, q_token_stride, q_dtype, q_scale, cache, page_stride, num_pages, page_size, block_table,
+                     block_table_stride, num_seqs, seq_lens, seqs, B, q_len, H, softmax_scale, x, x_token_stride, lse,
+                     workspace, workspace_bytes, wait_limit_ns, held, stream);
 }
 
 int64_t mlaqp_kv4_attend_workspace(int B, int q_len, int H, int device) {

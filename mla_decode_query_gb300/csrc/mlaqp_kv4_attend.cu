@@ -10,27 +10,43 @@ namespace mlaqp {
 
 namespace {
 
-constexpr uint32_t kAttWaitNs = 1000000000u;
-
 __device__ __forceinline__ uint32_t att_clock() {
   uint32_t t;
   asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
   return t;
 }
 
-// Bounded wait of one thread; gives up early once another one has.  (Kept
-// short: it is inlined some thirty times, and a larger kernel than the
-// instruction caches hold runs at half the speed.  So the host's word is set
-// once, at the kernel's end.)
+// What a wait may take; 0 once one has run out, and all others give up too.
+__device__ __forceinline__ volatile uint32_t& att_limit(AttSchedule& s) {
+  return *reinterpret_cast<volatile uint32_t*>(&s.wait_ns);
+}
+
+// Bounded wait of one thread.  (Kept short: it is inlined some thirty times,
+// and a larger kernel than the instruction caches hold runs at half the speed.
+// So the host's word is set once, at the kernel's end.)
 __device__ __forceinline__ bool att_wait_one(uint32_t bar, uint32_t parity, AttSchedule& s) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint32_t t0 = att_clock();
 #pragma unroll 1
   do {
     if (mbar_try_wait(bar, parity)) return true;
-  } while (att_clock() - t0 < kAttWaitNs && !*reinterpret_cast<volatile int*>(&s.fail));
-  *reinterpret_cast<volatile int*>(&s.fail) = 1;
+  } while (att_clock() - t0 < att_limit(s));
+  att_limit(s) = 0;
   return false;
+}
+
+// The wait, at its role's end, for what a warp has itself in flight: copies
+// and products have to land before the CTA gives its shared and tensor memory
+// back, whichever warp gave up before (this one may have had nothing to wait
+// for).  So it does not end with the others' waits, only with its own limit.
+__device__ __forceinline__ void att_settle(uint32_t bar, uint32_t parity, uint32_t t0, uint32_t limit, AttSchedule& s) {
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (att_clock() - t0 >= limit) {
+      att_limit(s) = 0;
+      return;
+    }
+  }
 }
 
 // The same for a whole warp, with one answer for all its lanes.
@@ -156,9 +172,9 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     for (int i = 1;; ++i) {
       if (kr <= tile && __all_sync(0xffffffffu, rope_free())) load_rope();
       if (stage_free()) return true;
-      if ((i & 63) == 0) {
-        if (att_clock() - t_in > kAttWaitNs) *reinterpret_cast<volatile int*>(&s.fail) = 1;
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s.fail))) return false;
+      if ((i & 63) == 0 && __any_sync(0xffffffffu, att_clock() - t_in >= att_limit(s))) {
+        att_limit(s) = 0;
+        return false;
       }
     }
   };
@@ -227,20 +243,14 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
       entry += entries;
     }
   }
-  if (ok) ok = finish_rope(k - 1);
-  if (!ok) {  // copies in flight land before the CTA ends
-    auto drain = [&](uint32_t bar, uint32_t parity) {
-      const uint32_t at = att_clock();
+  if (ok) finish_rope(k - 1);
+  const uint32_t at = att_clock();
 #pragma unroll 1
-      while (!mbar_try_wait(bar, parity) && att_clock() - at < kAttWaitNs) {
-      }
-    };
+  for (int i = max(0, u - L::Units); i < u; ++i)
+    att_settle(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1, at, p.wait_ns, s);
 #pragma unroll 1
-    for (int i = max(0, u - L::Units); i < u; ++i) drain(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1);
-#pragma unroll 1
-    for (int i = max(0, kr - L::RopeBufs); i < kr; ++i)
-      drain(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1);
-  }
+  for (int i = max(0, kr - L::RopeBufs); i < kr; ++i)
+    att_settle(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1, at, p.wait_ns, s);
 }
 
 // --------------------------------------------------------------------------
@@ -380,18 +390,9 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
 // thread's MMAs came 175 cycles apart.
 // --------------------------------------------------------------------------
 
-// What was issued completes before the CTA ends (bar: the warp's own).
-__device__ __forceinline__ void att_drain(uint32_t bar, bool leader) {
-  if (leader) umma_commit(bar);
-  const uint32_t at = att_clock();
-#pragma unroll 1
-  while (!mbar_try_wait(bar, 0) && att_clock() - at < kAttWaitNs) {
-  }
-}
-
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
-                                               uint32_t tmem, int t0, int t1) {
+__device__ __forceinline__ void att_mma_scores(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s,
+                                               uint32_t smem, uint32_t bars, uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
   constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
@@ -438,12 +439,13 @@ __device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& 
       __syncwarp();
     }
   }
-  if (!ok) att_drain(bars + 8 * L::Drain, leader);
+  if (leader) umma_commit(bars + 8 * L::Drain);
+  att_settle(bars + 8 * L::Drain, 0, att_clock(), p.wait_ns, s);
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
-                                               uint32_t tmem, int t0, int t1) {
+__device__ __forceinline__ void att_mma_output(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s,
+                                               uint32_t smem, uint32_t bars, uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
   const bool leader = elect_one();
@@ -478,7 +480,8 @@ __device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& 
       __syncwarp();
     }
   }
-  if (!ok) att_drain(bars + 8 * (L::Drain + 1), leader);
+  if (leader) umma_commit(bars + 8 * (L::Drain + 1));
+  att_settle(bars + 8 * (L::Drain + 1), 0, att_clock(), p.wait_ns, s);
 }
 
 // --------------------------------------------------------------------------
@@ -780,8 +783,8 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     soft_barrier(group);  // the maxima of the last tile have been read
     if (lane < HR) s.wmax[warp][lane] = mine;
     soft_barrier(group);
-    const bool done = att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
-    if (!done || *reinterpret_cast<volatile int*>(&s.fail)) {
+    // (one answer for all lanes: another warp may give up at this moment)
+    if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s) || __any_sync(0xffffffffu, att_limit(s) == 0)) {
       t = next_t;
       it = next;
       continue;
@@ -899,6 +902,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     if (tid >= L::RawEmpty && tid < L::ScaleFull) count = L::UnitWarps;
     if (tid >= L::K8Full && tid < L::K8Empty) count = kAttDequantWarps / 4;
     if ((tid >= L::SEmpty && tid <= L::PFull) || tid == L::QFull || tid == L::OEmpty) count = 32 * kAttSoftWarps;
+    if (tid - p.held_first < p.held_count) ++count;  // (none outside the test of the waits)
     mbar_init(bars + 8 * tid, count);
     fence_barrier_init();
   }
@@ -907,7 +911,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     const float f = __uint_as_float(static_cast<uint32_t>(133 - tid) << 23);
     s.lut[tid][0] = pack_e4m3x2(0.5f * f, 0.f) | (pack_e4m3x2(1.5f * f, f) << 16);
     s.lut[tid][1] = pack_e4m3x2(3.f * f, 2.f * f) | (pack_e4m3x2(6.f * f, 4.f * f) << 16);
-    if (tid == 0) s.fail = 0;
+    if (tid == 0) s.wait_ns = p.wait_ns;
   }
   pdl_wait();
   if (warp == kAttScoreWarp) tmem_alloc(smem_u32(&s.tmem), 512);
@@ -953,16 +957,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, t0, t1);
     } else if (warp == kAttScoreWarp) {
-      att_mma_scores<R, E4>(s, base, bars, tmem, t0, t1);
+      att_mma_scores<R, E4>(p, s, base, bars, tmem, t0, t1);
     } else if (warp == kAttOutputWarp) {
-      att_mma_output<R, E4>(s, base, bars, tmem, t0, t1);
+      att_mma_output<R, E4>(p, s, base, bars, tmem, t0, t1);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   __syncwarp();
-  if (tid == 0 && s.fail) atomicOr(&g_device_status, kDevStatusWaitTimeout);
+  if (tid == 0 && s.wait_ns == 0) atomicOr(&g_device_status, kDevStatusWaitTimeout);
   if (warp == kAttScoreWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -1120,14 +1124,17 @@ struct AttKernels {
   const void* main;
   const void* join;
   int smem;
-  bool splits_regs;  // its warps share the launch's registers out anew
+  bool splits_regs;           // its warps share the launch's registers out anew
+  int stage[kAttStages + 1];  // first barrier of each hand-over, and of what follows the last
 };
 
 template <int R, bool E4>
 AttKernels att_kernels() {
+  using L = AttPlan<R, E4>;
   return AttKernels{reinterpret_cast<const void*>(&mlaqp_kv4_attend_kernel<R, E4>),
-                    reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), AttPlan<R, E4>::Bytes,
-                    AttPlan<R, E4>::SoftRegs != kAttRegs};
+                    reinterpret_cast<const void*>(&mlaqp_kv4_join_kernel<R>), L::Bytes, L::SoftRegs != kAttRegs,
+                    {L::RawFull, L::RawEmpty, L::ScaleFull, L::RopeFull, L::RopeEmpty, L::K8Full, L::K8Empty, L::SFull,
+                     L::SEmpty, L::PFull, L::PvDone, L::QFull, L::OEmpty, L::Drain}};
 }
 
 // 16 rows where all (query token, head) pairs of a sequence fit, else groups
@@ -1140,10 +1147,15 @@ AttKernels att_pick(int q_len, int H, bool e4m3) {
 
 }  // namespace
 
-cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream) {
+cudaError_t kv4_attend(const Kv4AttendParams& params, bool q_e4m3, int sm_count, cudaStream_t stream) {
+  Kv4AttendParams p = params;
   const AttKernels k = att_pick(p.q_len, p.H, q_e4m3);
   const int ctas = sm_count < kAttMaxCtas ? sm_count : kAttMaxCtas;
-  void* args[1] = {const_cast<Kv4AttendParams*>(&p)};
+  if (p.held > 0) {
+    p.held_first = static_cast<unsigned>(k.stage[p.held - 1]);
+    p.held_count = static_cast<unsigned>(k.stage[p.held] - k.stage[p.held - 1]);
+  }
+  void* args[1] = {&p};
   const cudaError_t e = kv4_launch(k.main, static_cast<unsigned>(ctas), kAttThreads, k.smem, stream, args);
   if (e != cudaSuccess) return e;
   return kv4_launch(k.join, static_cast<unsigned>(kJoinCtasPerSm * sm_count), kJoinThreads, sizeof(JoinShared), stream,

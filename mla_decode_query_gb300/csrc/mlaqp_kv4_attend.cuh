@@ -105,13 +105,13 @@ constexpr int kRopeTile = kAttTile * kKv4RopeBytes;
 constexpr int kK8Block = kAttTile * 128;  // 128 latents of a tile
 constexpr int kK8Tile = 4 * kK8Block;
 
-// What follows from the lengths, and the mark that a wait ran out.
+// What follows from the lengths, and the limit of the waits.
 struct AttSchedule {
   int prefix[kAttMaxSeqs + 1];  // length of the line before each row group
   int len[kAttMaxSeqs];
   int scan[8];
   int cut, begin, end, group;  // this CTA's stretch, its first tile, that tile's row group
-  int fail;
+  uint32_t wait_ns;  // 0: a wait ran out
 };
 
 template <int R, int Ring>  // Ring: tokens of all copy units in flight
@@ -180,6 +180,7 @@ struct AttPlan {
                        SFull = K8Empty + 8, SEmpty = SFull + SBufs, PFull = SEmpty + SBufs, PvDone = PFull + 1,
                        QFull = PvDone + 1, OEmpty = QFull + 1, Drain = OEmpty + 1, BarCount = Drain + 2;
   static_assert(BarCount <= 42, "barriers");
+  static_assert(Drain - OEmpty == 1 && QFull - PvDone == 1, "kAttStages hand-overs, in this order");
 };
 
 // Instruction descriptor: FP32 accumulator, operand formats and majors.

@@ -92,7 +92,15 @@ struct Kv4AttendParams {
   int64_t x_ts;
   float* lse;
   uint8_t* ws;
+  uint32_t wait_ns;        // limit of a wait in the attention kernel
+  int held;                // test of the waits: the hand-over that never happens, 0: none
+  unsigned held_first, held_count;  // its barriers, which expect an arrival too many (set by kv4_attend)
 };
+// The hand-overs between the attention kernel's warps, in the order of its
+// barriers: copies landed, copy units free, scales, rope rows landed, rope rows
+// free, codes converted, their tiles free, scores, scores read, probabilities,
+// output products, queries, output read.
+constexpr int kAttStages = 13;
 cudaError_t kv4_attend(const Kv4AttendParams& p, bool q_e4m3, int sm_count, cudaStream_t stream);
 cudaError_t kv4_attend_setup(int rows);  // 16 or 32: the kernels for that many rows
 int kv4_attend_rows(int q_len, int H);   // of a row group

@@ -55,6 +55,10 @@ _c_int64 = ctypes.c_int64
 _KV4_TABLES = [_c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int, _c_int]
 # cache, page_stride, layer_stride, layers
 _KV4_POOL = [_c_void_p, _c_int64, _c_int64, _c_int]
+# q, its stride, q_dtype, q_scale; one layer's cache; tables; sizes; x, lse, workspace
+_KV4_ATTEND = [_c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int64, _c_int,
+               _c_void_p, _c_void_p, _c_int, _c_int, _c_int, ctypes.c_float, _c_void_p, _c_int64, _c_void_p, _c_void_p,
+               _c_int64]
 _SIGNATURES = {
     "mlaqp_can_implement": (_c_int, [_c_int] * 8),
     "mlaqp_prewarm": (_c_int, [_c_int] * 5),
@@ -91,9 +95,8 @@ _SIGNATURES = {
                                   _c_void_p, _c_int, _c_void_p]),
     "mlaqp_kv4_gather": (_c_int, [_c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int, _c_void_p, _c_int64,
                                   _c_void_p]),
-    "mlaqp_kv4_attend": (_c_int, [_c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int64, _c_int, _c_int,
-                                  _c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int,
-                                  ctypes.c_float, _c_void_p, _c_int64, _c_void_p, _c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_attend": (_c_int, _KV4_ATTEND + [_c_void_p]),
+    "mlaqp_debug_kv4_attend_bounded_wait": (_c_int, _KV4_ATTEND + [ctypes.c_uint, _c_int, _c_void_p]),
     "mlaqp_kv4_attend_workspace": (_c_int64, [_c_int] * 4),
     "mlaqp_kv4_extend": (_c_int, _KV4_TABLES + [_c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_void_p]),
     "mlaqp_kv4_fork": (_c_int, _KV4_TABLES + [_c_void_p, _c_void_p, _c_int] + _KV4_POOL
@@ -348,6 +351,17 @@ def mlaqp_kv4_attend(q, q_token_stride, q_dtype, q_scale, cache, page_stride, nu
         int(num_pages), int(page_size), _ptr(block_table), int(block_table_stride), int(num_seqs), _ptr(seq_lens),
         _ptr(seqs), int(B), int(q_len), int(H), float(softmax_scale), _ptr(x), int(x_token_stride), _ptr(lse),
         _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def mlaqp_debug_kv4_attend_bounded_wait(q, q_token_stride, q_dtype, q_scale, cache, page_stride, num_pages, page_size,
+                                        block_table, block_table_stride, num_seqs, seq_lens, seqs, B, q_len, H,
+                                        softmax_scale, x, x_token_stride, lse, workspace, workspace_bytes,
+                                        wait_limit_ns, held, stream=None) -> int:
+    return load_library().mlaqp_debug_kv4_attend_bounded_wait(
+        _ptr(q), int(q_token_stride), _fmt(q_dtype, OUT_DTYPES), _ptr(q_scale), _ptr(cache), int(page_stride),
+        int(num_pages), int(page_size), _ptr(block_table), int(block_table_stride), int(num_seqs), _ptr(seq_lens),
+        _ptr(seqs), int(B), int(q_len), int(H), float(softmax_scale), _ptr(x), int(x_token_stride), _ptr(lse),
+        _ptr(workspace), int(workspace_bytes), int(wait_limit_ns), int(held), _stream(stream))
 
 
 def mlaqp_kv4_attend_workspace(B, q_len, H, device=-1) -> int:

@@ -223,3 +223,13 @@ def test_interleaved_layers_are_accepted(built_library):
         pytest.skip("a GPU is present; covered by the GPU tests")
     a = dict(POOL, page_stride=3 * 6400, layer_stride=6400)
     assert mq.mlaqp_kv4_copy_pages(**a, num_pages=64, page_size=16, src=A, dst=2 * A, n=2, stream=0) == mq.MLAQP_ERR_CUDA
+
+
+@pytest.mark.parametrize("limit,held", [(0, 0), (10 ** 9 + 1, 0), (1000, -1), (1000, 14)])
+def test_bounded_wait_hook_refusals(built_library, limit, held):
+    a = dict(q=A, q_token_stride=576 * 16, q_dtype="bf16", q_scale=None, cache=8 * A, page_stride=25600, num_pages=16,
+             page_size=64, block_table=4 * A, block_table_stride=4, num_seqs=3, seq_lens=5 * A, seqs=None, B=3, q_len=1,
+             H=16, softmax_scale=0.07, x=2 * A, x_token_stride=512 * 16, lse=3 * A, workspace=16 * A,
+             workspace_bytes=1 << 26, stream=0)
+    assert mq.mlaqp_debug_kv4_attend_bounded_wait(**a, wait_limit_ns=limit, held=held) == INVALID
+    assert mq.mlaqp_last_error() != ""
