@@ -605,12 +605,13 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
   const uint32_t here = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + row0;  // first row's columns
   float* mref = s.mref[warp];
   float* alpha = s.alpha[warp];
-  // A wait that runs out (then all later ones do at once) does not end the
-  // warp here: it goes on with what is there, so that no other one is left
-  // alone at a barrier, and writes nothing.
+  // A wait that runs out ends the warp's work, but not its part in the
+  // barriers of its group (`gave_up`).  Nothing may go on behind such a wait:
+  // tensor memory may still be a product's.
   // Row group -1 has no tiles: it only prepares the first one's queries.
   AttItem it = {s.group, 0, 0, t0};
-  int k = 0;
+  int k = 0, n = 0;
+  int due = 0;  // barriers ahead of a warp that gave up: 0 tile n's and on, 1 the next tile's and on, 2 the next row group's
   for (int t = t0, item = -1; t < t1; ++item) {
     const int turn = item & 1;
     // every warp has left the row group before (what follows reuses its
@@ -628,9 +629,9 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     }
     if (lane < HR) mref[lane] = kAttUnseen;
     __syncwarp();
-    for (int n = item < 0 ? -1 : 0; n < it.count; ++n) {
+    for (n = item < 0 ? -1 : 0; n < it.count; ++n) {
       const int sb = k % L::SBufs;
-      if (n >= 0) att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s);
+      if (n >= 0 && !att_wait(bars + 8 * (L::SFull + sb), (k / L::SBufs) & 1, s)) goto gave_up;
       // the scores of the row group's last tile are in: its queries are done with
       if (n == it.count - 1 && next_t < t1) att_query<R, E4>(p, s, smem, bars, next.v, turn ^ 1);
       if (n < 0) continue;
@@ -640,7 +641,7 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
 #pragma unroll
       for (int part = 0; part <= L::QTerms; ++part)
         tmem_ld_begin<HR>(here + sb * L::SCols + part * R, &v[HR * part]);
-      att_wait(bars + 8 * (L::K8Full + 4 * (k & 1)), (k / 2) & 1, s);  // the tile's scales are in, too
+      if (!att_wait(bars + 8 * (L::K8Full + 4 * (k & 1)), (k / 2) & 1, s)) goto gave_up;  // the tile's scales are in, too
       const uint32_t sm = s.smax[k % kAttScaleTiles][tok];
       const float ts = sm == kKv4ScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float((sm - 6u) << 23);
       const float its = __uint_as_float((260u - sm) << 23);
@@ -708,7 +709,9 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
           x[r + 3] = y[r + 3] - m.w;
         }
         if (n > 0) {
-          att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);
+          due = 1;
+          if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) goto gave_up;
+          due = 0;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 12; ++c) {  // four blocks of latents, three terms
@@ -723,7 +726,9 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
           tmem_wait_st();
         }
       }
-      if (k > 0) att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s);  // P is free
+      due = 1;
+      if (k > 0 && !att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s)) goto gave_up;  // P is free
+      due = 0;
       uint32_t terms[3][HR / 4];
 #pragma unroll
       for (int r = 0; r < HR; r += 4) {
@@ -784,11 +789,9 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     if (lane < HR) s.wmax[warp][lane] = mine;
     soft_barrier(group);
     // (one answer for all lanes: another warp may give up at this moment)
-    if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s) || __any_sync(0xffffffffu, att_limit(s) == 0)) {
-      t = next_t;
-      it = next;
-      continue;
-    }
+    due = 2;
+    if (!att_wait(bars + 8 * L::PvDone, (k - 1) & 1, s) || __any_sync(0xffffffffu, att_limit(s) == 0)) goto gave_up;
+    due = 0;
     tc_fence_after();
     float* part = nullptr;
     if (!complete) {
@@ -846,6 +849,25 @@ __device__ __forceinline__ void att_softmax(const Kv4AttendParams& p, typename A
     mbar_arrive(bars + 8 * L::OEmpty);
     t = next_t;
     it = next;
+  }
+  return;
+
+gave_up:
+  tmem_wait_ld();  // the scores' loads
+  if (due == 0 && soft_barrier_any(group, false)) soft_barrier(group);
+  for (;;) {
+    if (due < 2) {
+#pragma unroll 1
+      for (++n; n < it.count; ++n)
+        if (soft_barrier_any(group, false)) soft_barrier(group);
+      soft_barrier(group);
+      soft_barrier(group);
+    }
+    if (it.next >= t1) return;
+    it = att_item(s.prefix, it.v, it.next, t1);
+    n = -1;
+    due = 1;
+    soft_barrier(group);
   }
 }
 

@@ -249,6 +249,7 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
         : "memory");
 }
 #undef MLAQP_R8
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A warpgroup's registers a thread from here on (kAttRegs before).
@@ -295,7 +296,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 
 // Barrier of a group of four softmax warps (group 0 or 1); the second form
 // tells whether any thread says yes.  Every one of these warps passes every
-// barrier, also after a wait has run out.
+// barrier, also when it has given up.
 __device__ __forceinline__ void soft_barrier(int group) {
   asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
 }

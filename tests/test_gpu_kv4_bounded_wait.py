@@ -62,3 +62,16 @@ def test_one_tile(cuda_device, q_len, H, dtype):
         _ok(_held(c, held, 10 ** 8))
         c.check()
         assert _device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len,H,B", [(1, 16, 200), (2, 16, 120)])
+def test_several_tiles_and_sequences_a_cta(cuda_device, q_len, H, B, dtype):
+    rng = np.random.default_rng(B)
+    c = Case([int(n) for n in rng.integers(300, 700, B)], P=32, q_len=q_len, H=H, dtype=dtype, seed=B)
+    _check_every_stage(c, range(1, STAGES + 1))
+    x, lse = c.outputs()
+    for b in (0, 57, B - 1):
+        keys = c.keys(b)
+        m = (b + 1) * q_len - 1
+        c.compare(x[m], lse[m], c.q[m], keys, f"sequence {b}")
