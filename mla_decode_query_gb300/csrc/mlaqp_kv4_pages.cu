@@ -9,10 +9,11 @@
 // serial walk.  Page contents are moved by a second kernel of many CTAs that
 // reads the jobs the first one left in the workspace; it is bound by memory:
 // a compaction that moves 214 MB reads and writes them in 63 us, 6.8 TB/s.
-// The one-CTA kernels are chains of loads and barriers, 5 to 10 us up to 16384
-// pages (release: a CTA a sequence, 5 us); beyond, the counts are what one SM
-// takes in: extending by a page takes 17 us in a pool of 2^17, 85 in one of
-// 2^20 (78 with 16-byte loads of the counts, not worth a second path).
+// The one-CTA kernels are chains of loads and barriers, 7 to 12 us cold up to
+// 16384 pages (release: a CTA a sequence, 5 to 6 us); beyond, the counts are
+// what one SM takes in: extending by a page takes 17 us in a pool of 2^17, 83
+// in one of 2^20 (some 7 less with 16-byte loads of the counts, not worth a
+// second path).
 
 #include "mlaqp_dispatch.h"
 #include "mlaqp_kv4.cuh"
