@@ -35,17 +35,12 @@ __device__ __forceinline__ bool att_wait_one(uint32_t bar, uint32_t parity, AttS
   return false;
 }
 
-// The wait, at its role's end, for what a warp has itself in flight: copies
-// and products have to land before the CTA gives its shared and tensor memory
-// back, whichever warp gave up before (this one may have had nothing to wait
-// for).  So it does not end with the others' waits, only with its own limit.
-__device__ __forceinline__ void att_settle(uint32_t bar, uint32_t parity, uint32_t t0, uint32_t limit, AttSchedule& s) {
+// The wait for what is in flight once a wait has run out: does not end with the
+// others, only with its own limit.
+__device__ __forceinline__ void att_settle(uint32_t bar, uint32_t parity, uint32_t t0, uint32_t limit) {
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if (att_clock() - t0 >= limit) {
-      att_limit(s) = 0;
-      return;
-    }
+    if (att_clock() - t0 >= limit) return;
   }
 }
 
@@ -244,13 +239,10 @@ __device__ __forceinline__ void att_load(const Kv4AttendParams& p, typename AttP
     }
   }
   if (ok) finish_rope(k - 1);
-  const uint32_t at = att_clock();
-#pragma unroll 1
-  for (int i = max(0, u - L::Units); i < u; ++i)
-    att_settle(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1, at, p.wait_ns, s);
-#pragma unroll 1
-  for (int i = max(0, kr - L::RopeBufs); i < kr; ++i)
-    att_settle(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1, at, p.wait_ns, s);
+  if (lane == 0) {
+    s.units = u;
+    s.ropes = kr;
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -391,8 +383,8 @@ __device__ __forceinline__ void att_dequant(typename AttPlan<R, E4>::Shared& s, 
 // --------------------------------------------------------------------------
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_scores(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s,
-                                               uint32_t smem, uint32_t bars, uint32_t tmem, int t0, int t1) {
+__device__ __forceinline__ void att_mma_scores(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
+                                               uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_s = att_idesc(kAttTile, L::NQ, kFmtE4M3, kFmtE4M3, false, false);
   constexpr uint32_t id_r = att_idesc(kAttTile, R, kFmtBf16, kFmtBf16, false, false);
@@ -439,13 +431,11 @@ __device__ __forceinline__ void att_mma_scores(const Kv4AttendParams& p, typenam
       __syncwarp();
     }
   }
-  if (leader) umma_commit(bars + 8 * L::Drain);
-  att_settle(bars + 8 * L::Drain, 0, att_clock(), p.wait_ns, s);
 }
 
 template <int R, bool E4>
-__device__ __forceinline__ void att_mma_output(const Kv4AttendParams& p, typename AttPlan<R, E4>::Shared& s,
-                                               uint32_t smem, uint32_t bars, uint32_t tmem, int t0, int t1) {
+__device__ __forceinline__ void att_mma_output(typename AttPlan<R, E4>::Shared& s, uint32_t smem, uint32_t bars,
+                                               uint32_t tmem, int t0, int t1) {
   using L = AttPlan<R, E4>;
   constexpr uint32_t id_o = att_idesc(kAttTile, L::NP, kFmtE4M3, kFmtE5M2, true, true);
   const bool leader = elect_one();
@@ -480,8 +470,32 @@ __device__ __forceinline__ void att_mma_output(const Kv4AttendParams& p, typenam
       __syncwarp();
     }
   }
-  if (leader) umma_commit(bars + 8 * (L::Drain + 1));
-  att_settle(bars + 8 * (L::Drain + 1), 0, att_clock(), p.wait_ns, s);
+}
+
+// What copies and products a CTA in which a wait has run out has in flight
+// lands before it gives its shared and tensor memory back, whichever warp gave
+// up: the ones that copy and issue may have had nothing to wait for.  (Where
+// none ran out the waits have seen all of it land: O is read behind the last
+// product.  Done by the warps at the end of their roles in any case, this cost
+// 32 sequences of up to 8191 tokens 0.5 us.)
+template <int R, bool E4>
+__device__ __forceinline__ void att_land(typename AttPlan<R, E4>::Shared& s, uint32_t bars, uint32_t limit) {
+  using L = AttPlan<R, E4>;
+  const int warp = threadIdx.x >> 5;
+  const uint32_t at = att_clock();
+  if (warp == kAttLoadWarp) {
+    const int u = s.units, kr = s.ropes;
+#pragma unroll 1
+    for (int i = max(0, u - L::Units); i < u; ++i)
+      att_settle(bars + 8 * (L::RawFull + i % L::Units), (i / L::Units) & 1, at, limit);
+#pragma unroll 1
+    for (int i = max(0, kr - L::RopeBufs); i < kr; ++i)
+      att_settle(bars + 8 * (L::RopeFull + i % L::RopeBufs), (i / L::RopeBufs) & 1, at, limit);
+  } else if (warp == kAttScoreWarp || warp == kAttOutputWarp) {
+    const uint32_t bar = bars + 8 * (L::Drain + (warp == kAttOutputWarp ? 1 : 0));
+    if (elect_one()) umma_commit(bar);  // the lane that issued: the same at every call
+    att_settle(bar, 0, at, limit);
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -933,7 +947,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     const float f = __uint_as_float(static_cast<uint32_t>(133 - tid) << 23);
     s.lut[tid][0] = pack_e4m3x2(0.5f * f, 0.f) | (pack_e4m3x2(1.5f * f, f) << 16);
     s.lut[tid][1] = pack_e4m3x2(3.f * f, 2.f * f) | (pack_e4m3x2(6.f * f, 4.f * f) << 16);
-    if (tid == 0) s.wait_ns = p.wait_ns;
+    if (tid == 0) {
+      s.wait_ns = p.wait_ns;
+      s.units = s.ropes = 0;
+    }
   }
   pdl_wait();
   if (warp == kAttScoreWarp) tmem_alloc(smem_u32(&s.tmem), 512);
@@ -979,13 +996,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
     } else if (warp == kAttLoadWarp) {
       att_load<R, E4>(p, s, base, bars, t0, t1);
     } else if (warp == kAttScoreWarp) {
-      att_mma_scores<R, E4>(p, s, base, bars, tmem, t0, t1);
+      att_mma_scores<R, E4>(s, base, bars, tmem, t0, t1);
     } else if (warp == kAttOutputWarp) {
-      att_mma_output<R, E4>(p, s, base, bars, tmem, t0, t1);
+      att_mma_output<R, E4>(s, base, bars, tmem, t0, t1);
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (att_limit(s) == 0) {  // the same for all: nothing sets it behind the barrier
+    att_land<R, E4>(s, bars, p.wait_ns);
+    tc_fence_before();
+    __syncthreads();
+  }
   tc_fence_after();
   __syncwarp();
   if (tid == 0 && s.wait_ns == 0) atomicOr(&g_device_status, kDevStatusWaitTimeout);

@@ -112,6 +112,7 @@ struct AttSchedule {
   int scan[8];
   int cut, begin, end, group;  // this CTA's stretch, its first tile, that tile's row group
   uint32_t wait_ns;  // 0: a wait ran out
+  int units, ropes;  // copy units and rope tiles asked for, when the copying warp has ended
 };
 
 template <int R, int Ring>  // Ring: tokens of all copy units in flight
