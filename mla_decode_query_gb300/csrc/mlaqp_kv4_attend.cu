@@ -1020,10 +1020,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 // a row, or 128 of its 512 latents where there are few rows; the CTA's eight
 // warps take the pieces in turn.  Bound by latency: what the attention kernel
 // noted of the row groups, then M, l and the first pieces' sums at once.  Two
-// CTAs per SM: 32 sequences of up to 8191 tokens take 27.9 us (both kernels),
-// with one 29.7, with three 30.3, with four 33.5; 16 of up to 4100 tokens, 4
-// query tokens, 27.3, 30.3, 30.8 and 34.2; 64 of up to 32768 157, 160.5, 160
-// and 163.
+// CTAs per SM: 32 sequences of up to 8191 tokens take 27.3 us (both kernels),
+// with one 29.0, with three 29.8, with four 32.7; 16 of up to 4100 tokens, 4
+// query tokens, 27.1, 29.9, 30.7 and 33.8; 64 of up to 32768 152, 156, 155
+// and 159.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtasPerSm = 2;

@@ -55,14 +55,14 @@
 // grown by more than 2^3.
 //
 // What bounds it (GB300, 152 SMs, H = 16).  64 sequences of 16000 to 32768
-// tokens, E4M3 queries: 157 us, 4.07 TB/s of cache and rows, 60% of the copy
-// rate of 6.79 TB/s.  A tile takes an SM 3100 to 3400 cycles; its bytes alone
+// tokens, E4M3 queries: 152 us, 4.20 TB/s of cache and rows, 62% of the copy
+// rate of 6.79 TB/s.  A tile takes an SM 3000 to 3300 cycles; its bytes alone
 // would take 2230, its 36 MMAs 2155 (some 60 each whatever N is).  What is
 // left is the way of a tile through the pipeline: scores 2500 cycles beside
 // the output product before, softmax 2100, output 2000, conversion of the
 // tile that takes its place 1300, over two K8 tiles; a third one (64 KB) does
-// not fit.  Short calls (32 sequences of up to 8191 tokens: 27.8 us, 2.0 TB/s;
-// one of 131071: 25 us, 2.1 TB/s; six or seven tiles per SM) spend 15000
+// not fit.  Short calls (32 sequences of up to 8191 tokens: 27.2 us, 2.1 TB/s;
+// one of 131071: 24.7 us, 2.1 TB/s; six or seven tiles per SM) spend 15000
 // cycles, 8 us, until the first probabilities, and 5 to 6 us in the join.
 #pragma once
 
