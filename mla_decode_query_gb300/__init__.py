@@ -2,7 +2,7 @@
 latent cache with the attention over it, and the V up-projection after it.
 
 The operation runs in ``libmlaqp.so`` (CUDA C++ for sm_103a, C ABI in
-``include/mlaqp.h`` and ``include/mlaqp_kv4.h``); ``mla_decode_query_gb300.mlaqp`` is its thin ctypes
+``include/mlaqp.h``, ``include/mlaqp_kv4.h`` and ``include/mlaqp_kv4_step.h``); ``mla_decode_query_gb300.mlaqp`` is its thin ctypes
 binding and ``mla_decode_query_gb300.inputs`` the seeded synthetic inputs.
 Importing the package does not load the library; the first call does, and
 fails loudly if it has not been built.
@@ -16,6 +16,9 @@ from .mlaqp import (  # noqa: F401
     MLAQP_DEVSTATUS_BAD_INDEX,
     MLAQP_DEVSTATUS_OUT_OF_PAGES,
     MLAQP_DEVSTATUS_WAIT_TIMEOUT,
+    MLAQP_KV4_DIGEST_BYTES,
+    MLAQP_ROPE_HALVES,
+    MLAQP_ROPE_INTERLEAVED,
     MLAQP_ERR_CUDA,
     MLAQP_ERR_INVALID_ARG,
     MLAQP_ERR_UNSUPPORTED,
@@ -39,10 +42,12 @@ from .mlaqp import (  # noqa: F401
     mlaqp_debug_v_up_bounded_wait,
     mlaqp_device_status,
     mlaqp_kv4_append,
+    mlaqp_kv4_append_rope,
     mlaqp_kv4_attend,
     mlaqp_kv4_attend_workspace,
     mlaqp_kv4_compact,
     mlaqp_kv4_copy_pages,
+    mlaqp_kv4_digest,
     mlaqp_kv4_extend,
     mlaqp_kv4_fork,
     mlaqp_kv4_gather,
@@ -50,6 +55,9 @@ from .mlaqp import (  # noqa: F401
     mlaqp_kv4_pages_workspace,
     mlaqp_kv4_prewarm,
     mlaqp_kv4_release,
+    mlaqp_kv4_select,
+    mlaqp_kv4_select_workspace,
+    mlaqp_kv4_step_prewarm,
     mlaqp_last_error,
     mlaqp_launch_shape,
     mlaqp_prefetch_weights,

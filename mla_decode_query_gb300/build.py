@@ -26,7 +26,8 @@ LIB_PATH = LIB_DIR / "libmlaqp.so"
 
 SOURCES = ["mlaqp_api.cu", "mlaqp_kernels_bf16.cu", "mlaqp_kernels_mxfp8.cu", "mlaqp_kernels_large.cu",
            "mlaqp_kernels_v_up.cu", "mlaqp_kernels_warp_bf16.cu", "mlaqp_kernels_warp_mxfp8.cu",
-           "mlaqp_kv4_api.cu", "mlaqp_kv4_rows.cu", "mlaqp_kv4_pages.cu", "mlaqp_kv4_attend.cu"]
+           "mlaqp_kv4_api.cu", "mlaqp_kv4_rows.cu", "mlaqp_kv4_pages.cu", "mlaqp_kv4_attend.cu",
+           "mlaqp_kv4_step_api.cu", "mlaqp_kv4_rope.cu", "mlaqp_kv4_digest.cu", "mlaqp_kv4_select.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 f"-I{INCLUDE}", f"-I{CSRC}"]

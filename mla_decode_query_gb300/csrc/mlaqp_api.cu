@@ -1238,7 +1238,7 @@ int mlaqp_prefetch_weights(const void* weight, const void* weight_scale, int H, 
 
 int mlaqp_device_status(unsigned int* status, int reset) {
   if (!status) return fail(MLAQP_ERR_INVALID_ARG, "status must not be NULL");
-  unsigned int a = 0, b = 0, c = 0, v = 0, wa = 0, wb = 0, ka = 0, kr = 0, kp = 0;
+  unsigned int a = 0, b = 0, c = 0, v = 0, wa = 0, wb = 0, ka = 0, kr = 0, kp = 0, ko = 0, kd = 0, ks = 0;
   cudaError_t e = mlaqp::device_status_bf16_weights(&a, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_mxfp8_weights(&b, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_large_m(&c, reset != 0);
@@ -1248,8 +1248,11 @@ int mlaqp_device_status(unsigned int* status, int reset) {
   if (e == cudaSuccess) e = mlaqp::device_status_kv4_attend(&ka, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_kv4_rows(&kr, reset != 0);
   if (e == cudaSuccess) e = mlaqp::device_status_kv4_pages(&kp, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_rope(&ko, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_digest(&kd, reset != 0);
+  if (e == cudaSuccess) e = mlaqp::device_status_kv4_select(&ks, reset != 0);
   if (e != cudaSuccess) return fail_cuda("reading the device status word", e);
-  *status = a | b | c | v | wa | wb | ka | kr | kp;
+  *status = a | b | c | v | wa | wb | ka | kr | kp | ko | kd | ks;
   return MLAQP_OK;
 }
 

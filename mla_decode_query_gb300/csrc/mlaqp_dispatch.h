@@ -78,5 +78,8 @@ cudaError_t device_status_warp_mxfp8(unsigned int* value, bool reset);
 cudaError_t device_status_kv4_attend(unsigned int* value, bool reset);
 cudaError_t device_status_kv4_rows(unsigned int* value, bool reset);
 cudaError_t device_status_kv4_pages(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_rope(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_digest(unsigned int* value, bool reset);
+cudaError_t device_status_kv4_select(unsigned int* value, bool reset);
 
 }  // namespace mlaqp

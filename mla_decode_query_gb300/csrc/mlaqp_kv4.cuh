@@ -50,6 +50,28 @@ __device__ __forceinline__ uint32_t kv4_word(const float (&f)[8]) {
   return (e2m1x8(f) & 0x77777777u) | (e2m1x8(s) & 0x88888888u);
 }
 
+// Word lane + 32k of a token (eight latents, as floats) into its page at
+// position `at`, with its block's scale byte.  The whole warp calls.
+__device__ __forceinline__ void kv4_put_word(uint8_t* base, uint32_t at, int shift, int k, float (&y)[8]) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t amax = 0;  // bits of the largest magnitude; a NaN's lie above those of infinity
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // a block is four lanes
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const bool bad = amax >= 0x7F800000u;
+  // exponent - 2, one more when the significand exceeds 1.75 = 7/4
+  const int s = min(max(static_cast<int>((amax + 0x1FFFFFu) >> 23) - 2, kKv4ScaleMin), kKv4ScaleMax);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - s) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] *= inv;
+  // blocks with bit 2 set have their halves swapped
+  const uint32_t word = 128 * k + 4 * (lane ^ ((lane >> 3) & 2));
+  *reinterpret_cast<uint32_t*>(base + kv4_code_off(at) + word) = bad ? 0u : kv4_word(y);
+  if ((lane & 3) == 0)
+    base[kv4_scale_off(at, shift) + 8 * k + (lane >> 2)] = static_cast<uint8_t>(bad ? kKv4ScaleNan : s);
+}
+
 // Four magnitudes (the low 16 bits of `mags`: nibbles 0..7) and their signs
 // (the top bits of the bytes of `signs`) -> two BF16x2 registers of the plain
 // code values (0, 0.5 .. 6): byte permutes look the two bytes of each value

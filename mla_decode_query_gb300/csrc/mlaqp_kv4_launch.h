@@ -47,6 +47,64 @@ cudaError_t kv4_append(const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t kv4_gather(const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t kv4_rows_setup();
 
+struct Kv4RopeParams {
+  Kv4Cache cache;
+  const uint16_t* latent;
+  const uint16_t* k_pe;
+  int64_t latent_ts, k_pe_ts;
+  const uint16_t* norm_weight;  // nullptr: no norm
+  float eps;
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  uint16_t* q_out;
+  int64_t q_out_ts, q_out_hs;
+  int H;
+  const int32_t* positions;
+  const float* cos_sin;
+  int num_positions;
+  const int32_t* slots;
+  int T;
+};
+cudaError_t kv4_append_rope(const Kv4RopeParams& p, bool halves, cudaStream_t stream);
+cudaError_t kv4_rope_setup();
+
+struct Kv4DigestParams {
+  Kv4Cache cache;
+  uint8_t* digests;
+  int64_t digest_stride;   // bytes
+  const int32_t* block_table;
+  int64_t table_stride;
+  int num_seqs;
+  const int32_t* seq_lens;
+  const int32_t* seqs;
+  const int32_t* new_tokens;
+  int n, max_new;
+};
+cudaError_t kv4_digest(const Kv4DigestParams& p, int sm_count, cudaStream_t stream);
+cudaError_t kv4_digest_setup();
+
+struct Kv4SelectParams {
+  const uint8_t* q;
+  int64_t q_ts;            // elements
+  const uint8_t* digests;
+  int64_t digest_stride;   // bytes
+  int num_pages, shift;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int num_seqs;
+  const int32_t* seq_lens;
+  const int32_t* seqs;
+  int B, q_len, H;
+  int k, first, last;
+  int32_t* table;
+  int64_t sel_stride;
+  int32_t* lens;
+  uint32_t* keys;          // [B*q_len][width]
+  int64_t width;
+};
+cudaError_t kv4_select(const Kv4SelectParams& p, bool q_e4m3, int sm_count, cudaStream_t stream);
+cudaError_t kv4_select_setup();
+
 // The sequence tables that the page operations change.
 struct Kv4Tables {
   int32_t* block_table;

@@ -1,4 +1,5 @@
-"""ctypes binding of ``libmlaqp.so`` (declared in ``include/mlaqp.h`` and ``include/mlaqp_kv4.h``).
+"""ctypes binding of ``libmlaqp.so`` (declared in ``include/mlaqp.h``, ``include/mlaqp_kv4.h`` and
+``include/mlaqp_kv4_step.h``).
 
 Argument marshalling only: every function here forwards to the C entry point
 of the same name and returns its status code unchanged; all of the operation
@@ -30,6 +31,11 @@ MLAQP_ERR_UNSUPPORTED = 1
 MLAQP_ERR_INVALID_ARG = 2
 MLAQP_ERR_CUDA = 3
 
+MLAQP_ROPE_INTERLEAVED = 0
+MLAQP_ROPE_HALVES = 1
+
+MLAQP_KV4_DIGEST_BYTES = 1168
+
 MLAQP_DEVSTATUS_WAIT_TIMEOUT = 1
 MLAQP_DEVSTATUS_BAD_INDEX = 2
 MLAQP_DEVSTATUS_OUT_OF_PAGES = 4
@@ -43,6 +49,7 @@ MAX_M_DECODE = 32
 V_HEAD_DIM = 128
 
 WEIGHT_FORMATS = {"bf16": MLAQP_WEIGHT_BF16, "mxfp8": MLAQP_WEIGHT_MXFP8}
+ROPE_STYLES = {"interleaved": MLAQP_ROPE_INTERLEAVED, "halves": MLAQP_ROPE_HALVES}
 OUT_DTYPES = {"bf16": MLAQP_OUT_BF16, "e4m3": MLAQP_OUT_E4M3}
 
 _lock = threading.Lock()
@@ -106,6 +113,17 @@ _SIGNATURES = {
     "mlaqp_kv4_copy_pages": (_c_int, _KV4_POOL + [_c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_void_p]),
     "mlaqp_kv4_pages_workspace": (_c_int64, [_c_int, _c_int]),
     "mlaqp_kv4_prewarm": (_c_int, [_c_int]),
+    "mlaqp_kv4_append_rope": (_c_int, [_c_void_p, _c_int64, _c_void_p, ctypes.c_float, _c_void_p, _c_int64, _c_void_p,
+                                       _c_int64, _c_int64, _c_void_p, _c_int64, _c_int64, _c_int, _c_void_p, _c_void_p,
+                                       _c_int, _c_int, _c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int,
+                                       _c_void_p]),
+    "mlaqp_kv4_digest": (_c_int, [_c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int64, _c_int, _c_void_p, _c_void_p,
+                                  _c_void_p, _c_int, _c_int, _c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_select": (_c_int, [_c_void_p, _c_int64, _c_int, _c_void_p, _c_int64, _c_int, _c_int, _c_void_p, _c_int64,
+                                  _c_int, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                  _c_void_p, _c_int64, _c_void_p, _c_void_p, _c_int64, _c_void_p]),
+    "mlaqp_kv4_select_workspace": (_c_int64, [_c_int, _c_int, _c_int64, _c_int]),
+    "mlaqp_kv4_step_prewarm": (_c_int, [_c_int]),
     "mlaqp_last_error": (ctypes.c_char_p, []),
     "mlaqp_version": (_c_int, []),
 }
@@ -417,6 +435,44 @@ def mlaqp_kv4_pages_workspace(num_pages, n) -> int:
 
 def mlaqp_kv4_prewarm(device=-1) -> int:
     return load_library().mlaqp_kv4_prewarm(int(device))
+
+
+def mlaqp_kv4_append_rope(latent, latent_token_stride, norm_weight, norm_eps, k_pe, k_pe_token_stride, q_pe, q_token_stride,
+                          q_head_stride, q_pe_out, q_out_token_stride, q_out_head_stride, H, positions, cos_sin,
+                          num_positions, rope_style, cache, page_stride, num_pages, page_size, slots, T,
+                          stream=None) -> int:
+    return load_library().mlaqp_kv4_append_rope(
+        _ptr(latent), int(latent_token_stride), _ptr(norm_weight), float(norm_eps), _ptr(k_pe), int(k_pe_token_stride),
+        _ptr(q_pe), int(q_token_stride), int(q_head_stride), _ptr(q_pe_out), int(q_out_token_stride),
+        int(q_out_head_stride), int(H), _ptr(positions), _ptr(cos_sin), int(num_positions), _fmt(rope_style, ROPE_STYLES),
+        _ptr(cache), int(page_stride), int(num_pages), int(page_size), _ptr(slots), int(T), _stream(stream))
+
+
+def mlaqp_kv4_digest(cache, page_stride, num_pages, page_size, block_table, block_table_stride, num_seqs, seq_lens, seqs,
+                     new_tokens, n, max_new, digests, digest_stride, stream=None) -> int:
+    return load_library().mlaqp_kv4_digest(
+        _ptr(cache), int(page_stride), int(num_pages), int(page_size), _ptr(block_table), int(block_table_stride),
+        int(num_seqs), _ptr(seq_lens), _ptr(seqs), _ptr(new_tokens), int(n), int(max_new), _ptr(digests),
+        int(digest_stride), _stream(stream))
+
+
+def mlaqp_kv4_select(q, q_token_stride, q_dtype, digests, digest_stride, num_pages, page_size, block_table,
+                     block_table_stride, num_seqs, seq_lens, seqs, B, q_len, H, k, first, last, sel_table, sel_stride,
+                     sel_lens, workspace, workspace_bytes, stream=None) -> int:
+    return load_library().mlaqp_kv4_select(
+        _ptr(q), int(q_token_stride), _fmt(q_dtype, OUT_DTYPES), _ptr(digests), int(digest_stride), int(num_pages),
+        int(page_size), _ptr(block_table), int(block_table_stride), int(num_seqs), _ptr(seq_lens), _ptr(seqs), int(B),
+        int(q_len), int(H), int(k), int(first), int(last), _ptr(sel_table), int(sel_stride), _ptr(sel_lens),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def mlaqp_kv4_select_workspace(B, q_len, block_table_stride, num_pages) -> int:
+    """Bytes of workspace, or -1 (see ``mlaqp_last_error``)."""
+    return load_library().mlaqp_kv4_select_workspace(int(B), int(q_len), int(block_table_stride), int(num_pages))
+
+
+def mlaqp_kv4_step_prewarm(device=-1) -> int:
+    return load_library().mlaqp_kv4_step_prewarm(int(device))
 
 
 def mlaqp_device_status(reset=False):
