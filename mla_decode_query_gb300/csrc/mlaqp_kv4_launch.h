@@ -10,17 +10,21 @@ namespace mlaqp {
 // Launch with programmatic dependent launch: every kernel of the 4-bit cache
 // waits for the previous one before it touches memory.
 inline cudaError_t kv4_launch(const void* fn, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
-                              void** args) {
+                              void** args, unsigned cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -101,6 +105,7 @@ struct Kv4SelectParams {
   int32_t* lens;
   uint32_t* keys;          // [B*q_len][width]
   int64_t width;
+  int cluster;             // CTAs of a sequence (set by kv4_select)
 };
 cudaError_t kv4_select(const Kv4SelectParams& p, bool q_e4m3, int sm_count, cudaStream_t stream);
 cudaError_t kv4_select_setup();
