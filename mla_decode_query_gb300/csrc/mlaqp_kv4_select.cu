@@ -22,6 +22,8 @@
 // 2048 places over the range that is still open (mostly two), then the pages
 // from there on in order of position.
 
+#include <atomic>
+
 #include "mlaqp_dispatch.h"
 #include "mlaqp_kv4.cuh"
 #include "mlaqp_kv4_launch.h"
@@ -31,26 +33,25 @@ namespace mlaqp {
 
 namespace {
 
-constexpr int kSelectChunks = kOutDim / 8;           // of eight channels
-constexpr int kSelectHeadGroups = 4;                 // heads h, h + 4, .. of a thread
-constexpr int kSelectThreads = kSelectChunks * kSelectHeadGroups;
+constexpr int kSelectThreads = 256;                  // eight warps: with two CTAs an SM 128 registers a thread
+constexpr int kSelectChunks = kLatent / 8;           // latents: a thread's are eight channels of four heads
+constexpr int kSelectHeadGroups = kSelectThreads / kSelectChunks;
+constexpr int kRopeChunks = kRope / 8;               // rope part: eight channels of one head, half of the threads
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectCtasPerSm = 2;
-constexpr int kSelectMaxCluster = 8;
 constexpr int kScorePages = 4;                       // in flight per warp
-constexpr int kScoreWords = 18;                      // pairs of up / down of a lane: 8 + 8 + 2
-constexpr int kScoreLane = 20;                       // a lane's words apart: 16-byte loads without bank conflicts
+constexpr int kScoreLane = 20;                       // a lane's 18 pairs of up / down apart: 16-byte loads without bank conflicts
 constexpr int kQueryWords = 32 * kScoreLane;         // of a query token
-constexpr int kBatchBytes = kScorePages * 2 * kOutDim;  // of digests, without their exponents
-constexpr int kStages = 2;                           // batches of a warp in shared memory
 constexpr int kBins = 2048, kBinsLog = 11;
-constexpr int kBinThreads = 256, kBinsEach = kBins / kBinThreads;
+constexpr int kBinsEach = kBins / kSelectThreads;
 constexpr int kCandidates = 32;                      // keys that a warp ranks
+constexpr int kFewEach = 4, kFewKeys = kFewEach * kSelectThreads;  // keys that the threads hold
+constexpr int kFewBins = 512, kFewBinsLog = 9;
 constexpr int kHeldKeys = 2048;                      // keys and pages that stay in shared memory
 constexpr int kChooseEach = 4;                       // pages of a thread in one sweep in order
-static_assert(kSelectThreads % 32 == 0 && kSelectThreads >= kBinThreads, "whole warps, a thread for some bins");
+static_assert(kRopeChunks * MLAQP_KV4_MAX_HEADS <= kSelectThreads && kBinsEach == 8 && kFewEach == 4, "threads");
 
-// Dynamic shared memory: this, the warps' stages (later the bins), the queries' words.
+// Dynamic shared memory: this, then the queries' words.
 struct SelectShared {
   uint32_t amax[kSelectWarps];
   uint32_t lo[kSelectWarps], hi[kSelectWarps];
@@ -59,15 +60,17 @@ struct SelectShared {
   int above, in;   // keys above that place, in it
   int found;       // candidates
   uint32_t candidate[kCandidates];
+  alignas(16) unsigned bins[kBins];
   alignas(16) uint32_t keys[kHeldKeys];  // of this CTA's query tokens, one after the other
   union {
-    alignas(16) uint32_t part[kSelectHeadGroups][kOutDim];  // up << 16 | -down, sums over a thread's heads
+    struct {  // up << 16 | -down
+      alignas(16) uint32_t part[kSelectHeadGroups][kLatent];        // sums over a thread's heads
+      alignas(16) uint32_t rope_part[MLAQP_KV4_MAX_HEADS][kRope];   // of a head
+    };
     alignas(16) int32_t pages[kHeldKeys];                   // (later) of the sequence, up to the last ones
   };
 };
-constexpr int kStagesAt = (sizeof(SelectShared) + 127) / 128 * 128;
-constexpr int kWordsAt = kStagesAt + kSelectWarps * kStages * kBatchBytes;
-static_assert(kBins * 4 <= kSelectWarps * kStages * kBatchBytes, "the bins take the stages' place");
+constexpr int kWordsAt = (sizeof(SelectShared) + 15) / 16 * 16;
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return tokens > 0 ? ((tokens - 1) >> shift) + 1 : 0; }
 
@@ -88,18 +91,11 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t rank, uint32_
       "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(addr), "r"(rank), "r"(v)
       : "memory");
 }
-// Asynchronous copies of this thread into shared memory; it alone reads them.
-__device__ __forceinline__ void copy_16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
+// Asynchronous copy of a word into shared memory, and the wait for this thread's.
 __device__ __forceinline__ void copy_4(uint32_t to, const void* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {  // all but the last N groups
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint32_t ld_l2(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -123,7 +119,9 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 // --------------------------------------------------------------------------
 constexpr int kQueryHeads = MLAQP_KV4_MAX_HEADS / kSelectHeadGroups;
 struct QueryPart {
-  uint32_t v[kQueryHeads][4];  // this thread's eight channels of its heads: pairs of BF16, or E4M3 codes in the first two
+  // this thread's eight latent channels of its heads, then its rope channels:
+  // pairs of BF16, or E4M3 codes in the first two
+  uint32_t v[kQueryHeads + 1][4];
 };
 
 // Four E4M3 codes as FP16 pairs (exact; NaN stays one).
@@ -146,14 +144,16 @@ __device__ __forceinline__ float f16_hi(uint32_t v) { return f16_lo(v >> 16); }
 
 template <bool E4>
 __device__ __forceinline__ void load_query(const Kv4SelectParams& p, int64_t m, QueryPart& q) {
-  const int chunk = threadIdx.x % kSelectChunks, g = threadIdx.x / kSelectChunks;
+  const int tid = threadIdx.x, chunk = tid % kSelectChunks, g = tid / kSelectChunks;
 #pragma unroll
-  for (int i = 0; i < kQueryHeads; ++i) {
-    const int h = g + kSelectHeadGroups * i;
+  for (int i = 0; i <= kQueryHeads; ++i) {
+    const bool rope = i == kQueryHeads;
+    const int h = rope ? tid / kRopeChunks : g + kSelectHeadGroups * i;
+    const int c = rope ? kLatent + 8 * (tid % kRopeChunks) : 8 * chunk;
     uint32_t(&v)[4] = q.v[i];
     v[0] = v[1] = v[2] = v[3] = 0;
     if (h >= p.H) continue;
-    const int64_t at = m * p.q_ts + h * kOutDim + 8 * chunk;
+    const int64_t at = m * p.q_ts + h * kOutDim + c;
     if constexpr (E4) {
       asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p.q + at));
     } else {
@@ -163,15 +163,12 @@ __device__ __forceinline__ void load_query(const Kv4SelectParams& p, int64_t m, 
   }
 }
 
-// Into `words` ([32 lanes][kScoreLane], this CTA's address) of `ctas` CTAs of
-// the cluster, or of this one alone (0).  All threads call.
+// Its largest magnitude, for all: into s.amax, behind a barrier of the caller.
 template <bool E4>
-__device__ __forceinline__ void query_words(SelectShared& s, QueryPart& q, uint32_t* words, int ctas) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = tid % kSelectChunks, g = tid / kSelectChunks;
+__device__ __forceinline__ void query_top(SelectShared& s, QueryPart& q) {
   uint32_t amax = 0;  // bits of the largest magnitude, BF16 or FP16
 #pragma unroll
-  for (int i = 0; i < kQueryHeads; ++i) {
+  for (int i = 0; i <= kQueryHeads; ++i) {
     if constexpr (E4) {
       const uint2 x = e4m3x4_f16(q.v[i][0]), y = e4m3x4_f16(q.v[i][1]);
       q.v[i][0] = x.x, q.v[i][1] = x.y, q.v[i][2] = y.x, q.v[i][3] = y.y;
@@ -180,8 +177,15 @@ __device__ __forceinline__ void query_words(SelectShared& s, QueryPart& q, uint3
     for (int u = 0; u < 4; ++u) amax = __vmaxu2(amax, q.v[i][u] & 0x7FFF7FFFu);
   }
   amax = __reduce_max_sync(0xffffffffu, max(amax & 0xFFFFu, amax >> 16));
-  if (lane == 0) s.amax[warp] = amax;
-  __syncthreads();  // (also: the token before has been read from s.part)
+  if ((threadIdx.x & 31) == 0) s.amax[threadIdx.x >> 5] = amax;
+}
+
+// Into `words` ([32 lanes][kScoreLane], this CTA's address) of `ctas` CTAs of
+// the cluster, or of this one alone (0).  All threads call.
+template <bool E4>
+__device__ __forceinline__ void query_words(SelectShared& s, const QueryPart& q, uint32_t* words, int ctas) {
+  const int tid = threadIdx.x;
+  uint32_t amax = 0;
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) amax = max(amax, s.amax[w]);
   const bool none = amax >= (E4 ? 0x7C00u : 0x7F80u);  // a NaN or an infinity
@@ -194,35 +198,37 @@ __device__ __forceinline__ void query_words(SelectShared& s, QueryPart& q, uint3
   constexpr float kWhole = 12582912.f;
   constexpr int kWholeBits = 0x4B400000;
   int up[8] = {}, all[8] = {};
-#pragma unroll
-  for (int i = 0; i < kQueryHeads; ++i)
+  auto add = [&](const uint32_t (&v)[4]) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const uint32_t two = q.v[i][u >> 1];
+      const uint32_t two = v[u >> 1];
       const float x = E4 ? (u & 1 ? f16_hi(two) : f16_lo(two)) : (u & 1 ? bf16_hi(two) : bf16_lo(two));
       const int n = __float_as_int(__fmaf_rn(x, scale, kWhole));
       all[u] += n - kWholeBits;
       up[u] += max(n, kWholeBits) - kWholeBits;
     }
-  uint32_t packed[8];
+  };
+  auto put = [&](uint32_t* to) {
+    uint32_t two[8];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) packed[u] = none ? 0u : static_cast<uint32_t>(up[u] << 16 | (up[u] - all[u]));
-  *reinterpret_cast<uint4*>(&s.part[g][8 * chunk]) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-  *reinterpret_cast<uint4*>(&s.part[g][8 * chunk + 4]) = make_uint4(packed[4], packed[5], packed[6], packed[7]);
+    for (int u = 0; u < 8; ++u) two[u] = none ? 0u : static_cast<uint32_t>(up[u] << 16 | (up[u] - all[u]));
+    *reinterpret_cast<uint4*>(to) = make_uint4(two[0], two[1], two[2], two[3]);
+    *reinterpret_cast<uint4*>(to + 4) = make_uint4(two[4], two[5], two[6], two[7]);
+  };
+#pragma unroll
+  for (int i = 0; i < kQueryHeads; ++i) add(q.v[i]);
+  put(&s.part[tid / kSelectChunks][8 * (tid % kSelectChunks)]);
+  if (tid < kRopeChunks * MLAQP_KV4_MAX_HEADS) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) up[u] = all[u] = 0;
+    add(q.v[kQueryHeads]);
+    put(&s.rope_part[tid / kRopeChunks][8 * (tid % kRopeChunks)]);
+  }
   __syncthreads();
-  // word w of lane l: pairs of up for the latents 16l.., of down for the same,
-  // and of up (l < 16) or down for four rope elements
-#pragma unroll
-  for (int i = tid; i < 32 * kScoreWords; i += kSelectThreads) {
-    const int l = i / kScoreWords, w = i % kScoreWords;
-    const bool rope = w >= 16, high = rope ? l < 16 : w < 8;
-    const int c = rope ? kLatent + 4 * (l & 15) + 2 * (w - 16) : 16 * l + 2 * (w & 7);
-    uint2 sum = make_uint2(0, 0);  // neither half overflows: 16 heads * 2047
-#pragma unroll
-    for (int a = 0; a < kSelectHeadGroups; ++a) {
-      const uint2 x = *reinterpret_cast<const uint2*>(&s.part[a][c]);
-      sum.x += x.x, sum.y += x.y;
-    }
+  // Words w < 16 of lane l: pairs of up for the latents 16l.., of down for the
+  // same; 16 and 17: of up (l < 16) or down for four rope elements.  Neither half
+  // of a sum overflows: 16 heads * 2047.
+  auto word = [&](int l, int w, uint2 sum, bool high) {
     const uint32_t two = high ? __byte_perm(sum.x, sum.y, 0x7632) : __vneg2(__byte_perm(sum.x, sum.y, 0x5410));
     if (ctas == 0) {
       words[l * kScoreLane + w] = two;
@@ -230,6 +236,27 @@ __device__ __forceinline__ void query_words(SelectShared& s, QueryPart& q, uint3
       const uint32_t at = smem_u32(&words[l * kScoreLane + w]);
       for (int r = 0; r < ctas; ++r) st_cluster(at, r, two);
     }
+  };
+#pragma unroll
+  for (int i = tid; i < 32 * 16; i += kSelectThreads) {
+    const int l = i / 16, w = i % 16;
+    uint2 sum = make_uint2(0, 0);
+#pragma unroll
+    for (int a = 0; a < kSelectHeadGroups; ++a) {
+      const uint2 x = *reinterpret_cast<const uint2*>(&s.part[a][16 * l + 2 * (w & 7)]);
+      sum.x += x.x, sum.y += x.y;
+    }
+    word(l, w, sum, w < 8);
+  }
+  if (tid < 64) {
+    const int l = tid / 2, w = tid % 2;
+    uint2 sum = make_uint2(0, 0);
+#pragma unroll
+    for (int a = 0; a < MLAQP_KV4_MAX_HEADS; ++a) {
+      const uint2 x = *reinterpret_cast<const uint2*>(&s.rope_part[a][4 * (l & 15) + 2 * w]);
+      sum.x += x.x, sum.y += x.y;
+    }
+    word(l, 16 + w, sum, l < 16);
   }
 }
 
@@ -237,19 +264,27 @@ __device__ __forceinline__ void query_words(SelectShared& s, QueryPart& q, uint3
 // Scores of four pages at a time
 // --------------------------------------------------------------------------
 
-// A warp's copy of a digest's bounds into `to`, and its score from there.  A
-// lane copies what it reads: 16 bytes of either bound of the latents, 4 of the
-// rope part's.
-__device__ __forceinline__ void copy_digest(uint32_t to, const uint8_t* d) {
-  const int lane = threadIdx.x & 31;
-  copy_16(to + 16 * lane, d + 16 * lane);
-  copy_16(to + kLatent + 16 * lane, d + kLatent + 16 * lane);
-  copy_4(to + 2 * kLatent + 4 * lane, d + 2 * kLatent + 4 * lane);
-}
+// A lane's share of four digests: 16 bytes of either bound of the latents, 4 of
+// the rope part's.
+struct PageBatch {
+  uint4 hi[kScorePages], lo[kScorePages];
+  uint32_t rope[kScorePages];
+  // of the digests whose addresses lanes first .. first + 3 hold
+  __device__ __forceinline__ void load(const uint8_t* at, int first) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) {
+      const uint8_t* d = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), first + u));
+      hi[u] = ld_u128(d + 16 * lane);
+      lo[u] = ld_u128(d + kLatent + 16 * lane);
+      rope[u] = ld_u32(d + 2 * kLatent + 4 * lane);
+    }
+  }
+};
 
-// Keys of the four pages at `batch` for the query token of `words`; exps and
-// good of page `first + u` lie with that lane.  Lane u < 4 gets page u's.
-__device__ __forceinline__ uint32_t score_batch(const uint8_t* batch, const uint32_t* words, uint32_t exps, bool good, int first) {
+// Keys of four pages for the query token of `words`; lane first + u holds page
+// u's exponents, negative for a page out of the pool.  Lane u < 4 gets page u's.
+__device__ __forceinline__ uint32_t score_batch(const PageBatch& batch, const uint32_t* words, int exps, int first) {
   const int lane = threadIdx.x & 31;
   const uint32_t* w = words + lane * kScoreLane;
   int a[kScorePages], r[kScorePages];
@@ -260,7 +295,7 @@ __device__ __forceinline__ uint32_t score_batch(const uint8_t* batch, const uint
     const uint4 x = *reinterpret_cast<const uint4*>(w + 8 * half), y = *reinterpret_cast<const uint4*>(w + 8 * half + 4);
 #pragma unroll
     for (int u = 0; u < kScorePages; ++u) {
-      const uint4 d = *reinterpret_cast<const uint4*>(batch + u * 2 * kOutDim + half * kLatent + 16 * lane);
+      const uint4 d = half ? batch.lo[u] : batch.hi[u];
       a[u] = dp2a(x.x, d.x, a[u], false), a[u] = dp2a(x.y, d.x, a[u], true);
       a[u] = dp2a(x.z, d.y, a[u], false), a[u] = dp2a(x.w, d.y, a[u], true);
       a[u] = dp2a(y.x, d.z, a[u], false), a[u] = dp2a(y.y, d.z, a[u], true);
@@ -270,8 +305,7 @@ __device__ __forceinline__ uint32_t score_batch(const uint8_t* batch, const uint
   const uint2 z = *reinterpret_cast<const uint2*>(w + 16);
 #pragma unroll
   for (int u = 0; u < kScorePages; ++u) {
-    const uint32_t d = *reinterpret_cast<const uint32_t*>(batch + u * 2 * kOutDim + 2 * kLatent + 4 * lane);
-    r[u] = __reduce_add_sync(0xffffffffu, dp2a(z.y, d, dp2a(z.x, d, 0, false), true));
+    r[u] = __reduce_add_sync(0xffffffffu, dp2a(z.y, batch.rope[u], dp2a(z.x, batch.rope[u], 0, false), true));
     a[u] = __reduce_add_sync(0xffffffffu, a[u]);
   }
   // from here on a page a lane
@@ -279,12 +313,11 @@ __device__ __forceinline__ uint32_t score_batch(const uint8_t* batch, const uint
   const int sum = u & 2 ? (u & 1 ? a[3] : a[2]) : (u & 1 ? a[1] : a[0]);
   const int rsum = u & 2 ? (u & 1 ? r[3] : r[2]) : (u & 1 ? r[1] : r[0]);
   exps = __shfl_sync(0xffffffffu, exps, first + u);
-  good = __shfl_sync(0xffffffffu, static_cast<int>(good), first + u);
   const uint32_t ea = exps & 255u, er = exps >> 8 & 255u;
   float f = __fadd_rn(__fmul_rn(static_cast<float>(sum), __uint_as_float(ea << 23)),
                       __fmul_rn(static_cast<float>(rsum), __uint_as_float(er << 23)));
   if (ea == 255u || er == 255u) f = INFINITY;
-  return good ? score_key(f) : 0u;
+  return exps < 0 ? 0u : score_key(f);
 }
 
 // --------------------------------------------------------------------------
@@ -314,26 +347,145 @@ __device__ __noinline__ int4 choose_scan(SelectShared& s, int a, int b) {
   return sum;
 }
 
-// Query token m, which sees n tokens; row: its sequence's pages.  held: the
-// place of its keys in s.keys, -1 where they are in the workspace.  All threads call.
-__device__ __forceinline__ void choose_pages(const Kv4SelectParams& p, SelectShared& s, unsigned* bins, int m, int n,
-                                             const int32_t* row, int held_at) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pages = pages_of(n, p.shift);
-  const int taken = min(pages, p.k);
+// What query token m, which sees n tokens, takes anyway, and what lies behind.
+// row: its sequence's pages.  All threads call.
+__device__ __forceinline__ void put_fixed(const Kv4SelectParams& p, int m, int n, const int32_t* row) {
+  const int tid = threadIdx.x;
+  const int pages = pages_of(n, p.shift), taken = min(pages, p.k);
   int32_t* out = p.table + m * p.sel_stride;
   if (tid == 0) p.lens[m] = pages > 0 ? ((taken - 1) << p.shift) + (n - ((pages - 1) << p.shift)) : 0;
   for (int r = taken + tid; r < p.k; r += kSelectThreads) out[r] = -1;
-  const bool held = held_at >= 0;
-  auto page_at = [&](int j) { return held ? s.pages[j] : row[j]; };
-  if (pages <= p.k) {
-    for (int r = tid; r < pages; r += kSelectThreads) out[r] = page_at(r);
-    return;
+  const bool all = pages <= p.k;
+  const int head = all ? pages : p.first, fixed = all ? pages : p.first + p.last;
+  for (int r = tid; r < fixed; r += kSelectThreads) {
+    const int gap = r < head ? 0 : r - head;
+    out[r < head ? r : p.k - p.last + gap] = row[r < head ? r : pages - p.last + gap];
   }
-  for (int r = tid; r < p.first + p.last; r += kSelectThreads)
-    out[r < p.first ? r : p.k - p.last + (r - p.first)] = page_at(r < p.first ? r : pages - p.last + (r - p.first));
-  const int keep = p.k - p.first - p.last, count = pages - p.first - p.last;  // of the pages between
-  if (keep == 0) return;
+}
+
+// The best `keep` of `count` <= kFewKeys keys from `keys` on, in order, into
+// `out`: keys in registers, one histogram of 512 places over their range, which
+// every warp scans for itself, and the few keys of the place that holds the last
+// one taken ranked.  Four barriers.  False, with nothing written, where too many
+// fall there.  All threads call.
+__device__ __forceinline__ bool choose_few(SelectShared& s, const uint32_t* keys, const int32_t* pages,
+                                           int count, int keep, int32_t* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t key[kFewEach];
+  const int j0 = kFewEach * tid;
+#pragma unroll
+  for (int u = 0; u < kFewEach; ++u) key[u] = 0u;
+  if (j0 < count) {  // (what lies behind the last one is not used)
+    const uint4 x = *reinterpret_cast<const uint4*>(keys + j0);
+    key[0] = x.x, key[1] = x.y, key[2] = x.z, key[3] = x.w;
+  }
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (int u = 0; u < kFewEach; ++u) {
+    if (j0 + u < count) lo = min(lo, key[u]), hi = max(hi, key[u]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) s.lo[warp] = lo, s.hi[warp] = hi;
+  if (tid < kFewBins / 4) reinterpret_cast<uint4*>(s.bins)[tid] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) s.found = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) lo = min(lo, s.lo[w]), hi = max(hi, s.hi[w]);
+  if (lo == 0 && tid == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
+  const int drop = max(32 - __clz(hi - lo) - kFewBinsLog, 0);
+#pragma unroll
+  for (int u = 0; u < kFewEach; ++u)
+    if (j0 + u < count) atomicAdd(&s.bins[(key[u] - lo) >> drop], 1u);
+  __syncthreads();
+  // the 16 places that hold it: lane l sums places 16 (31 - l) to 16 (31 - l) + 15
+  int sum = 0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(s.bins + 16 * (31 - lane) + e);
+    sum += static_cast<int>(x.x + x.y + (x.z + x.w));
+  }
+  int above = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, above, d);
+    if (lane >= d) above += x;
+  }
+  int who = __ffs(__ballot_sync(0xffffffffu, keep <= above)) - 1;
+  const int top = 16 * (31 - who) + 15;
+  const int before16 = __shfl_sync(0xffffffffu, above - sum, who);
+  // then the place: lane l < 16 has the l-th from the top
+  const int n = static_cast<int>(s.bins[top - (lane & 15)]);
+  above = n;
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, above, d);
+    if ((lane & 15) >= d) above += x;
+  }
+  above += before16 - n;
+  who = __ffs(__ballot_sync(0xffffffffu, keep <= above + n)) - 1;
+  const int place = top - who;
+  above = __shfl_sync(0xffffffffu, above, who);
+  const int in = __shfl_sync(0xffffffffu, n, who);
+  const bool rank = above + in != keep && drop > 0;  // some of them, and they differ
+  if (rank && in > kCandidates) return false;
+  lo += static_cast<uint32_t>(place) << drop;
+  hi = lo + ((1u << drop) - 1u);
+  if (rank) {
+    // every warp ranks those that are left
+#pragma unroll
+    for (int u = 0; u < kFewEach; ++u)
+      if (j0 + u < count && key[u] >= lo && key[u] <= hi) s.candidate[atomicAdd(&s.found, 1)] = key[u];
+    __syncthreads();
+    const uint32_t mine = lane < in ? s.candidate[lane] : 0u;
+    int more = 0, same = 0;
+#pragma unroll 1
+    for (int c = 0; c < in; ++c) {
+      const uint32_t other = __shfl_sync(0xffffffffu, mine, c);
+      more += other > mine;
+      same += other == mine;
+    }
+    const bool last = lane < in && above + more < keep && keep <= above + more + same;
+    const int who2 = __ffs(__ballot_sync(0xffffffffu, last)) - 1;
+    lo = hi = __shfl_sync(0xffffffffu, mine, who2);
+    above += __shfl_sync(0xffffffffu, more, who2);
+  }
+  // taken: keys above hi, and of those from lo to hi the first keep - above
+  int mine = 0;  // of this thread: above, equal << 16
+#pragma unroll
+  for (int u = 0; u < kFewEach; ++u)
+    if (j0 + u < count) mine += key[u] > hi ? 1 : key[u] >= lo ? 1 << 16 : 0;
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) s.scan[warp][0] = before;
+  __syncthreads();
+  before -= mine;
+  for (int w = 0; w < warp; ++w) before += s.scan[w][0];
+  int nth = before >> 16;
+  int at = (before & 0xFFFF) + min(nth, keep - above);
+#pragma unroll
+  for (int u = 0; u < kFewEach; ++u) {
+    if (j0 + u >= count) break;
+    const bool mid = key[u] >= lo && key[u] <= hi;
+    if (key[u] > hi || (mid && nth < keep - above)) out[at++] = pages[j0 + u];
+    nth += mid;
+  }
+  return true;
+}
+
+// The same for any number of keys, by histograms of 2048 places over the range
+// that is still open: mostly one or two, then every warp ranks what is left.
+// held: the place of the keys in s.keys, -1 where they are in the workspace.
+// All threads call.
+__device__ __forceinline__ void choose_by_bins(const Kv4SelectParams& p, SelectShared& s, int m, const int32_t* row,
+                                               int held_at, int count, int keep) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t* out = p.table + m * p.sel_stride;
+  const bool held = held_at >= 0;
   const uint32_t* far_keys = p.keys + m * p.width + p.first;
   auto key_of = [&](int j) { return held ? s.keys[held_at + j] : ld_l2(far_keys + j); };
 
@@ -346,7 +498,7 @@ __device__ __forceinline__ void choose_pages(const Kv4SelectParams& p, SelectSha
     hi = max(hi, key);
   }
   if (tid == 0) s.found = 0;
-  for (int e = tid; e < kBins / 4; e += kSelectThreads) reinterpret_cast<uint4*>(bins)[e] = make_uint4(0, 0, 0, 0);
+  for (int e = tid; e < kBins / 4; e += kSelectThreads) reinterpret_cast<uint4*>(s.bins)[e] = make_uint4(0, 0, 0, 0);
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) s.lo[warp] = lo, s.hi[warp] = hi;
@@ -361,14 +513,14 @@ __device__ __forceinline__ void choose_pages(const Kv4SelectParams& p, SelectSha
     const int drop = max(open - kBinsLog, 0);
     for (int j = tid; j < count; j += kSelectThreads) {
       const uint32_t key = key_of(j);
-      if (key >= lo && key - lo <= hi - lo) atomicAdd(&bins[(key - lo) >> drop], 1u);
+      if (key >= lo && key - lo <= hi - lo) atomicAdd(&s.bins[(key - lo) >> drop], 1u);
     }
     __syncthreads();
     // thread t: eight bins from the top, cleared for the next round
     unsigned here[kBinsEach] = {};
     int sum = 0;
-    if (tid < kBinThreads) {
-      uint4* at = reinterpret_cast<uint4*>(bins + kBins - kBinsEach * (tid + 1));
+    {
+      uint4* at = reinterpret_cast<uint4*>(s.bins + kBins - kBinsEach * (tid + 1));
       const uint4 x = at[0], y = at[1];
       at[0] = at[1] = make_uint4(0, 0, 0, 0);
       here[0] = y.w, here[1] = y.z, here[2] = y.y, here[3] = y.x;
@@ -435,7 +587,7 @@ __device__ __forceinline__ void choose_pages(const Kv4SelectParams& p, SelectSha
     for (int u = 0; u < kChooseEach; ++u) {
       if (j + u >= count) break;
       const bool mid = key[u] >= lo && key[u] <= hi;
-      if (key[u] > hi || (mid && nth < keep - above)) out[at++] = page_at(p.first + j + u);
+      if (key[u] > hi || (mid && nth < keep - above)) out[at++] = held ? s.pages[p.first + j + u] : row[p.first + j + u];
       nth += mid;
     }
     done += before.z;
@@ -482,36 +634,44 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
   const int pages = pages_of(len, p.shift);
   const int count = pages > p.k ? pages - p.first - p.last : 0;
   const int tokens = (p.q_len + ctas - 1) / ctas;  // a CTA chooses for tokens rank, rank + ctas, ..
-  const bool held = count > 0 && pages <= kHeldKeys && static_cast<int64_t>(tokens) * count <= kHeldKeys;
+  const int room = (count + 3) / 4 * 4;            // for a token's keys
+  const bool held = count > 0 && pages <= kHeldKeys && static_cast<int64_t>(tokens) * room <= kHeldKeys;
   if (count > 0) {
     const int32_t* between = row + p.first;
-    // Batch k of this warp is four entries, its lane u + 4 (k % 8) holding page
-    // u: entries and exponents of eight batches at a time.
+    // Batch k of this warp is four entries, its lane u + 4 (k % 8) seeing to entry
+    // u: addresses and exponents of eight batches at a time.  In the place of a
+    // page out of the pool, and behind the last one, page 0's digest is read and
+    // not used.
     const int warps = kSelectWarps * ctas, mine = kSelectWarps * rank + warp;
     const int batches = ((count + kScorePages - 1) / kScorePages - mine + warps - 1) / warps;
     auto entry = [&](int k0) {
       const int n = kScorePages * (warps * (k0 + lane / kScorePages) + mine) + lane % kScorePages;
       return n < count ? between[n] : -1;
     };
-    auto digest_of = [&](int page) { return p.digests + page * p.digest_stride; };
     auto in_pool = [&](int page) { return page >= 0 && page < p.num_pages; };
-    const uint32_t stages = smem_u32(smem + kStagesAt) + warp * kStages * kBatchBytes;
-    auto copy_batch = [&](int k, int page) {  // page: of the eight batches with k
-#pragma unroll
-      for (int u = 0; u < kScorePages; ++u) {
-        const int id = __shfl_sync(0xffffffffu, page, k % 8 * kScorePages + u);
-        if (k < batches && in_pool(id)) copy_digest(stages + (k % kStages) * kBatchBytes + u * 2 * kOutDim, digest_of(id));
-      }
-      copy_commit();
+    auto digest_of = [&](int page) { return p.digests + (in_pool(page) ? page : 0) * p.digest_stride; };
+    auto exps_of = [&](int page, const uint8_t* digest) {
+      const int e = static_cast<int>(ld_u32(digest + 2 * kOutDim) & 0xFFFFu);
+      return in_pool(page) ? e : -1;
     };
-    int page = entry(0), next = -1;
-    copy_batch(0, page);
-    copy_batch(1, page);
-    uint32_t exps = in_pool(page) ? ld_u32(digest_of(page) + 2 * kOutDim) : 0u, next_exps = 0;
+    // the queries' largest magnitude while the first entries are under way, the rest
+    // of the queries while the first digests are
+    int next = entry(0);
+    if (i < p.q_len) query_top<E4>(s, q);
+    __syncthreads();
+    const uint8_t *digest = digest_of(next), *next_digest = digest;
+    PageBatch even, odd;
+    even.load(digest, 0);
+    int exps = exps_of(next, digest), next_exps = exps;
     if (ctas > 1) cluster_wait();  // the others are there: their shared memory may be written
-    for (; i < p.q_len; i += step) {
+    while (i < p.q_len) {
       query_words<E4>(s, q, words + i * kQueryWords, share ? ctas : 0);
-      if (i + step < p.q_len) load_query<E4>(p, m0 + i + step, q);
+      i += step;
+      if (i >= p.q_len) break;
+      load_query<E4>(p, m0 + i, q);
+      __syncthreads();  // (s.amax and s.part have been read)
+      query_top<E4>(s, q);
+      __syncthreads();
     }
     if (share) {
       cluster_arrive();
@@ -519,50 +679,77 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     } else {
       __syncthreads();
     }
-    if (held && rank < p.q_len)  // for the choice, with whatever batch comes next
+    if (held && rank < p.q_len)  // for the choice
       for (int j = tid; j < pages; j += kSelectThreads) copy_4(smem_u32(&s.pages[j]), row + j);
-#pragma unroll 1
-    for (int k = 0; k < batches; ++k) {
-      copy_wait<kStages - 1>();
-      const uint8_t* batch = smem + kStagesAt + (warp * kStages + k % kStages) * kBatchBytes;
-      const int at = k % 8 * kScorePages;
+    // While a batch is scored the one behind it is under way, and its entries
+    // and exponents long before.
+    auto round = [&](const PageBatch& now, PageBatch& then, int k) {
+      if (k % 8 == 0) next = entry(k + 8);
+      if (k % 8 == 4) {
+        next_digest = digest_of(next);
+        next_exps = exps_of(next, next_digest);
+      }
+      if (k + 1 < batches) then.load(k % 8 < 7 ? digest : next_digest, (k + 1) % 8 * kScorePages);
       const int n = kScorePages * (warps * k + mine) + lane;
 #pragma unroll 1
       for (int t = 0; t < p.q_len; ++t) {
-        const uint32_t key = score_batch(batch, words + t * kQueryWords, exps, in_pool(page), at);
+        const uint32_t key = score_batch(now, words + t * kQueryWords, exps, k % 8 * kScorePages);
         if (lane < kScorePages && n < count) {
           if (!held)
             p.keys[(m0 + t) * p.width + p.first + n] = key;
           else
-            st_cluster(smem_u32(&s.keys[t / ctas * count + n]), t % ctas, key);
+            st_cluster(smem_u32(&s.keys[t / ctas * room + n]), t % ctas, key);
         }
       }
-      // what comes next: a batch into this one's place, and its entries long before
-      if (k % 8 == 0) next = entry(k + 8);
-      if (k % 8 == 4) next_exps = in_pool(next) ? ld_u32(digest_of(next) + 2 * kOutDim) : 0u;
-      copy_batch(k + kStages, k % 8 + kStages < 8 ? page : next);
-      if (k % 8 == 7) page = next, exps = next_exps;
+      if (k % 8 == 7) digest = next_digest, exps = next_exps;
+    };
+#pragma unroll 1
+    for (int k = 0; k < batches; k += 2) {
+      round(even, odd, k);
+      if (k + 1 < batches) round(odd, even, k + 1);
     }
-    copy_wait<0>();
-    if (ctas > 1) {  // all keys are there
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-  } else if (ctas > 1) {
-    cluster_wait();
+    copy_wait();
+    if (ctas > 1) cluster_arrive();
   }
-  unsigned* bins = reinterpret_cast<unsigned*>(smem + kStagesAt);
-  for (int t = rank; t < p.q_len; t += ctas)
-    choose_pages(p, s, bins, static_cast<int>(m0) + t, max(0, len - (p.q_len - 1 - t)), row, held ? t / ctas * count : -1);
+  for (int t = rank; t < p.q_len; t += ctas) put_fixed(p, static_cast<int>(m0) + t, max(0, len - (p.q_len - 1 - t)), row);
+  if (ctas > 1)
+    cluster_wait();  // all keys are there
+  else
+    __syncthreads();
+  if (count == 0) return;
+  for (int t = rank; t < p.q_len; t += ctas) {
+    const int m = static_cast<int>(m0) + t, at = held ? t / ctas * room : -1;
+    const int sees = pages_of(max(0, len - (p.q_len - 1 - t)), p.shift);
+    const int keep = p.k - p.first - p.last, from = sees - p.first - p.last;
+    if (sees <= p.k || keep == 0) continue;
+    if (held && from <= kFewKeys &&
+        choose_few(s, s.keys + at, s.pages + p.first, from, keep, p.table + m * p.sel_stride + p.first))
+      continue;
+    choose_by_bins(p, s, m, row, at, from, keep);
+  }
 }
-
 
 const void* select_kernel(bool e4m3) {
   return e4m3 ? reinterpret_cast<const void*>(&mlaqp_kv4_select_kernel<true>)
               : reinterpret_cast<const void*>(&mlaqp_kv4_select_kernel<false>);
 }
+
+// CTAs of a sequence.  As many as find room at two an SM, up to 8 (64 sequences
+// of up to 512 pages: 11.1 us with 4, 15.2 with 2, 17.3 with 8; 16 sequences of
+// up to 569 pages, 4 query tokens: 13.3 with 8, 16.0 with 4, 18.5 with 16), 16
+// where those are no more than the SMs (one sequence of 1024 pages: 6.9 us, 8.4
+// with 8); no more than have a batch for each warp.
+constexpr int kSelectCluster = 8, kSelectWideCluster = 16;
+int select_cluster(int B, int64_t width, int sm_count, bool wide) {
+  int n = wide && B * kSelectWideCluster <= sm_count ? kSelectWideCluster : kSelectCluster;
+  while (n > 1 && B * n > kSelectCtasPerSm * sm_count) n /= 2;
+  const int64_t some = kSelectWarps * kScorePages;
+  while (n > 1 && n / 2 * some >= width) n /= 2;
+  return n;
+}
+
+// Whether the device takes clusters of 16.
+std::atomic<bool> g_wide{false};
 
 constexpr size_t select_bytes(int q_len) { return kWordsAt + sizeof(uint32_t) * kQueryWords * static_cast<size_t>(q_len); }
 
@@ -570,10 +757,7 @@ constexpr size_t select_bytes(int q_len) { return kWordsAt + sizeof(uint32_t) * 
 
 cudaError_t kv4_select(const Kv4SelectParams& params, bool q_e4m3, int sm_count, cudaStream_t stream) {
   Kv4SelectParams p = params;
-  p.cluster = kSelectMaxCluster;
-  while (p.cluster > 1 && p.B * p.cluster > kSelectCtasPerSm * sm_count) p.cluster /= 2;
-  const int64_t some = (p.width + kSelectWarps * kScorePages - 1) / (kSelectWarps * kScorePages);
-  while (p.cluster > 1 && p.cluster / 2 >= some) p.cluster /= 2;
+  p.cluster = select_cluster(p.B, p.width, sm_count, g_wide.load(std::memory_order_relaxed));
   void* args[1] = {&p};
   return kv4_launch(select_kernel(q_e4m3), static_cast<unsigned>(p.B * p.cluster), kSelectThreads, select_bytes(p.q_len),
                     stream, args, static_cast<unsigned>(p.cluster));
@@ -587,8 +771,24 @@ cudaError_t kv4_select_setup() {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(select_bytes(MLAQP_KV4_MAX_Q_LEN)));
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, k);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   }
-  return e;
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSelectWideCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSelectWideCluster, 1, 1);
+  cfg.blockDim = dim3(kSelectThreads, 1, 1);
+  cfg.dynamicSmemBytes = select_bytes(MLAQP_KV4_MAX_Q_LEN);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int room = 0;
+  const cudaError_t asked = cudaOccupancyMaxActiveClusters(&room, select_kernel(false), &cfg);
+  if (asked != cudaSuccess) cudaGetLastError();  // then not
+  g_wide.store(asked == cudaSuccess && room > 0, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 cudaError_t device_status_kv4_select(unsigned int* value, bool reset) { return read_device_status(value, reset); }
