@@ -22,7 +22,7 @@ namespace mlaqp {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // Sum of `hi` and what `lo` holds beyond its last bit.
 struct TwoFloat {
