@@ -3,14 +3,12 @@
 // outwards on a power-of-two grid of the page (one for the latents, one for
 // the rope part).
 //
-// Values are E2M1 codes times a power of two, or BF16: exact in BF16, and a
-// maximum is exact too, so a digest does not depend on the order in which
-// tokens are looked at.  A CTA takes a page.  Latents: a thread takes a block
-// of 32 (16 bytes of codes, one scale byte) of every 16th token; rope rows: a
-// 16-byte chunk of every 32nd token.  Maxima and minima are kept in packed
-// BF16, joined across a warp by shuffles and across warps in shared memory.
-// Bound by memory (400 bytes a token) where there are many pages, by the
-// latency table -> codes -> barriers where there are few.
+// A maximum is exact, so a digest does not depend on the order in which tokens
+// are looked at.  A CTA takes a page, a warp 64 channels of all its tokens, and
+// maxima and minima are kept as packed 16-bit floats and joined across a warp;
+// only the page's magnitude crosses warps.  Bound by the ALU (decoding, maxima
+// and minima of 512 elements a token); where there are few pages by the latency
+// lists -> lengths -> table -> scales, codes -> barriers.
 
 #include "mlaqp_dispatch.h"
 #include "mlaqp_kv4.cuh"
@@ -23,51 +21,60 @@ namespace {
 
 constexpr int kDigestThreads = 256;
 constexpr int kDigestWarps = kDigestThreads / 32;
-constexpr int kDigestCtasPerSm = 4;
+constexpr int kDigestCtasPerSm = 3;
+constexpr int kDigestAhead = 4;  // tokens of a lane under way: 32 of the page
 constexpr int kDigestExpMin = -60, kDigestExpMax = 60;
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+template <bool F16>
+__device__ __forceinline__ uint32_t max_x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  if constexpr (F16)
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+template <bool F16>
+__device__ __forceinline__ uint32_t min_x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  if constexpr (F16)
+    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// Largest and smallest of N pairs of values.
-template <int N>
+// Largest and smallest of N pairs of values, FP16 or BF16.
+template <int N, bool F16 = false>
 struct Extremes {
   uint32_t hi[N], lo[N];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < N; ++i) hi[i] = 0xFF80FF80u, lo[i] = 0x7F807F80u;  // -infinity, +infinity
+    for (int i = 0; i < N; ++i) hi[i] = F16 ? 0xFC00FC00u : 0xFF80FF80u, lo[i] = hi[i] ^ 0x80008000u;  // -infinity, +infinity
   }
   __device__ __forceinline__ void take(int i, uint32_t v) {
-    hi[i] = max_bf16x2(hi[i], v);
-    lo[i] = min_bf16x2(lo[i], v);
+    hi[i] = max_x2<F16>(hi[i], v);
+    lo[i] = min_x2<F16>(lo[i], v);
   }
   // Joined with the lane that differs in bit `mask`: the first half of the
   // pairs stays with the one that has it clear, the second with the other.
-  __device__ __forceinline__ Extremes<N / 2> halve(int mask) const {
-    Extremes<N / 2> r;
+  __device__ __forceinline__ Extremes<N / 2, F16> halve(int mask) const {
+    Extremes<N / 2, F16> r;
     const bool up = (threadIdx.x & mask) != 0;
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       const uint32_t h = __shfl_xor_sync(0xffffffffu, up ? hi[i] : hi[i + N / 2], mask);
       const uint32_t l = __shfl_xor_sync(0xffffffffu, up ? lo[i] : lo[i + N / 2], mask);
-      r.hi[i] = max_bf16x2(up ? hi[i + N / 2] : hi[i], h);
-      r.lo[i] = min_bf16x2(up ? lo[i + N / 2] : lo[i], l);
+      r.hi[i] = max_x2<F16>(up ? hi[i + N / 2] : hi[i], h);
+      r.lo[i] = min_x2<F16>(up ? lo[i + N / 2] : lo[i], l);
     }
     return r;
   }
   __device__ __forceinline__ void join(int mask) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], mask));
-      lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], mask));
+      hi[i] = max_x2<F16>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], mask));
+      lo[i] = min_x2<F16>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], mask));
     }
   }
 };
@@ -75,6 +82,8 @@ struct Extremes {
 constexpr int kDigestJobs = kDigestThreads;  // looked up at once
 struct DigestShared {
   int32_t page[kDigestJobs];
+  alignas(16) uint8_t scales[2][128][kKv4Blocks];  // a page's
+  uint32_t scale[2][kDigestWarps];
   // by warp, of two pages by turns
   uint32_t amax[2][kDigestWarps], rope_amax[2][kDigestWarps];
   unsigned bad[2][kDigestWarps];  // bit 0: of the latents, bit 1: of the rope part
@@ -91,6 +100,18 @@ __device__ __forceinline__ int digest_exponent(uint32_t amax) {
   return max(static_cast<int>((amax + 0x01FFFFu) >> 23) - 127 - 6, kDigestExpMin);
 }
 
+// Value of FP16 bits.
+__device__ __forceinline__ float f16_value(uint32_t bits) {
+  float f;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(bits));
+  return f;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // A pair's two bytes: largest rounded up, smallest rounded down.
 __device__ __forceinline__ void put_pair(uint8_t* hi_at, uint8_t* lo_at, uint32_t hi, uint32_t lo, int e, bool bad) {
   const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -100,89 +121,198 @@ __device__ __forceinline__ void put_pair(uint8_t* hi_at, uint8_t* lo_at, uint32_
   *reinterpret_cast<uint16_t*>(lo_at) = bad ? 0 : static_cast<uint16_t>((l0 & 0xFF) | (l1 & 0xFF) << 8);
 }
 
-// The digest of the page at `base`, into `out`.  Warp w takes the blocks 2w and
-// 2w + 1 of the latents, and of the first four two chunks of the rope rows, each
-// of all tokens: 32 bytes of a row, so that maxima are joined within the warp,
-// lanes of even and odd number one of the two, and only the page's magnitude
-// across warps.  All threads call; turn: 0 and 1 by turns.
-__device__ __forceinline__ void digest_page(DigestShared& s, const uint8_t* base, int shift, uint8_t* out, int turn) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tokens = 1 << shift;
-  unsigned bad = 0;
-  const int first = lane >> 1;  // tokens first, first + 16, ..
-
-  // rope rows, asked for first
-  const bool has_rope = warp < kRope / 16;
-  const int chunk = 2 * warp + (lane & 1);
-  Extremes<4> rope;
-  rope.clear();
-  uint4 row[4];
-  auto rope_rows = [&](int t0) {
+// Rope rows: the first four warps take two 16-byte chunks each, lanes of even
+// and odd number one of the two, of tokens lane / 2, + 16, ..
+struct RopePart {
+  Extremes<4> all;
+  Extremes<1> mine;  // pair lane / 8 of the chunk, when joined
+  uint32_t top;
+  __device__ __forceinline__ static bool has() { return threadIdx.x < 32 * (kRope / 16); }
+  __device__ __forceinline__ static int chunk() { return 2 * (threadIdx.x >> 5) + (threadIdx.x & 1); }
+  // (of 32 tokens)
+  __device__ __forceinline__ static void load(uint4 (&row)[2], const uint8_t* base, int shift, int t0) {
+    const int first = (threadIdx.x & 31) >> 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int t = t0 + first + 16 * i;
-      if (t < tokens) row[i] = ld_u128(base + kv4_rope_off(t, shift) + 16 * (chunk ^ (t & 7)));
+      if (t < 1 << shift) row[i] = ld_u128(base + kv4_rope_off(t, shift) + 16 * (chunk() ^ (t & 7)));
     }
-  };
-  auto rope_take = [&](int t0) {
+  }
+  // whether something is not finite
+  __device__ __forceinline__ bool take(const uint4 (&row)[2], int shift, int t0) {
+    const int first = (threadIdx.x & 31) >> 1;
+    uint32_t odd = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t0 + first + 16 * i >= tokens) break;
+    for (int i = 0; i < 2; ++i) {
+      if (t0 + first + 16 * i >= 1 << shift) break;
       const uint32_t v[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if ((v[u] & 0x7F80u) == 0x7F80u || (v[u] & 0x7F800000u) == 0x7F800000u) bad |= 2u;
-        rope.take(u, v[u]);
+        // a half's exponent of all ones carries into its sign
+        odd |= (v[u] & 0x7F807F80u) + 0x00800080u;
+        all.take(u, v[u]);
       }
     }
-  };
-  if (has_rope) rope_rows(0);
+    return (odd & 0x80008000u) != 0;
+  }
+  __device__ __forceinline__ void join() {
+    mine = all.halve(16).halve(8);
+    mine.join(4);
+    mine.join(2);
+    top = __reduce_max_sync(0xffffffffu, pair_amax(mine.hi[0], mine.lo[0]));
+  }
+};
 
-  const int block = 2 * warp + (lane & 1);
+// The page's exponent of the rope part and its bytes, and the exponent bytes.
+__device__ __forceinline__ void put_rope(uint8_t* out, const RopePart& rope, uint32_t amax, bool bad, bool lat_bad, int e) {
+  const int lane = threadIdx.x & 31;
+  const int re = digest_exponent(amax);
+  bad |= re > kDigestExpMax;
+  if (RopePart::has() && (lane & 6) == 0) {
+    uint8_t* at = out + 2 * kLatent + 2 * (4 * RopePart::chunk() + (lane >> 3));
+    put_pair(at, at + kRope, rope.mine.hi[0], rope.mine.lo[0], re, bad);
+  }
+  const int i = static_cast<int>(threadIdx.x) - (kDigestThreads - 4);
+  if (i >= 0) {
+    const uint32_t exps = (lat_bad ? 255u : static_cast<uint32_t>(e + 127)) | (bad ? 255u : static_cast<uint32_t>(re + 127)) << 8;
+    *reinterpret_cast<uint32_t*>(out + 2 * kOutDim + 4 * i) = i ? 0u : exps;
+  }
+}
+
+// Bounds of a page's latents where FP16 does not hold them (below): in BF16.
+// Warp w takes the blocks 2w and 2w + 1, lanes of even and odd number one of the
+// two, of tokens lane / 2, + 16, ..  All threads call.
+__device__ __noinline__ void digest_any(DigestShared& s, const uint8_t* base, int shift, uint8_t* out, int turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = lane >> 1, block = 2 * warp + (lane & 1);
   Extremes<16> lat;
   lat.clear();
 #pragma unroll 1
-  for (int t0 = 0; t0 < tokens; t0 += 64) {
-    uint4 codes[4];
-    uint32_t scale[4];
+  for (int t = first; t < 1 << shift; t += 16) {
+    const uint4 codes = ld_u128(base + kv4_code_off(t) + 16 * block);
+    const uint32_t f = kv4_scale_bf16x2(base[kv4_scale_off(t, shift) + block]);
+    const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + first + 16 * i;
-      if (t >= tokens) break;
-      codes[i] = ld_u128(base + kv4_code_off(t) + 16 * block);
-      scale[i] = base[kv4_scale_off(t, shift) + block];
+    for (int q = 0; q < 4; ++q) {
+      uint32_t o[4];
+      kv4_word_bf16(word[q], o);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) lat.take(4 * q + u, mul_bf16x2(o[u], f));
     }
-    if (t0 > 0 && has_rope) rope_rows(t0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (t0 + first + 16 * i >= tokens) break;
-      bad |= scale[i] == kKv4ScaleNan;
-      const uint32_t f = kv4_scale_bf16x2(scale[i]);
-      const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t o[4];
-        kv4_word_bf16(word[q], o);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) lat.take(4 * q + u, mul_bf16x2(o[u], f));
-      }
-    }
-    if (has_rope) rope_take(t0);
   }
-
   // lane 2r + (block & 1) is left with pair r of its block
   const Extremes<1> mine = lat.halve(16).halve(8).halve(4).halve(2);
   const uint32_t top = __reduce_max_sync(0xffffffffu, pair_amax(mine.hi[0], mine.lo[0]));
-  uint32_t rtop = 0;
-  Extremes<1> rmine;
-  if (has_rope) {  // pair lane >> 3 of the chunk
-    rmine = rope.halve(16).halve(8);
-    rmine.join(4);
-    rmine.join(2);
-    rtop = __reduce_max_sync(0xffffffffu, pair_amax(rmine.hi[0], rmine.lo[0]));
+  __syncthreads();  // (s.amax has been read)
+  if (lane == 0) s.amax[turn][warp] = top;
+  __syncthreads();
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < kDigestWarps; ++i) amax = max(amax, s.amax[turn][i]);
+  const int e = digest_exponent(amax);
+  // blocks with bit 2 set hold their halves in swapped order
+  const int pair = 16 * block + (first ^ ((block & 4) ? 8 : 0));
+  put_pair(out + 2 * pair, out + kLatent + 2 * pair, mine.hi[0], mine.lo[0], e, e > kDigestExpMax);
+  if (threadIdx.x == 0) out[2 * kOutDim] = static_cast<uint8_t>(e > kDigestExpMax ? 255 : e + 127);
+}
+
+// The digest of the page at `base`, into `out`.  All threads call; turn: 0 and 1
+// by turns.
+//
+// Latents in FP16, relative to the page's largest scale S: code * 2^max(s-S,-13).
+// The codes' FP16 have their lower bytes zero, so one byte permute looks four up,
+// and the pairs stay as they lie, with another code's byte below each: it decides
+// between equals only and is dropped at the end.  (That is 8 cycles a word of eight
+// and a CTA's warp on an SM, BF16 with its two bytes 15.)  A value more than 13
+// octaves down is not exact, but so far below the page's largest, which S is taken
+// from, that its bound is 0, 1 or -1 by its sign alone: with the largest at least 2
+// in these units the grid's step is 2^-5 or more, and 6 * 2^-13 less than it.  Where
+// the largest is below 2 (scale bytes larger than their codes need, which the
+// cache's own calls do not write but for magnitudes below 2^-39), the page is done
+// once more in BF16.
+//
+// Warp w takes the blocks 2w and 2w + 1, a lane two words (8 bytes) of every
+// eighth token.
+__device__ __forceinline__ void digest_page(DigestShared& s, const uint8_t* base, int shift, uint8_t* out, int turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tokens = 1 << shift;
+  const int sub = lane & 3, first = lane >> 2;
+  const int block = 2 * warp + (sub >> 1);
+
+  const int tid = threadIdx.x;
+  uint4 by = make_uint4(0, 0, 0, 0);
+  if (tid < tokens) by = ld_u128(base + kv4_scale_off(tid, shift));
+  uint2 codes[kDigestAhead];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < kDigestAhead; ++i)
+      if (t0 + 8 * i < tokens)
+        asm volatile("ld.global.v2.b32 {%0,%1}, [%2];"
+                     : "=r"(codes[i].x), "=r"(codes[i].y)
+                     : "l"(base + kv4_code_off(t0 + 8 * i + first) + 32 * warp + 8 * sub));
+  };
+  load(0);
+  uint4 row[2];
+  RopePart rope;
+  rope.all.clear();
+  if (RopePart::has()) RopePart::load(row, base, shift, 0);
+
+  uint32_t most = 0;
+  if (tid < tokens) {
+    *reinterpret_cast<uint4*>(s.scales[turn][tid]) = by;
+    const uint32_t w[4] = {by.x, by.y, by.z, by.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = __vmaxu2(most, __vmaxu2(w[i] & 0x00FF00FFu, w[i] >> 8 & 0x00FF00FFu));
+    most = max(most & 0xFFFFu, most >> 16);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) s.scale[turn][warp] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kDigestWarps; ++i) most = max(most, s.scale[turn][i]);
+  unsigned bad = most == kKv4ScaleNan;  // bit 0: of the latents
+  const int top_scale = static_cast<int>(min(max(most, static_cast<uint32_t>(kKv4ScaleMin)), static_cast<uint32_t>(kKv4ScaleMax)));
+
+  Extremes<8, true> lat;
+  lat.clear();
+#pragma unroll 1
+  for (int t0 = 0; t0 < tokens; t0 += 8 * kDigestAhead) {
+#pragma unroll
+    for (int i = 0; i < kDigestAhead; ++i) {
+      if (t0 + 8 * i >= tokens) break;
+      const int sc = min(max(static_cast<int>(s.scales[turn][t0 + 8 * i + first][block]), kKv4ScaleMin), kKv4ScaleMax);
+      const uint32_t f = static_cast<uint32_t>(max(sc - top_scale, -13) + 15) * 0x04000400u;
+      const uint32_t word[2] = {codes[i].x, codes[i].y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t m = word[k] & 0x77777777u;
+        const uint32_t a = __byte_perm(0x3E3C3800u, 0x46444240u, m) | (word[k] & 0x80808080u);
+        const uint32_t b = __byte_perm(0x3E3C3800u, 0x46444240u, m >> 16) | ((word[k] * 16u) & 0x80808080u);
+        lat.take(4 * k, mul_f16x2(a, f));             // elements 1, 3
+        lat.take(4 * k + 1, mul_f16x2(a * 256u, f));  // 0, 2
+        lat.take(4 * k + 2, mul_f16x2(b, f));         // 5, 7
+        lat.take(4 * k + 3, mul_f16x2(b * 256u, f));  // 4, 6
+      }
+    }
+    if (t0 + 8 * kDigestAhead < tokens) load(t0 + 8 * kDigestAhead);
+    if (RopePart::has()) {
+      bad |= rope.take(row, shift, t0) ? 2u : 0u;
+      if (t0 + 8 * kDigestAhead < tokens) RopePart::load(row, base, shift, t0 + 8 * kDigestAhead);
+    }
+  }
+  // lane (first, sub) is left with pair `first` of its eight
+  Extremes<1, true> mine = lat.halve(16).halve(8).halve(4);
+  mine.hi[0] &= 0xFF00FF00u;
+  mine.lo[0] &= 0xFF00FF00u;
+  const uint32_t m2 = __vmaxu2(mine.hi[0] & 0x7FFF7FFFu, mine.lo[0] & 0x7FFF7FFFu);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  if (RopePart::has()) rope.join();
   bad = __reduce_or_sync(0xffffffffu, bad);
-  if (lane == 0) s.amax[turn][warp] = top, s.rope_amax[turn][warp] = rtop, s.bad[turn][warp] = bad;
+  if (lane == 0) {
+    s.amax[turn][warp] = top;
+    s.rope_amax[turn][warp] = RopePart::has() ? rope.top : 0u;
+    s.bad[turn][warp] = bad;
+  }
   __syncthreads();
   uint32_t amax = 0, rope_amax = 0;
   bad = 0;
@@ -192,20 +322,28 @@ __device__ __forceinline__ void digest_page(DigestShared& s, const uint8_t* base
     rope_amax = max(rope_amax, s.rope_amax[turn][i]);
     bad |= s.bad[turn][i];
   }
-  const int e = digest_exponent(amax), re = digest_exponent(rope_amax);
-  const bool lat_bad = (bad & 1u) || e > kDigestExpMax, rope_bad = (bad & 2u) || re > kDigestExpMax;
-  // blocks with bit 2 set hold their halves in swapped order
-  const int pair = 16 * block + (first ^ ((block & 4) ? 8 : 0));
-  put_pair(out + 2 * pair, out + kLatent + 2 * pair, mine.hi[0], mine.lo[0], e, lat_bad);
-  if (has_rope && (lane & 6) == 0) {
-    uint8_t* at = out + 2 * kLatent + 2 * (4 * chunk + (lane >> 3));
-    put_pair(at, at + kRope, rmine.hi[0], rmine.lo[0], re, rope_bad);
+  const bool again = !(bad & 1u) && amax > 0 && amax < 0x4000u;  // the largest is below 2
+  const float unit = __uint_as_float(static_cast<uint32_t>(top_scale) << 23);  // 2^(S-127)
+  const int e = digest_exponent(__float_as_uint(f16_value(amax) * unit));
+  const bool lat_bad = (bad & 1u) || e > kDigestExpMax;
+  const float f = unit * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  uint32_t two = 0;  // bytes: the largest of the pair, the smallest of it
+  if (!lat_bad) {
+    const int h0 = __float2int_ru(f16_value(mine.hi[0] & 0xFFFFu) * f), h1 = __float2int_ru(f16_value(mine.hi[0] >> 16) * f);
+    const int l0 = __float2int_rd(f16_value(mine.lo[0] & 0xFFFFu) * f), l1 = __float2int_rd(f16_value(mine.lo[0] >> 16) * f);
+    two = (h0 & 0xFF) | (h1 & 0xFF) << 8 | (l0 & 0xFF) << 16 | static_cast<uint32_t>(l1 & 0xFF) << 24;
   }
-  if (tid >= kDigestThreads - 4) {
-    const int i = tid - (kDigestThreads - 4);
-    const uint32_t exps =
-        (lat_bad ? 255u : static_cast<uint32_t>(e + 127)) | (rope_bad ? 255u : static_cast<uint32_t>(re + 127)) << 8;
-    *reinterpret_cast<uint32_t*>(out + 2 * kOutDim + 4 * i) = i ? 0u : exps;
+  // elements (1, 3) or (5, 7) here and (0, 2) or (4, 6) with the neighbour make
+  // four in a row: this lane writes their largest, that one their smallest
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, two, 4);
+  const bool low = first & 1;
+  const uint32_t four = low ? __byte_perm(two, other, 0x7362) : __byte_perm(other, two, 0x5140);
+  const int word = (2 * (sub & 1) + (first >> 2)) ^ ((block & 4) ? 2 : 0);
+  *reinterpret_cast<uint32_t*>(out + (low ? kLatent : 0) + 32 * block + 8 * word + 4 * (first >> 1 & 1)) = four;
+  put_rope(out, rope, rope_amax, (bad & 2u) != 0, lat_bad, e);
+  if (again) {
+    __syncthreads();  // (what is written above is written over)
+    digest_any(s, base, shift, out, turn);
   }
 }
 

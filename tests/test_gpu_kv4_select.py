@@ -120,6 +120,31 @@ def test_special_values(cuda_device):
     assert got[10, 1153] == 187 and got[11, 1153] == 255
 
 
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_scales_far_apart(cuda_device, P):
+    """Values many octaves below the page's largest scale byte, and pages whose largest scale byte stands over small
+    codes or none."""
+    rng = np.random.default_rng(10 + P)
+    c = _rand_cache(rng, 9, P)
+    codes, scales = c[:, :256 * P].reshape(9, P, 16, 16), c[:, 384 * P:].reshape(9, P, 16)
+    scales[0] = rng.integers(90, 140, (P, 16))            # every octave
+    scales[1] = rng.integers(87, 168, (P, 16))
+    scales[2] = 100                                       # one block far above all others
+    scales[2, P // 2, 5] = 130
+    scales[3] = 117                                       # 13 and 14 octaves
+    scales[3, 0], scales[3, 1, ::2] = 130, 116
+    scales[4] = 120                                       # the largest scale stands over zeros
+    scales[4, 3, 7], codes[4, 3, 7] = 160, 0
+    codes[5] &= 0x99                                      # magnitudes 0 and 0.5 only, and signs
+    codes[6] = rng.choice([0, 0x88, 0x08, 0x80], codes[6].shape)  # zeros of either sign
+    codes[7] &= 0xBB                                      # at most 1.5
+    scales[8], codes[8] = rng.integers(87, 168, (P, 16)), 0
+    scales[8, 1, 2], codes[8, 1, 2, 3] = 88, 0x55         # all that is not zero lies far below
+    d = Digests(c, P, np.arange(9).reshape(1, 9), [9 * P])
+    d.run([0], [9 * P], 9 * P)
+    d.check(range(9))
+
+
 def test_what_is_out_of_range_is_left_out(cuda_device):
     rng = np.random.default_rng(2)
     P = 16
