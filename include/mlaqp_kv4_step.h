@@ -52,7 +52,8 @@ typedef enum {
  * The mean of squares is the FP32 number next to the exact one (it is summed in
  * two floats), so r and y do not depend on an order of summation; the root, its
  * reciprocal and both products are rounded to FP32 each, in this order.  Squares
- * and mean beyond FP32 (magnitudes of 2^64 and more) make r 0.
+ * and mean beyond FP32 (magnitudes of 2^64 and more) make r 0; squares below its
+ * normal range (magnitudes below 2^-63) lose bits, which matters without norm_eps.
  *
  *   latent, k_pe, their strides, cache, slots  as mlaqp_kv4_append
  *   norm_weight  BF16[512], 16-byte aligned, or NULL (norm_eps is then not used);
@@ -137,7 +138,8 @@ int mlaqp_kv4_digest(const void* cache, int64_t page_stride, int num_pages, int 
  *   A = sum over the latents of up[c]*largest[c] + down[c]*smallest[c],
  *   B' = the same over the rope elements, both exact
  *   score = fl(A) * 2^e_latent + fl(B') * 2^e_rope, in FP32, rounded to nearest
- *             (+infinity where an exponent byte is 255)
+ *             (+infinity where an exponent byte is 255, or where what lies there is
+ *             no digest and the sum no number)
  *
  * so the choice depends on no order of summation.  Only digests of full pages
  * that lie between the first and the last ones taken are read; a page out of
@@ -148,8 +150,8 @@ int mlaqp_kv4_digest(const void* cache, int64_t page_stride, int num_pages, int 
  *   workspace                   16-byte aligned device memory of
  *                               mlaqp_kv4_select_workspace() bytes for this call
  *                               alone while it runs
- * 1 <= H <= 16, 1 <= q_len <= 16, B*q_len <= 256; k >= 1, first >= 0, last >= 1,
- * first + last <= k <= sel_stride.  A sequence index or a length out of range is
+ * 1 <= H <= 16, 1 <= q_len <= 16, B*q_len <= 256; 1 <= k <= 2^20, first >= 0,
+ * last >= 1, first + last <= k <= sel_stride.  A sequence index or a length out of range is
  * reported and its rows are empty.  B = 0 launches nothing.
  */
 int mlaqp_kv4_select(const void* q, int64_t q_token_stride, int q_dtype, const void* digests, int64_t digest_stride,

@@ -232,6 +232,7 @@ int mlaqp_kv4_select(const void* q, int64_t q_token_stride, int q_dtype, const v
   if (st != MLAQP_OK) return st;
   if (k < 1 || first < 0 || last < 1 || static_cast<int64_t>(first) + last > k)
     return bad_arg("k >= 1, first >= 0, last >= 1 and first + last <= k are required");
+  if (k > MLAQP_KV4_MAX_PAGES) return host_fail(MLAQP_ERR_UNSUPPORTED, "k must be <= 2^20");
   if (sel_stride < k || sel_stride > (1ll << 31)) return bad_arg("sel_stride must be in k..2^31");
   if (B == 0) return MLAQP_OK;
   st = check_sequences(block_table, block_table_stride, num_seqs, seq_lens);

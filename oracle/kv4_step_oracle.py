@@ -93,9 +93,10 @@ def scores(q: np.ndarray, digests: np.ndarray) -> np.ndarray:
     lat = v[:, :512] @ up[:512] + v[:, 512:1024] @ down[:512]
     rope = v[:, 1024:1088] @ up[512:] + v[:, 1088:1152] @ down[512:]
     e = digests[:, 1152:1154].astype(np.int64)
-    power = np.exp2(np.minimum(e, 187) - 127.0).astype(np.float32)
+    power = np.exp2(np.minimum(e, 254) - 127.0).astype(np.float32)
+    power[e == 0] = 0.0  # (no digest has it: a float's bits without an exponent)
     s = lat.astype(np.float32) * power[:, 0] + rope.astype(np.float32) * power[:, 1]
-    s[(e == EXP_NONE).any(1)] = np.inf
+    s[(e == EXP_NONE).any(1) | np.isnan(s)] = np.inf
     return s
 
 

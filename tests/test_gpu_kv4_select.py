@@ -339,6 +339,19 @@ def test_unknown_digests_nan_queries_and_tiny_ones(cuda_device):
     s.run(4, 1, 6, 1, 1)
 
 
+@pytest.mark.parametrize("pages,k", [(300, 20), (1000, 500), (5000, 40)])
+def test_digests_that_were_never_written(cuda_device, pages, k):
+    """Any bytes: scores that are no numbers count as unknown pages do, and nothing is written beside the rows."""
+    rng = np.random.default_rng(pages)
+    d = rng.integers(0, 256, (pages, 1168), dtype=np.uint8)
+    d[::3] = 0xFF
+    d[1::3, 1152:1154] = 254  # sums of infinities of both signs
+    q_dev, q = _query(rng, 3, 16, False)
+    s = Select(d, 16, np.stack([rng.permutation(pages) for _ in range(3)]), [pages * 16] * 3, q_dev, q)
+    with np.errstate(all="ignore"):
+        s.run(3, 1, k, 1, 1, pad=5)
+
+
 def test_what_is_out_of_range(cuda_device):
     rng = np.random.default_rng(24)
     d = _rand_digests(rng, 60)

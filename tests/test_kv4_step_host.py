@@ -160,6 +160,7 @@ def _select(**kw):
     (dict(digests=None), INVALID),
     (dict(digest_stride=1160), INVALID),
     (dict(k=0), INVALID),
+    (dict(k=(1 << 20) + 1, sel_stride=1 << 21), UNSUPPORTED),
     (dict(first=-1), INVALID),
     (dict(last=0), INVALID),
     (dict(first=2, last=3), INVALID),
