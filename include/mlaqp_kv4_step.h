@@ -49,11 +49,12 @@ typedef enum {
  *              cos, sin those of pair j at positions[t], rounded once to BF16;
  *              elements stay where they are
  *
- * The mean of squares is the FP32 number next to the exact one (it is summed in
- * two floats), so r and y do not depend on an order of summation; the root, its
- * reciprocal and both products are rounded to FP32 each, in this order.  Squares
- * and mean beyond FP32 (magnitudes of 2^64 and more) make r 0; squares below its
- * normal range (magnitudes below 2^-63) lose bits, which matters without norm_eps.
+ * The sum of squares is the FP32 number next to the exact one (it is summed in two
+ * floats), so r and y do not depend on an order of summation; the root, its
+ * reciprocal and both products are rounded to FP32 each, in this order.  Where the
+ * sum is beyond FP32 (2^128; magnitudes of some 2^59.5 in all latents, or of 2^64 in
+ * one) r is 0; squares below FP32's normal range (magnitudes below 2^-63) lose bits,
+ * which matters without norm_eps.
  *
  *   latent, k_pe, their strides, cache, slots  as mlaqp_kv4_append
  *   norm_weight  BF16[512], 16-byte aligned, or NULL (norm_eps is then not used);

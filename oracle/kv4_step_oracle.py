@@ -24,7 +24,7 @@ def normalise(latent_bits: np.ndarray, weight_bits, eps: float) -> np.ndarray:
     if weight_bits is None:
         return x.astype(np.float32)
     with np.errstate(all="ignore"):
-        mean = ((x * x).sum(1, keepdims=True) / ko.LATENT).astype(np.float32)
+        mean = (x * x).sum(1, keepdims=True).astype(np.float32) / np.float32(ko.LATENT)
         r = np.float32(1.0) / np.sqrt(mean + np.float32(eps))
         return x.astype(np.float32) * r * bf16_to_f64(weight_bits).astype(np.float32)
 

@@ -174,6 +174,21 @@ def test_special_latents(cuda_device, eps):
         c.check(eps)
 
 
+def test_sums_of_squares_at_the_end_of_fp32(cuda_device):
+    c = Case(6, 0, 16, np.random.default_rng(21))
+    v = np.zeros((6, 512), dtype=np.float32)
+    v[0] = 1.25 * 2.0 ** 59     # sum 1.5625 * 2^127
+    v[1] = 1.5 * 2.0 ** 59      # sum 2.25 * 2^127: r = 0
+    v[2, 77] = 1.375 * 2.0 ** 63
+    v[3, 77] = 1.5 * 2.0 ** 63  # r = 0
+    v[4, ::2] = 1.5 * 2.0 ** 59
+    v[5] = np.where(np.arange(512) < 256, 1.25 * 2.0 ** 59, 2.0 ** 20)
+    c.latent = _bits(v)
+    c.dev["latent"] = to_device(c.latent)
+    c.run()
+    c.check()
+
+
 def test_one_buffer_for_everything_rotated_in_place(cuda_device):
     rng = np.random.default_rng(8)
     T, H, P, row = 20, 11, 32, 11 * 192 + 576 + 24
