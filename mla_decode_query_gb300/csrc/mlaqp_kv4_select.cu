@@ -50,6 +50,8 @@ constexpr int kSelectCtasPerSm = 2;
 constexpr int kScorePages = 4;                       // in flight per warp
 constexpr int kScoreLane = 20;                       // a lane's 18 pairs of up / down apart: 16-byte loads without bank conflicts
 constexpr int kQueryWords = 32 * kScoreLane;         // of a query token
+constexpr int kTokenAt = 20;                         // bits of a page's place in its sequence
+constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 constexpr int kBins = 2048, kBinsLog = 11;
 constexpr int kBinsEach = kBins / kSelectThreads;
 constexpr int kCandidates = 32;                      // keys that a warp ranks
@@ -58,6 +60,7 @@ constexpr int kFewBins = 512, kFewBinsLog = 9;
 constexpr int kHeldKeys = 2048;                      // keys and pages that stay in shared memory
 constexpr int kChooseEach = 4;                       // pages of a thread in one sweep in order
 static_assert(kRopeChunks * MLAQP_KV4_MAX_HEADS <= kSelectThreads && kBinsEach == 8 && kFewEach == 4, "threads");
+static_assert(MLAQP_KV4_MAX_PAGES <= 1 << kTokenAt && MLAQP_KV4_MAX_Q_LEN <= 1 << (31 - kTokenAt), "pages and tokens in a word");
 
 // Dynamic shared memory: this, then the queries' words.
 struct SelectShared {
@@ -290,9 +293,8 @@ struct PageBatch {
   }
 };
 
-// Keys of four pages for the query token of `words`; lane first + u holds page
-// u's exponents, negative for a page out of the pool.  Lane u < 4 gets page u's.
-__device__ __forceinline__ uint32_t score_batch(const PageBatch& batch, const uint32_t* words, int exps, int first) {
+// Sums of four pages for the query token of `words`; lane l gets page l % 4's.
+__device__ __forceinline__ int2 score_batch(const PageBatch& batch, const uint32_t* words) {
   const int lane = threadIdx.x & 31;
   const uint32_t* w = words + lane * kScoreLane;
   int a[kScorePages], r[kScorePages];
@@ -316,14 +318,16 @@ __device__ __forceinline__ uint32_t score_batch(const PageBatch& batch, const ui
     r[u] = __reduce_add_sync(0xffffffffu, dp2a(z.y, batch.rope[u], dp2a(z.x, batch.rope[u], 0, false), true));
     a[u] = __reduce_add_sync(0xffffffffu, a[u]);
   }
-  // from here on a page a lane
   const int u = lane & (kScorePages - 1);
-  const int sum = u & 2 ? (u & 1 ? a[3] : a[2]) : (u & 1 ? a[1] : a[0]);
-  const int rsum = u & 2 ? (u & 1 ? r[3] : r[2]) : (u & 1 ? r[1] : r[0]);
-  exps = __shfl_sync(0xffffffffu, exps, first + u);
+  return make_int2(u & 2 ? (u & 1 ? a[3] : a[2]) : (u & 1 ? a[1] : a[0]),
+                   u & 2 ? (u & 1 ? r[3] : r[2]) : (u & 1 ? r[1] : r[0]));
+}
+
+// Key of a page: its sums, its exponents, negative for a page out of the pool.
+__device__ __forceinline__ uint32_t key_of_sums(int2 sums, int exps) {
   const uint32_t ea = exps & 255u, er = exps >> 8 & 255u;
-  float f = __fadd_rn(__fmul_rn(static_cast<float>(sum), __uint_as_float(ea << 23)),
-                      __fmul_rn(static_cast<float>(rsum), __uint_as_float(er << 23)));
+  float f = __fadd_rn(__fmul_rn(static_cast<float>(sums.x), __uint_as_float(ea << 23)),
+                      __fmul_rn(static_cast<float>(sums.y), __uint_as_float(er << 23)));
   // (what is not a digest may give a NaN, which no key stands for)
   if (ea == 255u || er == 255u || isnan(f)) f = INFINITY;
   return exps < 0 ? 0u : score_key(f);
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     // u: addresses and exponents of eight batches at a time.  In the place of a
     // page out of the pool, and behind the last one, page 0's digest is read and
     // not used.
-    const int warps = kSelectWarps * ctas, mine = kSelectWarps * rank + warp;
+    const int warps = kSelectWarps * ctas, mine = ctas * warp + rank;  // a last, incomplete round is shared by all CTAs
     const int batches = ((count + kScorePages - 1) / kScorePages - mine + warps - 1) / warps;
     auto entry = [&](int k0) {
       const int n = kScorePages * (warps * (k0 + lane / kScorePages) + mine) + lane % kScorePages;
@@ -690,6 +694,24 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     }
     if (held && rank < p.q_len)  // for the choice
       for (int j = tid; j < pages; j += kSelectThreads) copy_4(smem_u32(&s.pages[j]), row + j);
+    // Sums wait in the lanes, four for a batch and query token, until all lanes
+    // have some: a warp makes 32 keys at once.
+    int2 sums = make_int2(0, 0);
+    int sums_exps = 0, filled = 0;
+    uint32_t sums_of = kNoPage;  // page between the fixed ones, token << kTokenAt
+    const int ctas_log = 31 - __clz(ctas);
+    auto put_keys = [&]() {
+      if (sums_of != kNoPage) {
+        const uint32_t key = key_of_sums(sums, sums_exps);
+        const int n = sums_of & ((1u << kTokenAt) - 1u), t = sums_of >> kTokenAt;
+        if (!held)
+          p.keys[(m0 + t) * p.width + p.first + n] = key;
+        else
+          st_cluster(smem_u32(&s.keys[(t >> ctas_log) * room + n]), t & (ctas - 1), key);
+      }
+      sums_of = kNoPage;
+      filled = 0;
+    };
     // While a batch is scored the one behind it is under way, and its entries
     // and exponents long before.
     auto round = [&](const PageBatch& now, PageBatch& then, int k) {
@@ -699,16 +721,17 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
         next_exps = exps_of(next, next_digest);
       }
       if (k + 1 < batches) then.load(k % 8 < 7 ? digest : next_digest, (k + 1) % 8 * kScorePages);
-      const int n = kScorePages * (warps * k + mine) + lane;
+      const int n = kScorePages * (warps * k + mine) + lane % kScorePages;
+      const int e = __shfl_sync(0xffffffffu, exps, k % 8 * kScorePages + lane % kScorePages);
 #pragma unroll 1
       for (int t = 0; t < p.q_len; ++t) {
-        const uint32_t key = score_batch(now, words + t * kQueryWords, exps, k % 8 * kScorePages);
-        if (lane < kScorePages && n < count) {
-          if (!held)
-            p.keys[(m0 + t) * p.width + p.first + n] = key;
-          else
-            st_cluster(smem_u32(&s.keys[t / ctas * room + n]), t % ctas, key);
+        const int2 sum = score_batch(now, words + t * kQueryWords);
+        if (lane / kScorePages == filled) {
+          sums = sum;
+          sums_exps = e;
+          sums_of = n < count ? static_cast<uint32_t>(n) | static_cast<uint32_t>(t) << kTokenAt : kNoPage;
         }
+        if (++filled == 32 / kScorePages) put_keys();
       }
       if (k % 8 == 7) digest = next_digest, exps = next_exps;
     };
@@ -717,6 +740,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
       round(even, odd, k);
       if (k + 1 < batches) round(odd, even, k + 1);
     }
+    put_keys();
     copy_wait();
     if (ctas > 1) cluster_arrive();
   }
