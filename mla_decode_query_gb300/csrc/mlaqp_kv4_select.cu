@@ -21,14 +21,15 @@
 // scans for itself, leaves a few keys to rank, and a prefix sum puts the pages in
 // order; more keys, or more of them in one place, take rounds of 2048 places.
 // One launch: a score kernel that cut all pages into equal stretches, with a
-// choice kernel behind it, took 21.7 us instead of 11.1.
+// choice kernel behind it, took 21.7 us instead of 10.5.
 //
 // What bounds it.  64 sequences of 16000 to 32768 tokens, pages of 64, H = 16:
-// 11.1 us, 28 MB of digests; on an SM a page costs some 25 cycles (18 dp2a at
-// two a cycle, 4 sums over the warp at half of one), 0.65 us pass until the
-// lengths are there, 2.2 with the queries, 3.5 to 5 in the scores, 1 waiting
-// for the longest of the cluster and 2.3 in the choice.  One sequence of 1024
-// pages: 7.0 us; 16 of up to 569 with 4 query tokens: 13.3.
+// 10.5 us, 28 MB of digests; 0.65 us pass until the lengths are there, 2.2 with
+// the queries, 2.8 to 3.5 in the scores, 1 waiting for the longest of the cluster
+// and 1.9 in the choice.  On an SM four pages cost a query token some 70 cycles
+// (72 dp2a at two a cycle, 8 sums over the warp at half of one).  One sequence of
+// 1024 pages: 6.7 us; 16 of up to 569 with 4 query tokens: 11.5, of which the
+// longest sequence scores for 4.6.
 
 #include <atomic>
 
@@ -238,7 +239,9 @@ __device__ __forceinline__ void query_words(SelectShared& s, const QueryPart& q,
   __syncthreads();
   // Words w < 16 of lane l: pairs of up for the latents 16l.., of down for the
   // same; 16 and 17: of up (l < 16) or down for four rope elements.  Neither half
-  // of a sum overflows: 16 heads * 2047.
+  // of a sum overflows: 16 heads * 2047.  Two warps see to the rope elements, the
+  // others to the latents.
+  constexpr int kLatentThreads = kSelectThreads - 64;
   auto word = [&](int l, int w, uint2 sum, bool high) {
     const uint32_t two = high ? __byte_perm(sum.x, sum.y, 0x7632) : __vneg2(__byte_perm(sum.x, sum.y, 0x5410));
     if (ctas == 0) {
@@ -249,7 +252,7 @@ __device__ __forceinline__ void query_words(SelectShared& s, const QueryPart& q,
     }
   };
 #pragma unroll
-  for (int i = tid; i < 32 * 16; i += kSelectThreads) {
+  for (int i = tid; i < 32 * 16 && tid < kLatentThreads; i += kLatentThreads) {
     const int l = i / 16, w = i % 16;
     uint2 sum = make_uint2(0, 0);
 #pragma unroll
@@ -259,8 +262,8 @@ __device__ __forceinline__ void query_words(SelectShared& s, const QueryPart& q,
     }
     word(l, w, sum, w < 8);
   }
-  if (tid < 64) {
-    const int l = tid / 2, w = tid % 2;
+  if (tid >= kLatentThreads) {
+    const int l = (tid - kLatentThreads) / 2, w = tid % 2;
     uint2 sum = make_uint2(0, 0);
 #pragma unroll
     for (int a = 0; a < MLAQP_KV4_MAX_HEADS; ++a) {
@@ -768,9 +771,9 @@ const void* select_kernel(bool e4m3) {
 }
 
 // CTAs of a sequence.  As many as find room at two an SM, up to 8 (64 sequences
-// of up to 512 pages: 11.1 us with 4, 15.2 with 2, 17.3 with 8; 16 sequences of
-// up to 569 pages, 4 query tokens: 13.3 with 8, 16.0 with 4, 18.5 with 16), 16
-// where those are no more than the SMs (one sequence of 1024 pages: 6.9 us, 8.4
+// of up to 512 pages: 10.5 us with 4, 14.0 with 2, 16.3 with 8; 16 sequences of
+// up to 569 pages, 4 query tokens: 11.5 with 8, 13.5 with 4, 16.5 with 16), 16
+// where those are no more than the SMs (one sequence of 1024 pages: 6.7 us, 8.0
 // with 8); no more than have a batch for each warp.
 constexpr int kSelectCluster = 8, kSelectWideCluster = 16;
 int select_cluster(int B, int64_t width, int sm_count, bool wide) {
