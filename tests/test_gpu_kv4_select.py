@@ -408,6 +408,25 @@ def test_streams_and_graph_replay(cuda_device):
     assert torch.equal(outs[0][0], want) and torch.equal(outs[0][1], want_lens[:9])
 
 
+def test_offsets_beyond_32_bits(cuda_device):
+    rng = np.random.default_rng(26)
+    P, pages, far = 16, 70, 1 << 26
+    c = _rand_cache(rng, pages, P)
+    big = torch.empty(2, pages, far, dtype=torch.uint8, device="cuda")
+    table = rng.permutation(pages)[None]
+    d = Digests(c, P, table, [pages * P])
+    d.cache, d.out, d.stride = big[0, :, :400 * P], big[1, :, :1168], far
+    d.cache.copy_(torch.from_numpy(c))
+    d.run([0], [pages * P], pages * P)
+    digests = d.out.cpu().numpy()
+    for p in range(pages):
+        np.testing.assert_array_equal(digests[p], so.digest(ko.read_tokens(c, P, range(p * P, p * P + P))))
+    q_dev, q = _query(rng, 1, 16, False)
+    s = Select(digests, P, table, [pages * P], q_dev, q)
+    s.d = d.out
+    s.run(1, 1, 9, 1, 1)
+
+
 # --------------------------------------------------------------------------
 # Together: decode steps of a layer with a cache that grows
 # --------------------------------------------------------------------------
