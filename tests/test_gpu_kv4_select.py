@@ -145,6 +145,30 @@ def test_scales_far_apart(cuda_device, P):
     d.check(range(9))
 
 
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+def test_few_and_many_pages(cuda_device, P, few):
+    """The same pages in a call that can fill a few pages and in one that can fill thousands."""
+    rng = np.random.default_rng(40 + P)
+    pages = 48
+    c = _rand_cache(rng, pages, P)
+    codes, scales = c[:, :256 * P].reshape(pages, P, 16, 16), c[:, 384 * P:].reshape(pages, P, 16)
+    rope = c[:, 256 * P:384 * P].view(np.uint16).reshape(pages, P, 64)
+    for j in range(0, 30, 6):
+        t, block = rng.integers(0, P), rng.integers(0, 16)
+        scales[j, t, block] = 255                                   # a NaN block
+        rope[j + 1, t, rng.integers(0, 64)] = (0x7F80, 0xFF80, 0x7FC1)[j % 3]
+        scales[j + 2] = rng.integers(87, 168, (P, 16))
+        scales[j + 3, t, block], codes[j + 3, t, block] = 165, 0     # the largest scale stands over zeros
+        codes[j + 4] = 0
+        codes[j + 4, t, block, 3] = 0x70                            # one value in the page
+        rope[j + 5] = 0
+        rope[j + 5, t, j] = 0xBF80
+    d = Digests(c, P, np.arange(pages).reshape(1, pages), [pages * P])
+    d.run([0], [pages * P], pages * P if few else 5000 * P)
+    d.check(range(pages))
+
+
 def test_what_is_out_of_range_is_left_out(cuda_device):
     rng = np.random.default_rng(2)
     P = 16
