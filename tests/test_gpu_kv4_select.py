@@ -199,6 +199,19 @@ def test_shared_pages_many_sequences_and_another_stream(cuda_device):
     d.check(sorted(set(table.reshape(-1))))
 
 
+def test_a_list_longer_than_is_looked_up_at_once(cuda_device):
+    rng = np.random.default_rng(4)
+    P, seqs = 16, 50000
+    c = _rand_cache(rng, 40, P)
+    table = rng.integers(0, 38, (seqs, 1))
+    table[0], table[-1] = 38, 39
+    new = np.ones(seqs, dtype=int)
+    new[1:-1:3] = 0
+    d = Digests(c, P, table, [P] * seqs)
+    d.run(np.arange(seqs), new, P)
+    d.check(range(40))
+
+
 # --------------------------------------------------------------------------
 # Selection
 # --------------------------------------------------------------------------
