@@ -14,7 +14,7 @@
  *
  *   append_rope -> digest -> mlaqp_run (q) -> select -> mlaqp_kv4_attend
  *
- * on k pages a query token instead of all: 43 us for the last two instead of 152
+ * on k pages a query token instead of all: 40 us for the last two instead of 149
  * for 64 sequences of 16K to 32K tokens at k = 32 pages of 64, and nothing gained
  * up to some 3K tokens a sequence.  Caches, slots, block tables and
  * the device status word are those of mlaqp_kv4.h, and so are the conventions:

@@ -1019,14 +1019,20 @@ __global__ void __launch_bounds__(kAttThreads, 1) mlaqp_kv4_attend_kernel(const 
 // order, so that the result does not depend on which CTA was first.  A job is
 // a row, or 128 of its 512 latents where there are few rows; the CTA's eight
 // warps take the pieces in turn.  Bound by latency: what the attention kernel
-// noted of the row groups, then M, l and the first pieces' sums at once.  Two
-// CTAs per SM: 32 sequences of up to 8191 tokens take 27.3 us (both kernels),
-// with one 29.0, with three 29.8, with four 32.7; 16 of up to 4100 tokens, 4
-// query tokens, 27.1, 29.9, 30.7 and 33.8; 64 of up to 32768 152, 156, 155
-// and 159.
+// noted of the row groups, then M, l and the first pieces' sums at once.
+// Where there are more rows than a quarter of the CTAs and none has more than
+// eight pieces, 128 latents of a row are a warp's job, without a barrier: 64
+// sequences of up to 32768 tokens 152 -> 149 us (both kernels), 16 of up to 4100
+// tokens with 4 query tokens 27.8 -> 25.1, 64 of 2048 30.5 -> 27.4, 256 of up to
+// 4000 76.7 -> 70.5.  For fewer rows it took 0.4 us more, and for both kinds in a
+// call as much again.  Two CTAs per SM, without that: 32 sequences of up to 8191
+// tokens take 27.3 us, with one 29.0, with three 29.8, with four 32.7; 16 of up to
+// 4100 tokens, 4 query tokens, 27.1, 29.9, 30.7 and 33.8; 64 of up to 32768 152,
+// 156, 155 and 159.
 // --------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtasPerSm = 2;
+constexpr int kJoinFew = 8;  // pieces that a warp joins
 
 struct JoinShared {
   AttGroup group[kAttMaxSeqs];
@@ -1098,6 +1104,42 @@ __device__ __forceinline__ float join_sums(JoinShared& j, int np, int r, int col
   return top;
 }
 
+// 128 latents of a row of at most kJoinFew pieces by a warp, without a barrier: the
+// same sums in the same order as above.
+template <class Slot>
+__device__ __forceinline__ void join_few(const Kv4AttendParams& p, int R, int np, int r, int col, int64_t q, int h,
+                                         const Slot& slot) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f;
+  if (lane < np) {
+    m = slot(lane)[R * kLatent + r];
+    l = slot(lane)[R * kLatent + R + r];
+  }
+  float4 o[kJoinFew];
+#pragma unroll
+  for (int c = 0; c < kJoinFew; ++c)
+    if (c < np) o[c] = *reinterpret_cast<const float4*>(slot(c) + r * kLatent + col + 4 * lane);
+  const float top = warp_max(m);
+  const float weight = m == -INFINITY ? 0.f : ex2(m - top);
+  const float part = __fmul_rn(l, weight);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < kJoinFew; ++c) {
+    if (c >= np) break;
+    const float f = __shfl_sync(0xffffffffu, weight, c);
+    sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, part, c));
+    x.x = __fadd_rn(x.x, __fmul_rn(o[c].x, f)), x.y = __fadd_rn(x.y, __fmul_rn(o[c].y, f));
+    x.z = __fadd_rn(x.z, __fmul_rn(o[c].z, f)), x.w = __fadd_rn(x.w, __fmul_rn(o[c].w, f));
+  }
+  const bool none = sum == 0.f;
+  const float inv = 1.f / sum;
+  *reinterpret_cast<uint2*>(p.x + q * p.x_ts + h * kLatent + col + 4 * lane) =
+      none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(x.y * inv, x.x * inv), pack_bf16x2(x.w * inv, x.z * inv));
+  if (lane == 0 && col == 0 && p.lse)
+    p.lse[q * p.H + h] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 template <int R>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     mlaqp_kv4_join_kernel(const __grid_constant__ Kv4AttendParams p) {
@@ -1122,7 +1164,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   const bool split = mine.pieces > 1;
   const unsigned who = __ballot_sync(0xffffffffu, split);
   if (lane == 0) j.split_warp[warp] = __popc(who);
-  __syncthreads();
+  const bool many = __syncthreads_or(mine.pieces > kJoinFew);
   int rank = __popc(who & ((1u << lane) - 1u)), n_split = 0;
   for (int w = 0; w < 8; ++w) {
     if (w < warp) rank += j.split_warp[w];
@@ -1131,13 +1173,24 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   if (split) j.split[rank] = tid;
   __syncthreads();
   const int cuts = n_split * per_group * 4 <= static_cast<int>(gridDim.x) ? 4 : 1;
+  const float* const base = reinterpret_cast<const float*>(p.ws + kAttGroupBytes);
+  if (cuts == 1 && !many) {
+    const int rows4 = per_group * 4, step = static_cast<int>(gridDim.x) * (kJoinThreads / 32);
+    for (int job = blockIdx.x + static_cast<int>(gridDim.x) * warp; job < n_split * rows4; job += step) {
+      const int v = j.split[job / rows4], r = job / 4 % per_group, rr = (v % groups) * R + r;
+      if (rr >= rows) continue;
+      const int at = j.group[v].slot;
+      join_few(p, R, j.group[v].pieces, r, job % 4 * 128, static_cast<int64_t>(v / groups) * p.q_len + rr / p.H, rr % p.H,
+               [&](int c) { return base + (c == 0 ? at : (at & ~1) + 2 * c) * att_slot_floats<R>(); });
+    }
+    return;
+  }
   const int jobs = n_split * per_group * cuts;
   for (int job = blockIdx.x; job < jobs; job += gridDim.x) {
     const int v = j.split[job / (per_group * cuts)], r = job / cuts % per_group, col = job % cuts * 128;
     const int rr = (v % groups) * R + r;
     if (rr >= rows) continue;
     const int np = j.group[v].pieces, at = j.group[v].slot;
-    const float* const base = reinterpret_cast<const float*>(p.ws + kAttGroupBytes);
     auto slot = [&](int c) { return base + (c == 0 ? at : (at & ~1) + 2 * c) * att_slot_floats<R>(); };
     const float top = cuts == 1 ? join_sums<R, 4>(j, np, r, 0, slot) : join_sums<R, 1>(j, np, r, col, slot);
     __syncthreads();

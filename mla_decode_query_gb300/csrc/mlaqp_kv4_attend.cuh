@@ -55,7 +55,7 @@
 // grown by more than 2^3.
 //
 // What bounds it (GB300, 152 SMs, H = 16).  64 sequences of 16000 to 32768
-// tokens, E4M3 queries: 152 us, 4.20 TB/s of cache and rows, 62% of the copy
+// tokens, E4M3 queries: 149 us, 4.29 TB/s of cache and rows, 63% of the copy
 // rate of 6.79 TB/s.  A tile takes an SM 3000 to 3300 cycles; its bytes alone
 // would take 2230, its 36 MMAs 2155 (some 60 each whatever N is).  What is
 // left is the way of a tile through the pipeline: scores 2500 cycles beside
