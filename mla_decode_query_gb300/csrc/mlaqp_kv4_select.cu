@@ -771,9 +771,9 @@ const void* select_kernel(bool e4m3) {
 }
 
 // CTAs of a sequence.  As many as find room at two an SM, up to 8 (64 sequences
-// of up to 512 pages: 10.5 us with 4, 14.0 with 2, 16.3 with 8; 16 sequences of
-// up to 569 pages, 4 query tokens: 11.5 with 8, 13.5 with 4, 16.5 with 16), 16
-// where those are no more than the SMs (one sequence of 1024 pages: 6.7 us, 8.0
+// of up to 512 pages: 10.7 us with 4, 14.0 with 2, 16.3 with 8; 16 sequences of
+// up to 569 pages, 4 query tokens: 11.8 with 8, 13.5 with 4, 16.5 with 16), 16
+// where those are no more than the SMs (one sequence of 1024 pages: 6.6 us, 8.0
 // with 8); no more than have a batch for each warp.
 constexpr int kSelectCluster = 8, kSelectWideCluster = 16;
 int select_cluster(int B, int64_t width, int sm_count, bool wide) {
