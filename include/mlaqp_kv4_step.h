@@ -103,7 +103,9 @@ int mlaqp_kv4_append_rope(const void* latent, int64_t latent_token_stride, const
 /*
  * Digests of the pages of one layer that have filled up: for i < n, those of
  * sequence s = seqs[i] whose last token is among its last new_tokens[i] ones
- * (0 <= new_tokens[i] <= max_new; more than the sequence has: all of them).
+ * (0 <= new_tokens[i] <= max_new; more than the sequence has: all of them).  The
+ * call looks up n * min(ceil(max_new/page_size), block_table_stride, num_pages)
+ * table entries, whatever new_tokens says.
  * Call it behind mlaqp_kv4_append with the lists given to mlaqp_kv4_extend,
  * and for every token a page's contents were written anew otherwise (a page
  * copied or moved by mlaqp_kv4_compact or mlaqp_kv4_copy_pages; the pages that

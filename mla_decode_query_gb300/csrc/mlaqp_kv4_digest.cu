@@ -28,6 +28,8 @@
 // With a warp 64 latents of all tokens instead of all of some, and the maxima joined
 // within warps: 12.5 and 3.2 us.  A warp a page: 10.6 and 3.1.
 
+#include <algorithm>
+
 #include "mlaqp_dispatch.h"
 #include "mlaqp_kv4.cuh"
 #include "mlaqp_kv4_launch.h"
@@ -299,8 +301,8 @@ __device__ __forceinline__ void digest_page(DigestShared<Warps>& s, const uint8_
     st_u128(out + 2 * kOutDim, make_uint4(byte | (bad ? 255u : static_cast<uint32_t>(e + 127)) << 8, 0u, 0u, 0u));
 }
 
-// The page of a job (an item of the list, and one of the pages that so many new
-// tokens can fill), -1: none.
+// The page of a job (an item of the list, and one of the `per` pages that it may
+// have filled), -1: none.
 __device__ __forceinline__ int digest_job(const Kv4DigestParams& p, int64_t job, int per) {
   const int shift = p.cache.shift;
   const int i = static_cast<int>(job / per), j = static_cast<int>(job % per);
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(32 * Warps, kDigestWarpsPerSm / Warps)
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int per = ((p.max_new - 1) >> p.cache.shift) + 1;  // pages that max_new tokens can fill
+  const int per = p.per;
   const int64_t jobs = static_cast<int64_t>(p.n) * per, ctas = gridDim.x;
   // The lookups are three loads one after the other: a lane a job, for 32 at once.
   for (int64_t j0 = blockIdx.x; j0 < jobs; j0 += 32 * ctas) {
@@ -356,9 +358,13 @@ const void* digest_kernel(int warps) {
 
 // Four warps a page while all CTAs find room at once, two beyond (64 tokens a page,
 // 100 pages: 3.8 us, 4.1 with two; 600: 5.9, 6.7; 1024: 9.8, 8.5; 6000: 45, 40).
-cudaError_t kv4_digest(const Kv4DigestParams& p, int sm_count, cudaStream_t stream) {
-  void* args[1] = {const_cast<Kv4DigestParams*>(&p)};
-  const int64_t jobs = static_cast<int64_t>(p.n) * (((p.max_new - 1) >> p.cache.shift) + 1);
+cudaError_t kv4_digest(const Kv4DigestParams& params, int sm_count, cudaStream_t stream) {
+  Kv4DigestParams p = params;
+  void* args[1] = {&p};
+  // as many as max_new tokens can fill, as a row holds and as there are
+  const int64_t most_full = std::min<int64_t>(p.table_stride, p.cache.num_pages);
+  p.per = static_cast<int>(std::min<int64_t>(((p.max_new - 1) >> p.cache.shift) + 1, most_full));
+  const int64_t jobs = static_cast<int64_t>(p.n) * p.per;
   const int warps = jobs * 4 <= static_cast<int64_t>(kDigestWarpsPerSm) * sm_count ? 4 : 2;
   const int64_t most = static_cast<int64_t>(kDigestWarpsPerSm / warps) * sm_count;
   return kv4_launch(digest_kernel(warps), static_cast<unsigned>(jobs < most ? jobs : most), 32 * warps, 0, stream, args);

@@ -83,6 +83,7 @@ struct Kv4DigestParams {
   const int32_t* seqs;
   const int32_t* new_tokens;
   int n, max_new;
+  int per;                 // pages of an item that are looked at (set by kv4_digest)
 };
 cudaError_t kv4_digest(const Kv4DigestParams& p, int sm_count, cudaStream_t stream);
 cudaError_t kv4_digest_setup();
