@@ -82,7 +82,6 @@ inline int check_list(const int32_t* list, int n, const char* what) {
 }
 
 // Which groups of kernels are ready, by device.
-constexpr int kMaxDevices = 64;
 template <int Groups>
 struct ReadyGroups {
   std::atomic<bool> ready[kMaxDevices][Groups];

@@ -7,6 +7,8 @@
 
 namespace mlaqp {
 
+constexpr int kMaxDevices = 64;  // that a process can use
+
 // Launch with programmatic dependent launch: every kernel of the 4-bit cache
 // waits for the previous one before it touches memory.
 inline cudaError_t kv4_launch(const void* fn, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,

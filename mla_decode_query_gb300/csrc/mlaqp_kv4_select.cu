@@ -784,8 +784,8 @@ int select_cluster(int B, int64_t width, int sm_count, bool wide) {
   return n;
 }
 
-// Whether the device takes clusters of 16.
-std::atomic<bool> g_wide{false};
+// Whether a device has room for clusters of 16 of either kernel (BF16, E4M3 queries).
+std::atomic<bool> g_wide[kMaxDevices][2];
 
 constexpr size_t select_bytes(int q_len) { return kWordsAt + sizeof(uint32_t) * kQueryWords * static_cast<size_t>(q_len); }
 
@@ -793,16 +793,21 @@ constexpr size_t select_bytes(int q_len) { return kWordsAt + sizeof(uint32_t) * 
 
 cudaError_t kv4_select(const Kv4SelectParams& params, bool q_e4m3, int sm_count, cudaStream_t stream) {
   Kv4SelectParams p = params;
-  p.cluster = select_cluster(p.B, p.width, sm_count, g_wide.load(std::memory_order_relaxed));
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  p.cluster = select_cluster(p.B, p.width, sm_count, g_wide[device][q_e4m3].load(std::memory_order_relaxed));
   void* args[1] = {&p};
   return kv4_launch(select_kernel(q_e4m3), static_cast<unsigned>(p.B * p.cluster), kSelectThreads, select_bytes(p.q_len),
                     stream, args, static_cast<unsigned>(p.cluster));
 }
 
 cudaError_t kv4_select_setup() {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   cudaFuncAttributes a;
-  cudaError_t e = cudaSuccess;
-  for (const void* k : {select_kernel(false), select_kernel(true)}) {
+  for (bool e4m3 : {false, true}) {
+    const void* k = select_kernel(e4m3);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(select_bytes(MLAQP_KV4_MAX_Q_LEN)));
@@ -820,10 +825,12 @@ cudaError_t kv4_select_setup() {
   cfg.dynamicSmemBytes = select_bytes(MLAQP_KV4_MAX_Q_LEN);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int room = 0;
-  const cudaError_t asked = cudaOccupancyMaxActiveClusters(&room, select_kernel(false), &cfg);
-  if (asked != cudaSuccess) cudaGetLastError();  // then not
-  g_wide.store(asked == cudaSuccess && room > 0, std::memory_order_relaxed);
+  for (bool e4m3 : {false, true}) {
+    int room = 0;
+    const cudaError_t asked = cudaOccupancyMaxActiveClusters(&room, select_kernel(e4m3), &cfg);
+    if (asked != cudaSuccess) cudaGetLastError();  // then not
+    g_wide[device][e4m3].store(asked == cudaSuccess && room > 0, std::memory_order_relaxed);
+  }
   return cudaSuccess;
 }
 

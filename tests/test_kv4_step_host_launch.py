@@ -134,3 +134,38 @@ def _digest(lib, n, max_new, table_stride, num_pages, page_size=16):
 def test_digest_looks_up_no_more_pages_than_there_can_be(lib, n, max_new, table_stride, num_pages, jobs):
     # so few that four warps a page find room at once: a CTA each
     assert _digest(lib, n, max_new, table_stride, num_pages) == (jobs, 128)
+
+
+def _select(lib, e4m3=0, B=1, table_stride=8192):
+    st = lib.mlaqp_kv4_select(A, 576 * 16, e4m3, 1 << 40, 1168, 8192, 16, 2 * A, table_stride, 4, 3 * A, None, B, 1, 16, 4, 1, 1,
+                              4 * A, 4, 5 * A, 6 * A, 1 << 20, None)
+    assert st == mq.MLAQP_OK
+    assert _int(lib, "grid").value == B * _int(lib, "cluster").value
+    return _int(lib, "cluster").value
+
+
+def _rooms(lib, *rooms):
+    at = (ctypes.c_int * 4).in_dll(lib, "room")
+    at[:] = [n for device in rooms for n in device]
+
+
+@pytest.mark.parametrize("order", [(0, 1), (1, 0)])
+def test_wide_clusters_on_the_devices_that_have_room(lib, order):
+    _rooms(lib, (1, 1), (0, 0))
+    for device in order:
+        assert lib.mlaqp_kv4_step_prewarm(device) == mq.MLAQP_OK
+    for device in (0, 1, 0):
+        _int(lib, "device").value = device
+        assert _select(lib) == (16, 8)[device]
+
+
+def test_wide_clusters_of_the_kernels_that_have_room(lib):
+    _rooms(lib, (1, 0), (0, 1))
+    for device in (0, 1):
+        _int(lib, "device").value = device
+        assert (_select(lib, 0), _select(lib, 1)) == ((16, 8), (8, 16))[device]
+
+
+@pytest.mark.parametrize("B,table_stride,cluster", [(1, 8192, 16), (1, 1024, 16), (1, 512, 16), (1, 256, 8), (1, 100, 4), (1, 32, 1)])
+def test_clusters_follow_the_table(lib, B, table_stride, cluster):
+    assert _select(lib, B=B, table_stride=table_stride) == cluster
