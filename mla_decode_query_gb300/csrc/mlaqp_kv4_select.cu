@@ -91,10 +91,20 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
   return r;
 }
-// (nothing but that this CTA runs)
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The .aligned forms want a warp's threads together, and loops and branches by
+// thread come before them.  (Relaxed: nothing but that this CTA runs.)
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;");
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // A word of shared memory of the cluster's CTA `rank`, at this CTA's address.
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t rank, uint32_t v) {
   asm volatile(
