@@ -155,6 +155,8 @@ int mlaqp_kv4_digest(const void* cache, int64_t page_stride, int num_pages, int 
  *   workspace                   16-byte aligned device memory of
  *                               mlaqp_kv4_select_workspace() bytes for this call
  *                               alone while it runs
+ * sel_table, sel_lens and workspace may overlap neither one another nor an input (of
+ * a table's row: its first min(block_table_stride, num_pages) entries).
  * 1 <= H <= 16, 1 <= q_len <= 16, B*q_len <= 256; 1 <= k <= 2^20, first >= 0,
  * last >= 1, first + last <= k <= sel_stride.  A sequence index or a length out of range is
  * reported and its rows are empty.  B = 0 launches nothing.

@@ -75,6 +75,12 @@ inline Range cache_span(const Kv4Cache& c) {
                           (static_cast<uint64_t>(MLAQP_KV4_TOKEN_BYTES) << c.shift));
 }
 
+// What is read of a block table: no more of a row than a sequence can have pages.
+inline Range table_span(const int32_t* block_table, int64_t stride, int num_seqs, int num_pages) {
+  const uint64_t row = static_cast<uint64_t>(stride < num_pages ? stride : num_pages);
+  return span(block_table, 4 * (static_cast<uint64_t>(num_seqs - 1) * static_cast<uint64_t>(stride) + row));
+}
+
 inline int check_list(const int32_t* list, int n, const char* what) {
   if (n < 0) return bad_arg("n must be >= 0");
   if (n > 0 && (!list || !aligned(list, 4))) return bad_arg(std::string(what) + " must be a 4-byte aligned list");

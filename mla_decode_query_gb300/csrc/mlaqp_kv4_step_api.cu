@@ -25,6 +25,7 @@ using mlaqp::overlaps;
 using mlaqp::page_shift;
 using mlaqp::Range;
 using mlaqp::span;
+using mlaqp::table_span;
 
 enum Group { kRopeGroup, kDigestGroup, kSelectGroup, kGroups };
 mlaqp::ReadyGroups<kGroups> g_ready;
@@ -75,9 +76,6 @@ int check_digests(const void* digests, int64_t stride) {
 
 Range digest_span(const void* digests, int64_t stride, int num_pages) {
   return span(digests, static_cast<uint64_t>(stride) * (num_pages - 1) + MLAQP_KV4_DIGEST_BYTES);
-}
-Range table_span(const int32_t* block_table, int64_t stride, int num_seqs) {
-  return span(block_table, 4ull * ((num_seqs - 1) * static_cast<uint64_t>(stride) + 1));
 }
 
 int check_select_sizes(int B, int q_len) {
@@ -188,7 +186,7 @@ int mlaqp_kv4_digest(const void* cache, int64_t page_stride, int num_pages, int 
   if (max_new < 1) return bad_arg("max_new must be >= 1");
   if (n == 0) return MLAQP_OK;
   const Range d = digest_span(digests, digest_stride, num_pages);
-  const Range ins[5] = {cache_span(p.cache), table_span(block_table, block_table_stride, num_seqs),
+  const Range ins[5] = {cache_span(p.cache), table_span(block_table, block_table_stride, num_seqs, num_pages),
                         span(seq_lens, 4ull * num_seqs), span(seqs, 4ull * n), span(new_tokens, 4ull * n)};
   for (const Range& r : ins)
     if (overlaps(d, r)) return bad_arg("digests overlap an input");
@@ -252,8 +250,8 @@ int mlaqp_kv4_select(const void* q, int64_t q_token_stride, int q_dtype, const v
   const Range outs[3] = {span(sel_table, 4 * ((M - 1) * static_cast<uint64_t>(sel_stride) + k)), span(sel_lens, 4 * M),
                          span(workspace, static_cast<uint64_t>(workspace_bytes))};
   const Range ins[5] = {span(q, eb * ((M - 1) * static_cast<uint64_t>(q_token_stride) + 576ull * H)),
-                        digest_span(digests, digest_stride, num_pages), table_span(block_table, block_table_stride, num_seqs),
-                        span(seq_lens, 4ull * num_seqs), span(seqs, seqs ? 4ull * B : 0)};
+                        digest_span(digests, digest_stride, num_pages),
+                        table_span(block_table, block_table_stride, num_seqs, num_pages), span(seq_lens, 4ull * num_seqs), span(seqs, seqs ? 4ull * B : 0)};
   for (int i = 0; i < 3; ++i) {
     for (const Range& r : ins)
       if (overlaps(outs[i], r)) return bad_arg("sel_table, sel_lens or workspace overlaps an input");
