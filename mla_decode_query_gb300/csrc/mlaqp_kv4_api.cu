@@ -179,7 +179,7 @@ int attend_impl(const void* q, int64_t q_token_stride, int q_dtype, const float*
                          span(workspace, workspace && workspace_bytes > 0 ? static_cast<uint64_t>(workspace_bytes) : 0)};
   const Range ins[6] = {span(q, static_cast<uint64_t>(eb) * ((M - 1) * static_cast<uint64_t>(q_token_stride) + 576ull * H)),
                         cache_span(p.cache),
-                        span(block_table, 4ull * ((num_seqs - 1) * static_cast<uint64_t>(block_table_stride) + 1)),
+                        mlaqp::table_span(block_table, block_table_stride, num_seqs, num_pages),
                         span(seq_lens, 4ull * num_seqs),
                         span(seqs, seqs ? 4ull * B : 0),
                         span(q_scale, q_scale ? 4 : 0)};

@@ -50,3 +50,27 @@ def test_behind_the_last_row_is_free(built_library):
     # a sequence has no more pages than there are: entries beyond are not read, however wide the row
     assert _select(num_pages=8, block_table_stride=1 << 20, sel_table=2 * A + 4 * 8) in NO_DEVICE
     assert _digest(num_pages=8, block_table_stride=1 << 20, digests=2 * A + 4 * 8) in NO_DEVICE
+
+
+def _attend(**kw):
+    a = dict(q=A, q_token_stride=576 * 16, q_dtype="bf16", q_scale=None, cache=8 * A, page_stride=6400, num_pages=64, page_size=16,
+             block_table=2 * A, block_table_stride=WIDTH, num_seqs=1, seq_lens=3 * A, seqs=None, B=1, q_len=1, H=16, softmax_scale=0.07,
+             x=4 * A, x_token_stride=512 * 16, lse=5 * A, workspace=32 * A, workspace_bytes=1 << 24, stream=0)
+    a.update(kw)
+    return mq.mlaqp_kv4_attend(**a)
+
+
+@pytest.mark.parametrize("num_seqs", [1, 3])
+@pytest.mark.parametrize("name,entry", [("x", 4), ("x", WIDTH - 4), ("lse", 1), ("lse", WIDTH - 1), ("workspace", 4)])
+def test_attend_refuses_outputs_in_the_last_row(built_library, num_seqs, name, entry):
+    at = 2 * A + 4 * (WIDTH * (num_seqs - 1) + entry)
+    assert _attend(num_seqs=num_seqs, **{name: at}) == INVALID
+    assert "overlaps an input" in mq.mlaqp_last_error()
+
+
+def test_attend_may_write_behind_the_last_row(built_library):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    assert _attend(x=2 * A + 4 * WIDTH) in NO_DEVICE
+    assert _attend(num_pages=8, block_table_stride=1 << 20, x=2 * A + 4 * 8) in NO_DEVICE
