@@ -418,7 +418,6 @@ __device__ __forceinline__ bool choose_few(SelectShared& s, const uint32_t* keys
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) lo = min(lo, s.lo[w]), hi = max(hi, s.hi[w]);
-  if (lo == 0 && tid == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
   const int drop = max(32 - __clz(hi - lo) - kFewBinsLog, 0);
 #pragma unroll
   for (int u = 0; u < kFewEach; ++u)
@@ -531,7 +530,6 @@ __device__ __forceinline__ void choose_by_bins(const Kv4SelectParams& p, SelectS
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kSelectWarps; ++w) lo = min(lo, s.lo[w]), hi = max(hi, s.hi[w]);
-  if (lo == 0 && tid == 0) atomicOr(&g_device_status, kDevStatusBadIndex);
   // Keys from `lo` to `hi`, `open` bits of them undecided: the place that holds
   // the last one taken, until all in it are taken or all in it are equal.
   int open = 32 - __clz(hi - lo), above = 0, in = count;
@@ -716,6 +714,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     auto put_keys = [&]() {
       if (sums_of != kNoPage) {
         const uint32_t key = key_of_sums(sums, sums_exps);
+        if (key == 0u) atomicOr(&g_device_status, kDevStatusBadIndex);  // (also where nothing is left to choose)
         const int n = sums_of & ((1u << kTokenAt) - 1u), t = sums_of >> kTokenAt;
         if (!held)
           p.keys[(m0 + t) * p.width + p.first + n] = key;

@@ -251,7 +251,8 @@ int mlaqp_kv4_select(const void* q, int64_t q_token_stride, int q_dtype, const v
                          span(workspace, static_cast<uint64_t>(workspace_bytes))};
   const Range ins[5] = {span(q, eb * ((M - 1) * static_cast<uint64_t>(q_token_stride) + 576ull * H)),
                         digest_span(digests, digest_stride, num_pages),
-                        table_span(block_table, block_table_stride, num_seqs, num_pages), span(seq_lens, 4ull * num_seqs), span(seqs, seqs ? 4ull * B : 0)};
+                        table_span(block_table, block_table_stride, num_seqs, num_pages), span(seq_lens, 4ull * num_seqs),
+                        span(seqs, seqs ? 4ull * B : 0)};
   for (int i = 0; i < 3; ++i) {
     for (const Range& r : ins)
       if (overlaps(outs[i], r)) return bad_arg("sel_table, sel_lens or workspace overlaps an input");

@@ -3,8 +3,9 @@ the CPU oracle.  Digests, tables and lengths are whole numbers and equal."""
 
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_kv4_select import Digests, _rand_cache
+from test_gpu_kv4_select import BAD_INDEX, Digests, Select, _query, _rand_cache, _rand_digests
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,25 @@ def test_pages_of_many_sequences(cuda_device, P):
     d = Digests(c, P, np.tile(np.arange(pages), (20, 1)), [pages * P] * 20)
     d.run(range(20), [pages * P] * 20, pages * P)
     d.check(range(pages))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_len,k,first,last", [(1, 3, 1, 2), (4, 6, 2, 4), (1, 40, 20, 20), (3, 5, 1, 2)])
+@pytest.mark.parametrize("pages", [60, 3000])
+def test_pages_out_of_range_are_reported_whether_or_not_there_is_a_choice(cuda_device, pages, q_len, k, first, last, e4m3):
+    """Also where the first and the last pages are all that is taken."""
+    rng = np.random.default_rng(pages + k)
+    q_dev, q = _query(rng, 2 * q_len, 8, e4m3)
+    table = np.stack([rng.permutation(pages) for _ in range(2)])
+    s = Select(_rand_digests(rng, pages), 16, table, [pages * 16, pages * 16 - 5], q_dev, q, e4m3)
+    s.run(2, q_len, k, first, last)
+    for row, at, bad in ((0, first, -1), (1, pages - last - 1, pages), (1, pages // 2, 2 ** 31 - 1)):
+        s.table[:] = table
+        s.table[row, at] = bad
+        s.t.copy_(torch.from_numpy(s.table))
+        s.run(2, q_len, k, first, last, status=BAD_INDEX)
+    # pages that are taken anyway are the attention's to report
+    s.table[:] = table
+    s.table[0, 0], s.table[1, -1] = -1, pages
+    s.t.copy_(torch.from_numpy(s.table))
+    s.run(2, q_len, k, first, last)
