@@ -665,14 +665,19 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     // Batch k of this warp is four entries, its lane u + 4 (k % 8) seeing to entry
     // u: addresses and exponents of eight batches at a time.  In the place of a
     // page out of the pool, and behind the last one, page 0's digest is read and
-    // not used.
+    // not used.  A page out of the pool is reported here: also where there is nothing
+    // to choose.
     const int warps = kSelectWarps * ctas, mine = ctas * warp + rank;  // a last, incomplete round is shared by all CTAs
     const int batches = ((count + kScorePages - 1) / kScorePages - mine + warps - 1) / warps;
+    auto in_pool = [&](int page) { return page >= 0 && page < p.num_pages; };
+    bool lost = false;  // any of this lane's entries
     auto entry = [&](int k0) {
       const int n = kScorePages * (warps * (k0 + lane / kScorePages) + mine) + lane % kScorePages;
-      return n < count ? between[n] : -1;
+      if (n >= count) return -1;
+      const int page = between[n];
+      lost |= !in_pool(page);
+      return page;
     };
-    auto in_pool = [&](int page) { return page >= 0 && page < p.num_pages; };
     auto digest_of = [&](int page) { return p.digests + (in_pool(page) ? page : 0) * p.digest_stride; };
     auto exps_of = [&](int page, const uint8_t* digest) {
       const int e = static_cast<int>(ld_u32(digest + 2 * kOutDim) & 0xFFFFu);
@@ -714,7 +719,6 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
     auto put_keys = [&]() {
       if (sums_of != kNoPage) {
         const uint32_t key = key_of_sums(sums, sums_exps);
-        if (key == 0u) atomicOr(&g_device_status, kDevStatusBadIndex);  // (also where nothing is left to choose)
         const int n = sums_of & ((1u << kTokenAt) - 1u), t = sums_of >> kTokenAt;
         if (!held)
           p.keys[(m0 + t) * p.width + p.first + n] = key;
@@ -753,6 +757,7 @@ __global__ void __launch_bounds__(kSelectThreads, kSelectCtasPerSm)
       if (k + 1 < batches) round(odd, even, k + 1);
     }
     put_keys();
+    if (lost) atomicOr(&g_device_status, kDevStatusBadIndex);
     copy_wait();
     if (ctas > 1) cluster_arrive();
   }
