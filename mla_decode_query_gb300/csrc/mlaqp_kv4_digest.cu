@@ -21,12 +21,12 @@
 // cache's own calls do not write but for magnitudes below 2^-39), the page is done
 // in BF16.
 //
-// What bounds it.  1024 pages of 64 tokens: 9.2 us, 27 MB at 3.0 TB/s (6000 of them
-// 40 us, 4.0 TB/s): the ALU, some 40 instructions a token and warp, 16 of them maxima
-// and minima, which an SM issues two of a cycle.  64 candidates of which some fill a
-// page of 16: 2.9 us, the chain lists -> lengths -> table -> scales, codes -> join.
-// With a warp 64 latents of all tokens instead of all of some, and the maxima joined
-// within warps: 12.5 and 3.2 us.  A warp a page: 10.6 and 3.1.
+// What bounds it.  1024 pages of 64 tokens: 9.4 us with other pages in every call, 27
+// MB at 2.9 TB/s (6000 of them 40 us, 4.0 TB/s): the ALU, some 40 instructions a token
+// and warp, 16 of them maxima and minima, which an SM issues two of a cycle.  64
+// candidates of which some fill a page of 16: 2.9 us, the chain lists -> lengths ->
+// table -> scales, codes -> join.  With a warp 64 latents of all tokens instead of all
+// of some, and the maxima joined within warps: 12.5 and 3.2 us.
 
 #include <algorithm>
 
@@ -356,8 +356,12 @@ const void* digest_kernel(int warps) {
 
 }  // namespace
 
-// Four warps a page while all CTAs find room at once, two beyond (64 tokens a page,
-// 100 pages: 3.8 us, 4.1 with two; 600: 5.9, 6.7; 1024: 9.8, 8.5; 6000: 45, 40).
+// Four warps a page while all CTAs find room at once, two beyond.  Pages of 64 tokens,
+// others in every call, with four, two and one: 100 of them 3.6, 4.1, 5.7 us; 600: 5.8,
+// 6.6, 7.8; 1024: 10.9, 9.7, 13.7; 2048: 18.3, 17.9, 16.5; 6000: 45.6, 39.9, 41.4.
+// Rounds of CTAs make the steps: for 2048 a warp a page is one round less.  A candidate
+// that fills no page costs a lane its lookup: 64 sequences of a page each 1.5 us, with
+// room for 131072 new tokens in pages of 16 (524288 candidates) 5.7.
 cudaError_t kv4_digest(const Kv4DigestParams& params, int sm_count, cudaStream_t stream) {
   Kv4DigestParams p = params;
   void* args[1] = {&p};

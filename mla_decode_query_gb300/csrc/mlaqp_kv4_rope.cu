@@ -8,19 +8,22 @@
 // summed in two floats (a square of a BF16 is exact in FP32, and two-sum keeps
 // what an addition rounds off), so r is the number that an exact sum would
 // give but for ties to 2^-45: codes at a border do not depend on the order of
-// a reduction.  That costs 7 operations a latent, hidden behind memory (4
-// operations, with a sum that begins at a power of two: 18.2 us instead of 18.5
-// below, but rows end at 2^63 instead of the end of FP32).
+// a reduction.  That costs 7 operations a latent (4 operations, with a sum that
+// begins at a power of two: 18.2 us instead of 18.5 below, but rows end at 2^63
+// instead of the end of FP32; no norm at all: 16.1).
 //
 // Rotation: pair (a, b) -> (a cos - b sin, b cos + a sin).  A lane keeps the
 // angles of its pairs for all heads: of four pairs in one 16-byte chunk
 // (interleaved), or of eight pairs in chunks c and c + 4 (halves).
 //
-// What bounds it.  16385 tokens with 16 heads: 18.5 us, memory (122 MB at 6.6
-// TB/s, 97% of a copy's rate; 0.67 instructions issued a cycle).  1027 tokens with
-// 11 heads 2.6 us, 64 tokens 2.4: the chain launch -> position, slot -> angles
-// -> stores.  Four tokens a CTA: eight or sixteen took 19.3 and 21.3 us, and 64
-// tokens 2.7.
+// What bounds it.  16385 tokens with 16 heads: 18.5 us (halves 19.0), 97 MB at 5.2
+// TB/s, 77% of a copy's rate: memory, and a start and an end of some 4 us beside it
+// (3.4 rounds of CTAs; 65536 tokens take 59.2 us, 6.5 TB/s; 0.67 instructions issued
+// a cycle).  With 32 heads 32.0 us (halves 29.3) of 24.1 at a copy's rate, with 128
+// 116 (93.5) of 83.2: from head 17 on a lane has one head in flight, of which halves
+// are two chunks.  1027 tokens with 11 heads 2.5 us, 64 tokens 2.4: the chain launch
+// -> position, slot -> angles -> stores.  Four tokens a CTA: eight or sixteen took
+// 19.3 and 21.3 us, and 64 tokens 2.7.
 
 #include "mlaqp_dispatch.h"
 #include "mlaqp_kv4.cuh"

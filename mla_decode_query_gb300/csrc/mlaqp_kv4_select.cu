@@ -21,15 +21,22 @@
 // scans for itself, leaves a few keys to rank, and a prefix sum puts the pages in
 // order; more keys, or more of them in one place, take rounds of 2048 places.
 // One launch: a score kernel that cut all pages into equal stretches, with a
-// choice kernel behind it, took 21.7 us instead of 10.5.
+// choice kernel behind it, took 21.7 us instead of 10.1.
 //
 // What bounds it.  64 sequences of 16000 to 32768 tokens, pages of 64, H = 16:
-// 10.5 us, 28 MB of digests; 0.65 us pass until the lengths are there, 2.2 with
-// the queries, 2.8 to 3.5 in the scores, 1 waiting for the longest of the cluster
+// 10.1 us, 28 MB of digests; 0.65 us pass until the lengths are there, 2.2 with
+// the queries, 2.5 to 3.5 in the scores, 1 waiting for the longest of the cluster
 // and 1.9 in the choice.  On an SM four pages cost a query token some 70 cycles
-// (72 dp2a at two a cycle, 8 sums over the warp at half of one).  One sequence of
-// 1024 pages: 6.7 us; 16 of up to 569 with 4 query tokens: 11.5, of which the
-// longest sequence scores for 4.6.
+// (72 dp2a at two a cycle, 8 sums over the warp at half of one).  16 of up to 569
+// pages with 4 query tokens: 11.3, of which the longest sequence scores for 4.6.
+//
+// The cluster's size follows from the table's width and the batch, so the longest
+// sequence decides: 40 of 2000 tokens in pages of 64 take 5.8 us, with one of 131071
+// beside them, on four CTAs, 18.9.  One sequence of 1024 pages takes 6.7 us with 8
+// heads and digests of normalised latents; with 16 heads and random digests 8.9,
+// and so one of 2048 pages 11.3 (64 of them taken).  Longer ones leave shared memory:
+// their keys go through the workspace and one CTA reads them several times, 4096
+// pages 26 us, 8192 47, 40009 233 (128, 256, 256 taken).
 
 #include <atomic>
 
