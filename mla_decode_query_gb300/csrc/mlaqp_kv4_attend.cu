@@ -1160,15 +1160,22 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
   if (mine.slot < 0 || mine.pieces > min(static_cast<int>(gridDim.x) / kJoinCtasPerSm, kAttMaxCtas) - (mine.slot >> 1))
     mine.pieces = 0;
   j.group[tid] = mine;
-  // the row groups that more than one CTA worked on, in order
+  // the row groups that more than one CTA worked on, in order, and whether any of
+  // them has more pieces than a warp joins (a bit beside a warp's count: with
+  // __syncthreads_or 32 sequences of up to 8191 tokens took 27.6 us instead of 27.4,
+  // one of 131071 26.4 instead of 26.25)
   const bool split = mine.pieces > 1;
   const unsigned who = __ballot_sync(0xffffffffu, split);
-  if (lane == 0) j.split_warp[warp] = __popc(who);
-  const bool many = __syncthreads_or(mine.pieces > kJoinFew);
+  const bool warp_many = __any_sync(0xffffffffu, mine.pieces > kJoinFew);
+  if (lane == 0) j.split_warp[warp] = __popc(who) | (warp_many ? 64 : 0);
+  __syncthreads();
   int rank = __popc(who & ((1u << lane) - 1u)), n_split = 0;
+  bool many = false;
   for (int w = 0; w < 8; ++w) {
-    if (w < warp) rank += j.split_warp[w];
-    n_split += j.split_warp[w];
+    const int n = j.split_warp[w] & 63;
+    if (w < warp) rank += n;
+    n_split += n;
+    many |= j.split_warp[w] >= 64;
   }
   if (split) j.split[rank] = tid;
   __syncthreads();
